@@ -11,6 +11,8 @@
  *                      it runs (Block docstring on the same page)
  *   hc_post_mixes_pre  hc_post of one sublayer fused with hc_mixes_pre of the
  *                      next (same docstring)
+ *   hc_checkpoint and the entry points after it: the stream kept in 8 bits for
+ *                      the backward pass, and the gradients of the above
  *
  * Conventions shared by every entry point
  *   - Every tensor pointer is a DEVICE pointer owned by the caller.  The
@@ -26,10 +28,11 @@
  *     layouts stated per function.
  *   - Arguments are validated on the host before anything is enqueued; a
  *     call that returns an error has launched nothing.  n == 0 is a valid
- *     no-op.  Supported: hc in {4, 8}; d > 0 with d % 8 == 0; every pointer
+ *     no-op (gradients that sum over tokens are then set to zero).  Supported: hc in {4, 8}; d > 0 with d % 8 == 0; every pointer
  *     16-byte aligned; iters >= 1; eps >= 0; norm_eps >= 0.
  *   - Outputs must not overlap inputs or each other, except that hc_post may
- *     write y over residual exactly (y == residual).
+ *     write y over residual exactly (y == residual), and where an entry point
+ *     states another such pair.
  *   - The library never aborts, exits or traps.  CUDA launch failures are
  *     returned as HC_ERR_CUDA.  Kernels with bounded internal waits record a
  *     timeout in a per-device error word that hc_device_error() reads.
@@ -37,7 +40,7 @@
  *     decode kernel (hc = 4, d % 256 == 0, d <= 5120, up to 16 tokens per
  *     16-CTA cluster the device co-schedules: 112 on GB300; it serves
  *     hc_mixes, hc_mixes_pre, hc_mixes_pre_norm and hc_post_mixes_pre on
- *     those shapes) and the hc_post kernel are launched with programmatic
+ *     those shapes), the hc_post kernel and the training kernels are launched with programmatic
  *     dependent launch, so they may start while the kernel enqueued just
  *     before them in the stream is still running.  They read every
  *     activation only after that kernel has completed, but the decode kernel
@@ -62,7 +65,8 @@ typedef enum hc_status {
     HC_OK = 0,
     HC_ERR_INVALID_ARG = 1,  /* null pointer, negative size, bad iters/eps,
                                 overlapping buffers, workspace too small */
-    HC_ERR_UNSUPPORTED = 2,  /* hc not in {4, 8}, sizes beyond int64 range */
+    HC_ERR_UNSUPPORTED = 2,  /* hc not in {4, 8}, sizes beyond int64 range, iters
+                                above an entry point's limit */
     HC_ERR_MISALIGNED = 3,   /* d % 8 != 0 or a pointer not 16-byte aligned */
     HC_ERR_CUDA = 4          /* a CUDA runtime call or launch failed */
 } hc_status;
@@ -295,6 +299,111 @@ hc_status hc_mixes_pre_noalloc(int64_t n, int hc, int64_t d, int iters, float ep
                                float norm_eps, const uint16_t *x, const float *w_mix,
                                const float *hc_scale, const float *hc_base, float *pre,
                                float *post, float *comb, uint16_t *y, hc_stream_t stream);
+
+/*
+ * Training: streams kept in 8 bits, and gradients
+ *
+ * The pages show the forward pass only; these entry points follow from its
+ * formulas.  A training step keeps one stream [n, hc, d] per sublayer boundary
+ * for the backward pass.  A "kept" tensor is that stream (or a sublayer output
+ * [n, d]) as bf16, or in 8 bits: rows of d channels in blocks of 32 (the last
+ * block of a row may be shorter), an e4m3 code per channel in codes [rows, d]
+ * and one byte per block in scales [rows, ceil(d / 32)].  A channel's value is
+ * code * 2^(byte - 127).  With E and M the biased exponent and the mantissa (in
+ * [1, 2)) of the block's largest finite magnitude, byte = max(1, E - 8 +
+ * (M > 1.75)): that magnitude over the scale then lies above 224 and at most
+ * at 448, the largest code (below for magnitudes under 2^-118).  Nothing
+ * saturates, and the one rounding is that of value / 2^(byte - 127) to e4m3, to
+ * nearest even; magnitudes that would round to 2^128, which bf16 lacks, become
+ * the code 240 below it.  NaN and the infinities become the code 0x7F (NaN) and
+ * leave the block's other channels as they would be without them.  Bytes from
+ * elsewhere are taken as they are in 1..254; 0 reads as a scale of 0.
+ *
+ * hc_checkpoint      x [rows, d] bf16 (in) -> codes, scales (out)
+ * hc_restore         codes, scales (in) -> x [rows, d] bf16 (out); exact: every
+ *                    value that hc_checkpoint leaves is a bf16 number
+ * Their shapes: rows >= 0 (0 is a no-op), d > 0 with d % 8 == 0.
+ */
+hc_status hc_checkpoint(int64_t rows, int64_t d, const uint16_t *x, uint8_t *codes,
+                        uint8_t *scales, hc_stream_t stream);
+hc_status hc_restore(int64_t rows, int64_t d, const uint8_t *codes, const uint8_t *scales,
+                     uint16_t *x, hc_stream_t stream);
+
+/*
+ * hc_pre_restore -- hc_pre of a kept stream: the sublayer input from which a
+ * recomputed sublayer starts, without the stream in between.
+ *   codes, scales: rows = n * hc (in);  pre [n, hc] float (in);
+ *   y [n, d] bf16 (out)
+ */
+hc_status hc_pre_restore(int64_t n, int hc, int64_t d, const uint8_t *codes,
+                         const uint8_t *scales, const float *pre, uint16_t *y,
+                         hc_stream_t stream);
+
+/*
+ * hc_post_checkpoint -- hc_post that also keeps the new stream: y is that of
+ * hc_post bit for bit, codes and scales are those of hc_checkpoint(y) with
+ * rows = n * hc.  y == residual (in place) is allowed.
+ */
+hc_status hc_post_checkpoint(int64_t n, int hc, int64_t d, const uint16_t *out,
+                             const uint16_t *residual, const float *post, const float *comb,
+                             uint16_t *y, uint8_t *codes, uint8_t *scales, hc_stream_t stream);
+
+/*
+ * hc_post_backward -- gradients of hc_post from dy, the gradient of its y:
+ *   dout_{t,c}      = sum_k post_{t,k} dy_{t,k,c}
+ *   dpost_{t,k}     = sum_c out_{t,c} dy_{t,k,c}
+ *   dcomb_{t,j,k}   = sum_c residual_{t,j,c} dy_{t,k,c}
+ *   dresidual_{t,j,c} = sum_k comb_{t,j,k} dy_{t,k,c}
+ *   dy [n, hc, d] bf16 (in)
+ *   out [n, d], residual [n, hc, d] (in): bf16 with scales NULL, or codes with
+ *   out_scales / residual_scales, each on its own
+ *   post [n, hc], comb [n, hc, hc] float (in)
+ *   dout [n, d] bf16, dpost [n, hc], dcomb [n, hc, hc] float (out)
+ *   dresidual [n, hc, d] bf16 (out, may be NULL, may be dy itself).  A caller
+ *   that hands dy on to hc_mixes_pre_backward as dstream does not need it.
+ * Sums run in binary32.
+ */
+hc_status hc_post_backward(int64_t n, int hc, int64_t d, const uint16_t *dy, const void *out,
+                           const uint8_t *out_scales, const void *residual,
+                           const uint8_t *residual_scales, const float *post, const float *comb,
+                           uint16_t *dout, float *dpost, float *dcomb, uint16_t *dresidual,
+                           hc_stream_t stream);
+
+/*
+ * hc_mixes_pre_backward -- gradients of hc_mixes_pre, and of the stream x that
+ * hc_post carries past the same sublayer.  With r, m (= mixes), z = m * scale +
+ * base, pre, post and comb as in hc_mixes and hc_split_sinkhorn, the loss
+ * depends on x through y (gradient dy), post (dpost), comb (dcomb) and, with
+ * dstream not NULL, through sum_j comb_{t,j,k} x_{t,j,c} (gradient dstream, the
+ * dy of hc_post_backward):
+ *   dpre_j = sum_c dy_c x_{j,c};  dz: the split's gradient;  dm = dz * scale
+ *   dx_{j,c} = pre_j dy_c + sum_i r dm_i w_{i,(j,c)}
+ *              - (r^2 / F) (sum_i dm_i m_i) x_{j,c} + sum_k comb_{j,k} dstream_{k,c}
+ *   dw_{i,f} = sum_t r dm_i x_f;  dscale_g = sum_t sum_{i in g} dz_i m_i;
+ *   dbase_i = sum_t dz_i
+ *   dy [n, d] bf16 (in);  x [n, hc, d] (in): bf16 with x_scales NULL, or codes
+ *   mixes [n, mix_hc] float (in): what the forward call returned.  pre and comb
+ *   are formed from it again, with the same iters and eps.  r is that of x as
+ *   kept.
+ *   w_mix, hc_scale, hc_base as in hc_mixes_pre (in)
+ *   dpost [n, hc], dcomb [n, hc, hc] float (in)
+ *   dstream [n, hc, d] bf16 (in, may be NULL)
+ *   dx [n, hc, d] bf16 (out; may be dstream itself)
+ *   dw_mix [mix_hc, hc*d], dscale [3], dbase [mix_hc] float (out): sums over
+ *   this call's tokens, written and not added to; zeros for n == 0
+ *   workspace: hc_mixes_pre_backward_bytes(n, hc, d) bytes, 256-byte aligned,
+ *   not shared with another call in flight; its contents need not be kept.
+ * iters <= 256 (else HC_ERR_UNSUPPORTED).  The sums run in a fixed order: the
+ * same call gives the same bits.
+ */
+size_t hc_mixes_pre_backward_bytes(int64_t n, int hc, int64_t d);
+hc_status hc_mixes_pre_backward(int64_t n, int hc, int64_t d, int iters, float eps, float norm_eps,
+                                const uint16_t *dy, const void *x, const uint8_t *x_scales,
+                                const float *mixes, const float *w_mix, const float *hc_scale,
+                                const float *hc_base, const float *dpost, const float *dcomb,
+                                const uint16_t *dstream, uint16_t *dx, float *dw_mix,
+                                float *dscale, float *dbase, void *workspace,
+                                size_t workspace_bytes, hc_stream_t stream);
 
 /* Number of kernels this library has enqueued in this process (all devices,
  * all threads) since it was loaded.  Host-only counter for diagnostics. */

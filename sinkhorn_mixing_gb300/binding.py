@@ -55,6 +55,15 @@ def lib():
                                         P, P, P, P, ctypes.c_size_t, P]
         L.hc_post_mixes_pre.argtypes = [i64, i32, i64, P, P, P, P, P, i32, f32, f32, P, P, P, P,
                                         P, P, P, P, P, ctypes.c_size_t, P]
+        L.hc_checkpoint.argtypes = [i64, i64, P, P, P, P]
+        L.hc_restore.argtypes = [i64, i64, P, P, P, P]
+        L.hc_pre_restore.argtypes = [i64, i32, i64, P, P, P, P, P]
+        L.hc_post_checkpoint.argtypes = [i64, i32, i64, P, P, P, P, P, P, P, P]
+        L.hc_post_backward.argtypes = [i64, i32, i64, P, P, P, P, P, P, P, P, P, P, P, P]
+        L.hc_mixes_pre_backward.argtypes = [i64, i32, i64, i32, f32, f32, P, P, P, P, P, P, P, P,
+                                            P, P, P, P, P, P, P, ctypes.c_size_t, P]
+        L.hc_mixes_pre_backward_bytes.argtypes = [i64, i32, i64]
+        L.hc_mixes_pre_backward_bytes.restype = ctypes.c_size_t
         L.hc_workspace_bytes.argtypes = [i64, i32, i64]
         L.hc_workspace_bytes.restype = ctypes.c_size_t
         L.hc_device_error.argtypes = [ctypes.POINTER(ctypes.c_uint), i32]
@@ -62,7 +71,9 @@ def lib():
         L.hc_selftest_wait_timeout.argtypes = [ctypes.c_uint64, P]
         L.hc_selftest_wait_timeout.restype = i32
         for f in ("hc_mixes", "hc_split_sinkhorn", "hc_pre", "hc_post", "hc_mixes_pre",
-                  "hc_mixes_pre_norm", "hc_post_mixes_pre", "hc_device_error"):
+                  "hc_mixes_pre_norm", "hc_post_mixes_pre", "hc_device_error", "hc_checkpoint",
+                  "hc_restore", "hc_pre_restore", "hc_post_checkpoint", "hc_post_backward",
+                  "hc_mixes_pre_backward"):
             getattr(L, f).restype = i32
         _lib = L
     return _lib
@@ -336,6 +347,187 @@ def hc_post_mixes_pre(out, residual, post, comb, w_mix, hc_scale, hc_base,
                  _ptr(post_next), _ptr(comb_next), _ptr(y), _ptr(workspace), wbytes,
                  _stream(dev, stream)), "hc_post_mixes_pre")
     return x_next, y, pre, post_next, comb_next, mixes
+
+
+KEPT_BLOCK = 32  # channels that share a scale byte (hcmix.h, hc_checkpoint)
+
+
+def _sized(t, name, count, dtype, dev):
+    _need(t, name, dtype, dev)
+    if t.numel() != count:
+        raise ValueError("%s must hold %d values, got %d" % (name, count, t.numel()))
+    return t
+
+
+def _grad_out(t, name, shape, dtype, dev, stream):
+    """_out; a tensor made here for a stream other than the current one is not
+    handed out again by the allocator before that stream is done with it."""
+    made = t is None
+    t = _out(t, name, shape, dtype, dev)
+    if made and stream is not None:
+        t.record_stream(stream)
+    return t
+
+
+def _scale_shape(shape):
+    return tuple(shape[:-1]) + (-(-int(shape[-1]) // KEPT_BLOCK),)
+
+
+def _kept(t, name, shape, dev):
+    """A kept tensor of `shape`: bf16, or (codes, scales).  Returns the data
+    and the scales or None."""
+    if isinstance(t, torch.Tensor):
+        _need(t, name, torch.bfloat16, dev)
+        if tuple(t.shape) != tuple(shape):
+            raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+        return t, None
+    if not isinstance(t, (tuple, list)) or len(t) != 2:
+        raise TypeError("%s must be a bf16 tensor or (codes, scales)" % name)
+    codes, scales = t
+    for x, what, dtype, want in ((codes, "codes", torch.float8_e4m3fn, tuple(shape)),
+                                 (scales, "scales", torch.uint8, _scale_shape(shape))):
+        _need(x, "%s %s" % (name, what), dtype, dev)
+        if tuple(x.shape) != want:
+            raise ValueError("%s %s must have shape %s, got %s" % (name, what, want,
+                                                                   tuple(x.shape)))
+    return codes, scales
+
+
+def _rows(t):
+    if t.dim() < 1:
+        raise ValueError("a row of channels at least is needed")
+    d = int(t.shape[-1])
+    n = 1
+    for s in t.shape[:-1]:
+        n *= int(s)
+    return n, d
+
+
+def hc_checkpoint(x, codes=None, scales=None, stream=None):
+    """x [..., d] bf16 -> codes [..., d] float8_e4m3fn, scales [..., ceil(d / 32)]
+    uint8: a channel's value is code * 2^(scale - 127)."""
+    _need(x, "x", torch.bfloat16)
+    dev = x.device
+    n, d = _rows(x)
+    codes = _grad_out(codes, "codes", tuple(x.shape), torch.float8_e4m3fn, dev, stream)
+    scales = _grad_out(scales, "scales", _scale_shape(x.shape), torch.uint8, dev, stream)
+    _check(_call(dev, lib().hc_checkpoint, n, d, _ptr(x), _ptr(codes), _ptr(scales),
+                 _stream(dev, stream)), "hc_checkpoint")
+    return codes, scales
+
+
+def hc_restore(codes, scales, x=None, stream=None):
+    """codes [..., d], scales [..., ceil(d / 32)] of hc_checkpoint -> x [..., d] bf16."""
+    _need(codes, "codes", torch.float8_e4m3fn)
+    dev = codes.device
+    n, d = _rows(codes)
+    _kept((codes, scales), "x", tuple(codes.shape), dev)
+    x = _grad_out(x, "x", tuple(codes.shape), torch.bfloat16, dev, stream)
+    _check(_call(dev, lib().hc_restore, n, d, _ptr(codes), _ptr(scales), _ptr(x),
+                 _stream(dev, stream)), "hc_restore")
+    return x
+
+
+def hc_pre_restore(codes, scales, pre, y=None, stream=None):
+    """hc_pre of a kept stream: codes [..., hc, d], scales, pre [..., hc] -> y [..., d] bf16."""
+    _need(codes, "codes", torch.float8_e4m3fn)
+    dev = codes.device
+    lead, n, hc, d = _stream_dims(codes)
+    _kept((codes, scales), "x", tuple(codes.shape), dev)
+    _sized(pre, "pre", n * hc, torch.float32, dev)
+    y = _grad_out(y, "y", lead + (d,), torch.bfloat16, dev, stream)
+    _check(_call(dev, lib().hc_pre_restore, n, hc, d, _ptr(codes), _ptr(scales), _ptr(pre),
+                 _ptr(y), _stream(dev, stream)), "hc_pre_restore")
+    return y
+
+
+def hc_post_checkpoint(out, residual, post, comb, y=None, codes=None, scales=None, stream=None):
+    """hc_post that also keeps the new stream in 8 bits (y may be residual itself).
+    Returns (y, codes, scales)."""
+    _need(residual, "residual", torch.bfloat16)
+    dev = residual.device
+    lead, n, hc, d = _stream_dims(residual)
+    _sized(out, "out", n * d, torch.bfloat16, dev)
+    _sized(post, "post", n * hc, torch.float32, dev)
+    _sized(comb, "comb", n * hc * hc, torch.float32, dev)
+    shape = lead + (hc, d)
+    y = _grad_out(y, "y", shape, torch.bfloat16, dev, stream)
+    codes = _grad_out(codes, "codes", shape, torch.float8_e4m3fn, dev, stream)
+    scales = _grad_out(scales, "scales", _scale_shape(shape), torch.uint8, dev, stream)
+    _check(_call(dev, lib().hc_post_checkpoint, n, hc, d, _ptr(out), _ptr(residual), _ptr(post),
+                 _ptr(comb), _ptr(y), _ptr(codes), _ptr(scales), _stream(dev, stream)),
+           "hc_post_checkpoint")
+    return y, codes, scales
+
+
+def hc_post_backward(dy, out, residual, post, comb, want_dresidual: bool = False, dout=None,
+                     dpost=None, dcomb=None, dresidual=None, stream=None):
+    """Gradients of hc_post from dy [..., hc, d] bf16.  out [..., d] and residual
+    [..., hc, d] are bf16 tensors or (codes, scales) of hc_checkpoint.
+    Returns (dout, dpost, dcomb, dresidual-or-None); dresidual may be dy itself."""
+    _need(dy, "dy", torch.bfloat16)
+    dev = dy.device
+    lead, n, hc, d = _stream_dims(dy)
+    od, osc = _kept(out, "out", lead + (d,), dev)
+    rd, rsc = _kept(residual, "residual", lead + (hc, d), dev)
+    _sized(post, "post", n * hc, torch.float32, dev)
+    _sized(comb, "comb", n * hc * hc, torch.float32, dev)
+    dout = _grad_out(dout, "dout", lead + (d,), torch.bfloat16, dev, stream)
+    dpost = _grad_out(dpost, "dpost", lead + (hc,), torch.float32, dev, stream)
+    dcomb = _grad_out(dcomb, "dcomb", lead + (hc, hc), torch.float32, dev, stream)
+    if want_dresidual or dresidual is not None:
+        dresidual = _grad_out(dresidual, "dresidual", lead + (hc, d), torch.bfloat16, dev, stream)
+    _check(_call(dev, lib().hc_post_backward, n, hc, d, _ptr(dy), _ptr(od), _ptr(osc), _ptr(rd),
+                 _ptr(rsc), _ptr(post), _ptr(comb), _ptr(dout), _ptr(dpost), _ptr(dcomb),
+                 _ptr(dresidual), _stream(dev, stream)), "hc_post_backward")
+    return dout, dpost, dcomb, dresidual
+
+
+@functools.lru_cache(maxsize=256)
+def hc_mixes_pre_backward_bytes(n: int, hc: int, d: int) -> int:
+    return int(lib().hc_mixes_pre_backward_bytes(int(n), int(hc), int(d)))
+
+
+def hc_mixes_pre_backward(dy, x, mixes, w_mix, hc_scale, hc_base, dpost, dcomb, dstream=None,
+                          sinkhorn_iters: int = 20, eps: float = 1e-6, norm_eps: float = 1e-20,
+                          dx=None, dw_mix=None, dscale=None, dbase=None, workspace=None,
+                          stream=None):
+    """Gradients of hc_mixes_pre from dy [..., d] bf16, dpost [..., hc] and dcomb
+    [..., hc, hc]; with dstream [..., hc, d] (the dy of hc_post_backward) also of the
+    stream that hc_post carried past the sublayer.  x [..., hc, d] is a bf16 tensor or
+    (codes, scales); mixes is what hc_mixes_pre returned.
+    Returns (dx, dw_mix, dscale, dbase); dx may be dstream itself."""
+    _need(dy, "dy", torch.bfloat16)
+    dev = dy.device
+    data = x if isinstance(x, torch.Tensor) else x[0] if isinstance(x, (tuple, list)) and x else x
+    if not isinstance(data, torch.Tensor):
+        raise TypeError("x must be a bf16 tensor or (codes, scales)")
+    lead, n, hc, d = _stream_dims(data)
+    xd, xsc = _kept(x, "x", lead + (hc, d), dev)
+    mix = (2 + hc) * hc
+    if tuple(dy.shape) != lead + (d,):
+        raise ValueError("dy must have shape %s, got %s" % (lead + (d,), tuple(dy.shape)))
+    _sized(mixes, "mixes", n * mix, torch.float32, dev)
+    _sized(w_mix, "w_mix", mix * hc * d, torch.float32, dev)
+    _sized(hc_scale, "hc_scale", 3, torch.float32, dev)
+    _sized(hc_base, "hc_base", mix, torch.float32, dev)
+    _sized(dpost, "dpost", n * hc, torch.float32, dev)
+    _sized(dcomb, "dcomb", n * hc * hc, torch.float32, dev)
+    if dstream is not None:
+        _sized(dstream, "dstream", n * hc * d, torch.bfloat16, dev)
+    dx = _grad_out(dx, "dx", lead + (hc, d), torch.bfloat16, dev, stream)
+    dw_mix = _grad_out(dw_mix, "dw_mix", (mix, hc * d), torch.float32, dev, stream)
+    dscale = _grad_out(dscale, "dscale", (3,), torch.float32, dev, stream)
+    dbase = _grad_out(dbase, "dbase", (mix,), torch.float32, dev, stream)
+    wbytes = hc_mixes_pre_backward_bytes(n, hc, d)
+    workspace = _grad_out(workspace, "workspace", (wbytes,), torch.uint8, dev, stream) \
+        if workspace is None else _need(workspace, "workspace", torch.uint8, dev)
+    _check(_call(dev, lib().hc_mixes_pre_backward, n, hc, d, int(sinkhorn_iters), float(eps),
+                 float(norm_eps), _ptr(dy), _ptr(xd), _ptr(xsc), _ptr(mixes), _ptr(w_mix),
+                 _ptr(hc_scale), _ptr(hc_base), _ptr(dpost), _ptr(dcomb), _ptr(dstream), _ptr(dx),
+                 _ptr(dw_mix), _ptr(dscale), _ptr(dbase), _ptr(workspace), workspace.numel(),
+                 _stream(dev, stream)), "hc_mixes_pre_backward")
+    return dx, dw_mix, dscale, dbase
 
 
 def hc_launch_count() -> int:

@@ -7,6 +7,7 @@
 #include <mutex>
 
 #include "../../include/hcmix.h"
+#include "hc_check.h"
 #include "hc_decode.h"
 #include "hc_fused.h"
 #include "hc_internal.h"
@@ -115,62 +116,7 @@ cudaError_t device_info(DeviceInfo *out) {
 
 }  // namespace hc
 
-namespace {
-
-bool al16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-struct Range {
-    uintptr_t lo, hi;
-};
-Range rng(const void *p, uint64_t bytes) {
-    const uintptr_t a = reinterpret_cast<uintptr_t>(p);
-    return Range{a, a + (uintptr_t)bytes};
-}
-bool overlap(const Range &a, const Range &b) {
-    return a.lo < b.hi && b.lo < a.hi && a.hi > a.lo && b.hi > b.lo;
-}
-
-bool finite_nonneg(float v) { return v >= 0.0f && v < INFINITY; }
-
-// Shape checks shared by the entry points that take d.
-hc_status check_shape(int64_t n, int hc, int64_t d) {
-    if (n < 0 || d <= 0) return HC_ERR_INVALID_ARG;
-    if (hc != 4 && hc != 8) return HC_ERR_UNSUPPORTED;
-    if (d % 8 != 0) return HC_ERR_MISALIGNED;
-    // keep every byte count well inside int64: n <= 2^40, d <= 2^24
-    if (n > (int64_t(1) << 40) || d > (int64_t(1) << 24)) return HC_ERR_UNSUPPORTED;
-    return HC_OK;
-}
-
-hc_status check_hc_n(int64_t n, int hc) {
-    if (n < 0) return HC_ERR_INVALID_ARG;
-    if (hc != 4 && hc != 8) return HC_ERR_UNSUPPORTED;
-    if (n > (int64_t(1) << 40)) return HC_ERR_UNSUPPORTED;
-    return HC_OK;
-}
-
-hc_status ptrs_ok(std::initializer_list<const void *> ps) {
-    for (const void *p : ps)
-        if (p == nullptr) return HC_ERR_INVALID_ARG;
-    for (const void *p : ps)
-        if (!al16(p)) return HC_ERR_MISALIGNED;
-    return HC_OK;
-}
-
-// Every output range must be disjoint from every other listed range.
-bool disjoint(std::initializer_list<Range> outs, std::initializer_list<Range> ins) {
-    for (auto a = outs.begin(); a != outs.end(); ++a) {
-        for (auto b = a + 1; b != outs.end(); ++b)
-            if (overlap(*a, *b)) return false;
-        for (const Range &b : ins)
-            if (overlap(*a, b)) return false;
-    }
-    return true;
-}
-
-hc_status from_cuda(cudaError_t e) { return e == cudaSuccess ? HC_OK : HC_ERR_CUDA; }
-
-}  // namespace
+using namespace hc::check;
 
 extern "C" {
 
@@ -180,7 +126,7 @@ const char *hc_status_string(hc_status s) {
         case HC_ERR_INVALID_ARG:
             return "HC_ERR_INVALID_ARG: null pointer, negative size, bad iters/eps, "
                    "overlapping buffers or workspace too small";
-        case HC_ERR_UNSUPPORTED: return "HC_ERR_UNSUPPORTED: hc must be 4 or 8; sizes too large";
+        case HC_ERR_UNSUPPORTED: return "HC_ERR_UNSUPPORTED: hc must be 4 or 8; sizes or iters too large";
         case HC_ERR_MISALIGNED:
             return "HC_ERR_MISALIGNED: d must be a multiple of 8 and pointers 16-byte aligned";
         case HC_ERR_CUDA: return "HC_ERR_CUDA: a CUDA runtime call or kernel launch failed";

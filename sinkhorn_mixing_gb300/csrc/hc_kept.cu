@@ -1,0 +1,298 @@
+// hc_kept.cu -- rows kept in 8 bits (hc_kept.cuh has the format): to them, back
+// from them, the expansion that keeps its result, and the collapse from kept
+// copies.
+//
+// All four are HBM streams: each input is read once and each output written
+// once.  A lane moves vectors of 8 channels, 16 bytes of bf16 or 8 of codes,
+// several in flight; the vectors of all rows are numbered through (Slots), so
+// that narrow rows fill the warps as wide ones do, and four neighbouring lanes
+// hold the 32 channels of a block: its largest magnitude takes two shuffles
+// and nothing leaves the registers.
+#include "hc_kept.cuh"
+
+namespace hc {
+namespace {
+
+// Slot i stands for vector i % per of row i / per; per is the row's vector
+// count rounded up to whole blocks (4), so a group of four lanes never spans
+// two rows, and a row's last slots may lie past its end.  At most 2^31 slots
+// a launch: larger tensors take several.
+struct Slots {
+    uint32_t count;       // rows * per
+    uint32_t per;         // slots per row
+    uint32_t nv;          // vectors per row (d / 8)
+    uint32_t mul, shift;  // i / per = (i * mul) >> (32 + shift), i < 2^31
+    __device__ __forceinline__ void at(uint32_t i, int64_t &row, uint32_t &v) const {
+        const uint32_t q = __umulhi(i, mul) >> shift;
+        row = q;
+        v = i - q * per;
+    }
+};
+
+// With l = ceil(log2 per) and mul = ceil(2^(31+l) / per) the product's error
+// is below 2^l * 2^31 / 2^(31+l) / per, so the quotient is exact for i < 2^31.
+Slots make_slots(int64_t rows, int64_t d) {
+    Slots s;
+    s.nv = (uint32_t)(d / 8);
+    s.per = (uint32_t)(kept_blocks(d) * 4);
+    s.count = (uint32_t)(rows * s.per);
+    int l = 2;
+    while ((int64_t(1) << l) < s.per) ++l;
+    s.mul = (uint32_t)(((uint64_t(1) << (31 + l)) + s.per - 1) / s.per);
+    s.shift = (uint32_t)(l - 1);
+    return s;
+}
+
+// Calls f(first row, rows) for pieces of at most 2^30 slots.
+template <typename Fn>
+cudaError_t by_pieces(int64_t rows, int64_t d, Fn f) {
+    const int64_t most = (int64_t(1) << 30) / (kept_blocks(d) * 4);
+    for (int64_t r = 0; r < rows; r += most) {
+        const cudaError_t e = f(r, rows - r < most ? rows - r : most);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+
+// ---------------------------------------------------------- k_checkpoint
+template <int U>
+__global__ void __launch_bounds__(256) k_checkpoint(Slots sl, int64_t nblk,
+                                                    const uint4 *__restrict__ x,
+                                                    uint2 *__restrict__ codes,
+                                                    uint8_t *__restrict__ scales) {
+    griddep_wait_then_release();
+    const uint32_t lane = threadIdx.x & 31;
+    const uint32_t step = gridDim.x * 256u * U;
+    for (uint32_t i0 = (blockIdx.x * 256u + (threadIdx.x & ~31u)) * U; i0 < sl.count; i0 += step) {
+        uint4 r[U];
+        int64_t row[U];
+        uint32_t v[U];
+#pragma unroll
+        for (int a = 0; a < U; ++a) {
+            sl.at(i0 + 32 * a + lane, row[a], v[a]);
+            if (i0 + 32 * a + lane >= sl.count) v[a] = sl.nv;
+            r[a] = v[a] < sl.nv ? ld_stream(x + row[a] * sl.nv + v[a]) : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int a = 0; a < U; ++a) {
+            uint32_t byte;
+            const uint2 c = kept_quantise(r[a], byte);
+            if (v[a] < sl.nv) {
+                __stcs(codes + row[a] * sl.nv + v[a], c);
+                if ((lane & 3) == 0) scales[row[a] * nblk + (v[a] >> 2)] = (uint8_t)byte;
+            }
+        }
+    }
+}
+
+// ------------------------------------------------------------- k_restore
+template <int U>
+__global__ void __launch_bounds__(256) k_restore(Slots sl, int64_t nblk, Kept k,
+                                                 uint4 *__restrict__ x) {
+    griddep_wait_then_release();
+    const uint32_t lane = threadIdx.x & 31;
+    const uint32_t step = gridDim.x * 256u * U;
+    for (uint32_t i0 = (blockIdx.x * 256u + (threadIdx.x & ~31u)) * U; i0 < sl.count; i0 += step) {
+        KeptVec<true> r[U];
+        int64_t row[U];
+        uint32_t v[U];
+#pragma unroll
+        for (int a = 0; a < U; ++a) {
+            sl.at(i0 + 32 * a + lane, row[a], v[a]);
+            if (i0 + 32 * a + lane >= sl.count) v[a] = sl.nv;
+            if (v[a] < sl.nv) r[a].load(k, row[a], sl.nv, nblk, v[a]);
+        }
+#pragma unroll
+        for (int a = 0; a < U; ++a) {
+            if (v[a] < sl.nv) {
+                float f[8];
+                r[a].values(f);
+                st_stream(x + row[a] * sl.nv + v[a], pack8(f));
+            }
+        }
+    }
+}
+
+// --------------------------------------------------------- k_pre_restore
+// y = sum_j pre_j x_j of kept copies, the copies in the order of hc_pre.
+template <int HC, int U>
+__global__ void __launch_bounds__(256) k_pre_restore(Slots sl, int64_t nblk, Kept k,
+                                                     const float *__restrict__ pre,
+                                                     uint4 *__restrict__ y) {
+    griddep_wait_then_release();
+    const uint32_t lane = threadIdx.x & 31;
+    const uint32_t step = gridDim.x * 256u * U;
+    for (uint32_t i0 = (blockIdx.x * 256u + (threadIdx.x & ~31u)) * U; i0 < sl.count; i0 += step) {
+        KeptVec<true> r[U][HC];
+        int64_t t[U];
+        uint32_t v[U];
+#pragma unroll
+        for (int a = 0; a < U; ++a) {
+            sl.at(i0 + 32 * a + lane, t[a], v[a]);
+            if (i0 + 32 * a + lane >= sl.count) v[a] = sl.nv;
+            if (v[a] < sl.nv) {
+#pragma unroll
+                for (int j = 0; j < HC; ++j) r[a][j].load(k, t[a] * HC + j, sl.nv, nblk, v[a]);
+            }
+        }
+#pragma unroll
+        for (int a = 0; a < U; ++a) {
+            if (v[a] < sl.nv) {
+                float acc[8], f[8];
+#pragma unroll
+                for (int q = 0; q < HC / 4; ++q) {
+                    const float4 p = __ldg(reinterpret_cast<const float4 *>(pre + t[a] * HC) + q);
+                    const float pj[4] = {p.x, p.y, p.z, p.w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        r[a][4 * q + j].values(f);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            acc[e] = q + j == 0 ? pj[0] * f[e] : fmaf(pj[j], f[e], acc[e]);
+                    }
+                }
+                st_stream(y + t[a] * sl.nv + v[a], pack8(acc));
+            }
+        }
+    }
+}
+
+// ------------------------------------------------------ k_post_checkpoint
+// hc_post whose bf16 result is quantised before it leaves the registers: the
+// new stream is not read back for its checkpoint.  The sums run in hc_post's
+// order, so y is hc_post's bit for bit.  residual may equal y: a lane loads
+// every copy of a vector before it stores any of them.  Coefficients are
+// loaded per vector, row by row of comb: they hit the first-level cache, and
+// only the accumulators stay in registers.
+template <int HC>
+__global__ void __launch_bounds__(256) k_post_checkpoint(Slots sl, int64_t nblk,
+                                                         const uint4 *__restrict__ out,
+                                                         const uint4 *res,
+                                                         const float *__restrict__ post,
+                                                         const float *__restrict__ comb, uint4 *y,
+                                                         uint2 *__restrict__ codes,
+                                                         uint8_t *__restrict__ scales) {
+    griddep_wait_then_release();
+    const uint32_t lane = threadIdx.x & 31;
+    const uint32_t step = gridDim.x * 256u;
+    for (uint32_t i0 = blockIdx.x * 256u + (threadIdx.x & ~31u); i0 < sl.count; i0 += step) {
+        int64_t t;
+        uint32_t v;
+        sl.at(i0 + lane, t, v);
+        const bool in = i0 + lane < sl.count && v < sl.nv;
+        uint4 o = make_uint4(0, 0, 0, 0), r[HC];
+        if (in) {
+            o = ld_stream(out + t * sl.nv + v);
+        } else {
+            t = 0, v = 0;  // a row that exists, for the coefficients
+        }
+#pragma unroll
+        for (int j = 0; j < HC; ++j)
+            r[j] = in ? ld_stream(res + (t * HC + j) * sl.nv + v) : make_uint4(0, 0, 0, 0);
+        float acc[HC][8], f[8];
+        unpack8(o, f);
+        auto load_row = [&](const float *p, float c[HC]) {
+#pragma unroll
+            for (int q = 0; q < HC / 4; ++q) {
+                const float4 w = __ldg(reinterpret_cast<const float4 *>(p) + q);
+                c[4 * q] = w.x, c[4 * q + 1] = w.y, c[4 * q + 2] = w.z, c[4 * q + 3] = w.w;
+            }
+        };
+        float c[HC];
+        load_row(post + t * HC, c);
+#pragma unroll
+        for (int k = 0; k < HC; ++k)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) acc[k][e] = c[k] * f[e];
+#pragma unroll
+        for (int j = 0; j < HC; ++j) {
+            unpack8(r[j], f);
+            load_row(comb + (t * HC + j) * HC, c);
+#pragma unroll
+            for (int k = 0; k < HC; ++k)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) acc[k][e] = fmaf(c[k], f[e], acc[k][e]);
+        }
+#pragma unroll
+        for (int k = 0; k < HC; ++k) {
+            const uint4 p = pack8(acc[k]);
+            uint32_t byte;
+            const uint2 c8 = kept_quantise(p, byte);
+            if (in) {
+                const int64_t row = t * HC + k;
+                st_stream(y + row * sl.nv + v, p);
+                __stcs(codes + row * sl.nv + v, c8);
+                if ((lane & 3) == 0) scales[row * nblk + (v >> 2)] = (uint8_t)byte;
+            }
+        }
+    }
+}
+
+dim3 stream_grid(const Slots &sl, int u, int sms, int blocks_per_sm) {
+    const int64_t per_block = 256 * u;
+    const int64_t want = (sl.count + per_block - 1) / per_block;
+    const int64_t cap = (int64_t)sms * blocks_per_sm;
+    return dim3((unsigned)(want < cap ? want : cap));
+}
+
+Kept rows_from(const Kept &k, int64_t row, int64_t d) {
+    return Kept{static_cast<const uint8_t *>(k.data) + row * d, k.scales + row * kept_blocks(d)};
+}
+
+}  // namespace
+
+cudaError_t launch_checkpoint(int64_t rows, int64_t d, const uint16_t *x, uint8_t *codes,
+                              uint8_t *scales, const DeviceInfo &di, cudaStream_t s) {
+    const int64_t nblk = kept_blocks(d);
+    return by_pieces(rows, d, [&](int64_t r0, int64_t nr) {
+        const Slots sl = make_slots(nr, d);
+        return launch_overlapped(k_checkpoint<4>, stream_grid(sl, 4, di.sms, 8), dim3(256), 0, s,
+                                 sl, nblk, reinterpret_cast<const uint4 *>(x + r0 * d),
+                                 reinterpret_cast<uint2 *>(codes + r0 * d), scales + r0 * nblk);
+    });
+}
+
+cudaError_t launch_restore(int64_t rows, int64_t d, const Kept &k, uint16_t *x,
+                           const DeviceInfo &di, cudaStream_t s) {
+    const int64_t nblk = kept_blocks(d);
+    return by_pieces(rows, d, [&](int64_t r0, int64_t nr) {
+        const Slots sl = make_slots(nr, d);
+        return launch_overlapped(k_restore<4>, stream_grid(sl, 4, di.sms, 8), dim3(256), 0, s, sl,
+                                 nblk, rows_from(k, r0, d), reinterpret_cast<uint4 *>(x + r0 * d));
+    });
+}
+
+cudaError_t launch_pre_restore(int64_t n, int hc, int64_t d, const Kept &k, const float *pre,
+                               uint16_t *y, const DeviceInfo &di, cudaStream_t s) {
+    const int64_t nblk = kept_blocks(d);
+    return by_pieces(n, d, [&](int64_t t0, int64_t nt) {
+        const Slots sl = make_slots(nt, d);
+        uint4 *yv = reinterpret_cast<uint4 *>(y + t0 * d);
+        const Kept kt = rows_from(k, t0 * hc, d);
+        return hc == 4 ? launch_overlapped(k_pre_restore<4, 2>, stream_grid(sl, 2, di.sms, 8),
+                                           dim3(256), 0, s, sl, nblk, kt, pre + t0 * hc, yv)
+                       : launch_overlapped(k_pre_restore<8, 1>, stream_grid(sl, 1, di.sms, 8),
+                                           dim3(256), 0, s, sl, nblk, kt, pre + t0 * hc, yv);
+    });
+}
+
+cudaError_t launch_post_checkpoint(int64_t n, int hc, int64_t d, const uint16_t *out,
+                                   const uint16_t *res, const float *post, const float *comb,
+                                   uint16_t *y, uint8_t *codes, uint8_t *scales,
+                                   const DeviceInfo &di, cudaStream_t s) {
+    const int64_t nblk = kept_blocks(d);
+    return by_pieces(n, d, [&](int64_t t0, int64_t nt) {
+        const Slots sl = make_slots(nt, d);
+        const dim3 grid = stream_grid(sl, 1, di.sms, 8);
+        const int64_t row = t0 * hc;
+        const uint4 *ov = reinterpret_cast<const uint4 *>(out + t0 * d);
+        const uint4 *rv = reinterpret_cast<const uint4 *>(res + row * d);
+        uint4 *yv = reinterpret_cast<uint4 *>(y + row * d);
+        uint2 *cv = reinterpret_cast<uint2 *>(codes + row * d);
+        auto *kernel = hc == 4 ? &k_post_checkpoint<4> : &k_post_checkpoint<8>;
+        return launch_overlapped(kernel, grid, dim3(256), 0, s, sl, nblk, ov, rv, post + row,
+                                 comb + row * hc, yv, cv, scales + row * nblk);
+    });
+}
+
+}  // namespace hc

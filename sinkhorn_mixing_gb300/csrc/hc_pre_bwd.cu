@@ -1,0 +1,436 @@
+// hc_pre_bwd.cu -- gradients of hc_mixes_pre (and of the stream that hc_post
+// carries past the sublayer).
+//
+// Per token, with x the stream, F = HC d features, r = (mean x^2 + e)^-1/2, the
+// mix numbers m = r x W^T, logits z = m s + b, and G the gradient of the stream
+// that hc_post wrote with this call's comb:
+//   dpre_j = <dy, x_j>;  dz = the split's gradient from dpre, dpost, dcomb
+//   dm = dz s;  du = r dm;  q = -(r^2 / F) sum_i dm_i m_i
+//   dx_j = pre_j dy + q x_j + sum_i du_i W_ij + sum_k comb_jk G_k
+//   dW = sum over tokens of du x;  ds = sum dz m per group;  db = sum dz
+// Nothing of a token's dx is known before its dpre is, which sums over the
+// whole row, so the work is cut there: k_mix_backward makes the per-token
+// coefficients, k_dx and k_dw use them, k_sum adds the partial sums of dW, ds
+// and db in a fixed order.
+#include "hc_pre_bwd.h"
+
+namespace hc {
+namespace {
+
+constexpr int kMaxBlocks = 160 * 3;  // of k_mix_backward: rows of partial sums
+
+template <int HC>
+__host__ __device__ constexpr int mix_warps() { return 8 * HC / 32; }
+
+// -------------------------------------------------------- k_mix_backward
+// Warps 0-7 sum <dy, x_j> and sum x^2 of up to 8 tokens at a time (2^lg lanes
+// a token); mix_warps() more warps meanwhile run the same tokens' split
+// forward and backward, which needs neither sum until its end.  HC lanes share
+// a token, lane j holding row j of comb: a row step is local, a column step
+// sums over the lanes.
+//
+// The Sinkhorn steps are undone rather than kept: a step leaves its divisors
+// (HC numbers) in shared memory, and going back, the matrix before the step is
+// the one after it times them.  For C' = C / den, den = sum C + eps over the
+// row (or column):  dC = (dC' - sum dC' C') / den.
+template <int HC, bool K8>
+__global__ void __launch_bounds__(256 + 32 * mix_warps<HC>(), 3)
+    k_mix_backward(int64_t n, int64_t nv, int64_t nblk, int lg, int iters, float eps,
+                   float norm_eps, float features, const uint4 *__restrict__ dy, Kept x,
+                   const float *__restrict__ mixes, const float *__restrict__ scale,
+                   const float *__restrict__ base, const float *__restrict__ dpost,
+                   const float *__restrict__ dcomb, float *__restrict__ coef,
+                   float *__restrict__ partial) {
+    using CF = Coef<HC>;
+    constexpr int MIX = CF::kMix, MW = mix_warps<HC>(), THREADS = 256 + 32 * MW;
+    __shared__ float sums[2][8][HC + 1];
+    extern __shared__ float hist[];  // [MW][2 * iters - 1][32]
+    griddep_wait_then_release();
+    const int tpb = 256 >> lg, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    auto meet = [] { asm volatile("bar.sync 1, %0;" ::"n"(THREADS) : "memory"); };
+    const int64_t groups = (n + tpb - 1) / tpb;
+
+    if (warp < 8) {
+        const int lanes = 1 << lg, slot = threadIdx.x >> lg, l = threadIdx.x & (lanes - 1);
+        int buf = 0;
+        for (int64_t grp = blockIdx.x; grp < groups; grp += gridDim.x, buf ^= 1) {
+            const int64_t t = grp * tpb + slot;
+            float acc[HC + 1];
+#pragma unroll
+            for (int j = 0; j <= HC; ++j) acc[j] = 0.0f;
+            if (t < n) {
+#pragma unroll(HC == 4 ? 2 : 1)
+                for (int64_t v = l; v < nv; v += lanes) {
+                    const uint4 yv = __ldg(dy + t * nv + v);
+                    KeptVec<K8> xv[HC];
+#pragma unroll
+                    for (int j = 0; j < HC; ++j) xv[j].load(x, t * HC + j, nv, nblk, v);
+                    float yf[8], f[8];
+                    unpack8(yv, yf);
+#pragma unroll
+                    for (int j = 0; j < HC; ++j) {
+                        xv[j].values(f);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            acc[j] = fmaf(f[e], yf[e], acc[j]);
+                            acc[HC] = fmaf(f[e], f[e], acc[HC]);
+                        }
+                    }
+                }
+            }
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j <= HC; ++j)
+#pragma unroll
+                for (int off = 16; off > 0; off >>= 1)
+                    acc[j] += __shfl_xor_sync(0xFFFFFFFFu, acc[j], off);
+            if (lane == 0) {
+#pragma unroll
+                for (int j = 0; j <= HC; ++j) sums[buf][warp][j] = acc[j];
+            }
+            meet();
+        }
+        return;
+    }
+
+    const int mw = warp - 8, j = lane % HC, slot = mw * (32 / HC) + lane / HC;
+    const int steps = 2 * iters - 1;
+    float *h = hist + mw * steps * 32;
+    const float s0 = __ldg(scale), s1 = __ldg(scale + 1), s2 = __ldg(scale + 2);
+    const float b0 = __ldg(base + j), b1 = __ldg(base + HC + j);
+    float b2[HC];
+#pragma unroll
+    for (int k = 0; k < HC; ++k) b2[k] = __ldg(base + 2 * HC + j * HC + k);
+    float db0 = 0.0f, db1 = 0.0f, db2[HC], ds0 = 0.0f, ds1 = 0.0f, ds2 = 0.0f;
+#pragma unroll
+    for (int k = 0; k < HC; ++k) db2[k] = 0.0f;
+    // sums v[k] over the HC lanes of a token, in every one of them
+    auto over_rows = [](float v[HC]) {
+#pragma unroll
+        for (int off = 1; off < HC; off <<= 1)
+#pragma unroll
+            for (int k = 0; k < HC; ++k) v[k] += __shfl_xor_sync(0xFFFFFFFFu, v[k], off);
+    };
+
+    int buf = 0;
+    for (int64_t grp = blockIdx.x; grp < groups; grp += gridDim.x, buf ^= 1) {
+        const bool valid = slot < tpb && grp * tpb + slot < n;
+        const int64_t t = valid ? grp * tpb + slot : 0;  // idle lanes follow, and write nothing
+        const float *mt = mixes + t * MIX;
+        const float m0 = __ldg(mt + j), m1 = __ldg(mt + HC + j);
+        float m2[HC], P[HC], C[HC], G[HC], v[HC];
+#pragma unroll
+        for (int k = 0; k < HC; ++k) m2[k] = __ldg(mt + 2 * HC + j * HC + k);
+#pragma unroll
+        for (int k = 0; k < HC; ++k) G[k] = __ldg(dcomb + (t * HC + j) * HC + k);
+        const float gp = __ldg(dpost + t * HC + j);
+
+        // forward: the softmax P and the Sinkhorn steps, in the order of sinkhorn_comb
+#pragma unroll
+        for (int k = 0; k < HC; ++k) P[k] = fmaf(m2[k], s2, b2[k]);
+        float mx = P[0];
+#pragma unroll
+        for (int k = 1; k < HC; ++k) mx = fmaxf(mx, P[k]);
+#pragma unroll
+        for (int k = 0; k < HC; ++k) P[k] = expf(P[k] - mx);
+        float inv = rcp_refined(pair_sum(P));
+#pragma unroll
+        for (int k = 0; k < HC; ++k) {
+            C[k] = fmaf(P[k], inv, eps);
+            P[k] *= inv;
+        }
+        __syncwarp();
+        for (int i = 0; i < steps; ++i) {
+            if (i % 2 == 0) {
+#pragma unroll
+                for (int k = 0; k < HC; ++k) v[k] = C[k];
+                over_rows(v);
+                float own = 0.0f;
+#pragma unroll
+                for (int k = 0; k < HC; ++k) {
+                    v[k] += eps;
+                    if (k == j) own = v[k];
+                    C[k] *= rcp_refined(v[k]);
+                }
+                h[i * 32 + lane] = own;
+            } else {
+                const float den = pair_sum(C) + eps;
+                inv = rcp_refined(den);
+#pragma unroll
+                for (int k = 0; k < HC; ++k) C[k] *= inv;
+                h[i * 32 + lane] = den;
+            }
+        }
+        __syncwarp();
+        float *ct = coef + t * CF::kFloats;
+        if (valid) {
+#pragma unroll
+            for (int k = 0; k < HC; k += 4)
+                *reinterpret_cast<float4 *>(ct + CF::kComb + j * HC + k) =
+                    make_float4(C[k], C[k + 1], C[k + 2], C[k + 3]);
+        }
+        // backward through the steps
+        for (int i = steps - 1; i >= 0; --i) {
+            if (i % 2 == 0) {
+#pragma unroll
+                for (int k = 0; k < HC; ++k) v[k] = G[k] * C[k];
+                over_rows(v);
+                const float *dh = h + i * 32 + (lane - j);
+#pragma unroll
+                for (int k = 0; k < HC; ++k) {
+                    const float den = dh[k];
+                    G[k] = (G[k] - v[k]) * rcp_refined(den);
+                    C[k] *= den;
+                }
+            } else {
+                const float den = h[i * 32 + lane];
+#pragma unroll
+                for (int k = 0; k < HC; ++k) v[k] = G[k] * C[k];
+                const float dot = pair_sum(v);
+                inv = rcp_refined(den);
+#pragma unroll
+                for (int k = 0; k < HC; ++k) {
+                    G[k] = (G[k] - dot) * inv;
+                    C[k] *= den;
+                }
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < HC; ++k) v[k] = G[k] * P[k];
+        const float dot = pair_sum(v);
+#pragma unroll
+        for (int k = 0; k < HC; ++k) G[k] = P[k] * (G[k] - dot);  // dz of comb
+
+        // sigmoid(z) and its derivative e / (1+e)^2, e = e^-|z|
+        const float z0 = fmaf(m0, s0, b0), e0 = expf(-fabsf(z0)), r0 = rcp_refined(1.0f + e0);
+        const float z1 = fmaf(m1, s1, b1), e1 = expf(-fabsf(z1)), r1 = rcp_refined(1.0f + e1);
+        const float pre = (z0 >= 0.0f ? r0 : e0 * r0) + eps;
+        const float dz1 = 2.0f * gp * (e1 * r1 * r1);
+
+        meet();
+        float dpre = 0.0f, ss = 0.0f;
+        if (valid) {
+            for (int w = 0; w < (1 << lg) / 32; ++w) {
+                dpre += sums[buf][slot * ((1 << lg) / 32) + w][j];
+                ss += sums[buf][slot * ((1 << lg) / 32) + w][HC];
+            }
+        }
+        const float dz0 = dpre * (e0 * r0 * r0);
+        const float r2 = 1.0f / (ss / features + norm_eps), r = sqrtf(r2);
+        const float dm0 = dz0 * s0, dm1 = dz1 * s1;
+        float c2 = 0.0f;
+#pragma unroll
+        for (int k = 0; k < HC; ++k) c2 = fmaf(G[k], m2[k], c2);
+        float dot_m = fmaf(dm0, m0, fmaf(dm1, m1, c2 * s2));
+#pragma unroll
+        for (int off = 1; off < HC; off <<= 1)
+            dot_m += __shfl_xor_sync(0xFFFFFFFFu, dot_m, off);
+        if (valid) {
+            ct[j] = pre;
+            if (j < 4) ct[CF::kQ + j] = j == 0 ? -dot_m * r2 / features : 0.0f;
+            ct[CF::kDu + j] = dm0 * r;
+            ct[CF::kDu + HC + j] = dm1 * r;
+            const float f = s2 * r;
+#pragma unroll
+            for (int k = 0; k < HC; k += 4)
+                *reinterpret_cast<float4 *>(ct + CF::kDu + 2 * HC + j * HC + k) =
+                    make_float4(G[k] * f, G[k + 1] * f, G[k + 2] * f, G[k + 3] * f);
+            db0 += dz0, db1 += dz1;
+#pragma unroll
+            for (int k = 0; k < HC; ++k) db2[k] += G[k];
+            ds0 = fmaf(dz0, m0, ds0), ds1 = fmaf(dz1, m1, ds1), ds2 += c2;
+        }
+    }
+    // over the tokens of the warp; the scales' sums over the rows as well
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+        if (off >= HC) {
+            db0 += __shfl_xor_sync(0xFFFFFFFFu, db0, off);
+            db1 += __shfl_xor_sync(0xFFFFFFFFu, db1, off);
+#pragma unroll
+            for (int k = 0; k < HC; ++k) db2[k] += __shfl_xor_sync(0xFFFFFFFFu, db2[k], off);
+        }
+        ds0 += __shfl_xor_sync(0xFFFFFFFFu, ds0, off);
+        ds1 += __shfl_xor_sync(0xFFFFFFFFu, ds1, off);
+        ds2 += __shfl_xor_sync(0xFFFFFFFFu, ds2, off);
+    }
+    float *pt = partial + (int64_t)(blockIdx.x * MW + mw) * (MIX + 4);
+    if (lane < HC) {
+        pt[j] = db0;
+        pt[HC + j] = db1;
+#pragma unroll
+        for (int k = 0; k < HC; ++k) pt[2 * HC + j * HC + k] = db2[k];
+    }
+    if (lane == 0) pt[MIX] = ds0, pt[MIX + 1] = ds1, pt[MIX + 2] = ds2;
+}
+
+// ------------------------------------------------------------------ k_dx
+// One lane, 8 channels of all copies of a token; W from the cache.
+template <int HC, bool K8>
+__global__ void __launch_bounds__(256) k_dx(int64_t n, int64_t nv, int64_t nblk,
+                                            const uint4 *__restrict__ dy, Kept x,
+                                            const float *__restrict__ w, const uint4 *g, uint4 *dx,
+                                            const float *__restrict__ coef) {
+    using CF = Coef<HC>;
+    griddep_wait_then_release();
+    const int64_t total = n * nv;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total;
+         i += (int64_t)gridDim.x * 256) {
+        const int64_t t = i / nv, v = i % nv;
+        const float *c = coef + t * CF::kFloats;
+        uint4 gv[HC];
+#pragma unroll
+        for (int k = 0; k < HC; ++k)
+            gv[k] = g != nullptr ? ld_stream(g + (t * HC + k) * nv + v) : make_uint4(0, 0, 0, 0);
+        float yf[8], f[8], acc[8];
+        unpack8(ld_stream(dy + t * nv + v), yf);
+        for (int j = 0; j < HC; ++j) {
+            KeptVec<K8> xv;
+            xv.load(x, t * HC + j, nv, nblk, v);
+            xv.values(f);
+            const float pj = __ldg(c + j), q = __ldg(c + CF::kQ);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) acc[e] = fmaf(q, f[e], pj * yf[e]);
+#pragma unroll
+            for (int k = 0; k < HC; ++k) {
+                unpack8(gv[k], f);
+                const float cjk = __ldg(c + CF::kComb + j * HC + k);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) acc[e] = fmaf(cjk, f[e], acc[e]);
+            }
+            for (int m = 0; m < CF::kMix; ++m) {
+                const float du = __ldg(c + CF::kDu + m);
+                const float4 *wp =
+                    reinterpret_cast<const float4 *>(w + ((int64_t)m * HC + j) * nv * 8 + v * 8);
+                const float4 a = __ldg(wp), b = __ldg(wp + 1);
+                acc[0] = fmaf(du, a.x, acc[0]), acc[1] = fmaf(du, a.y, acc[1]);
+                acc[2] = fmaf(du, a.z, acc[2]), acc[3] = fmaf(du, a.w, acc[3]);
+                acc[4] = fmaf(du, b.x, acc[4]), acc[5] = fmaf(du, b.y, acc[5]);
+                acc[6] = fmaf(du, b.z, acc[6]), acc[7] = fmaf(du, b.w, acc[7]);
+            }
+            st_stream(dx + (t * HC + j) * nv + v, pack8(acc));
+        }
+    }
+}
+
+// ------------------------------------------------------------------ k_dw
+// One thread, one feature, all mix numbers, a range of tokens.
+template <int HC, bool K8>
+__global__ void __launch_bounds__(128) k_dw(int64_t n, int64_t d, int64_t nblk, int64_t per,
+                                            Kept x, const float *__restrict__ coef,
+                                            float *__restrict__ partial) {
+    using CF = Coef<HC>;
+    griddep_wait_then_release();
+    const int64_t F = HC * d, f = (int64_t)blockIdx.x * 128 + threadIdx.x;
+    if (f >= F) return;
+    const int64_t t0 = blockIdx.y * per, t1 = min(n, t0 + per);
+    float acc[CF::kMix];
+#pragma unroll
+    for (int i = 0; i < CF::kMix; ++i) acc[i] = 0.0f;
+    for (int64_t t = t0; t < t1; ++t) {
+        float xf;
+        if (K8) {
+            float unused;
+            e4m3x2_to_float(static_cast<const uint8_t *>(x.data)[t * F + f], xf, unused);
+            xf *= kept_scale(x.scales[(t * HC + f / d) * nblk + (f % d) / kKeptBlock]);
+        } else {
+            xf = bf16lo(static_cast<const uint16_t *>(x.data)[t * F + f]);
+        }
+        const float *du = coef + t * CF::kFloats + CF::kDu;
+#pragma unroll
+        for (int i = 0; i < CF::kMix; ++i) acc[i] = fmaf(__ldg(du + i), xf, acc[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < CF::kMix; ++i) partial[((int64_t)blockIdx.y * CF::kMix + i) * F + f] = acc[i];
+}
+
+// ----------------------------------------------------------------- k_sum
+__global__ void __launch_bounds__(256) k_sum(int64_t count, int ranges, const float *__restrict__ dwp,
+                                             float *__restrict__ dw, int mix, int rows,
+                                             const float *__restrict__ mp,
+                                             float *__restrict__ dscale, float *__restrict__ dbase) {
+    griddep_wait_then_release();
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i < count) {
+        float a = 0.0f;
+        for (int r = 0; r < ranges; ++r) a += dwp[r * count + i];
+        dw[i] = a;
+    }
+    if (blockIdx.x == 0 && threadIdx.x < mix + 3) {
+        double a = 0.0;
+        for (int r = 0; r < rows; ++r) a += (double)mp[(int64_t)r * (mix + 4) + threadIdx.x];
+        if (threadIdx.x < mix)
+            dbase[threadIdx.x] = (float)a;
+        else
+            dscale[threadIdx.x - mix] = (float)a;
+    }
+}
+
+size_t up256(size_t b) { return (b + 255) / 256 * 256; }
+
+int64_t dw_ranges(int64_t n) {
+    const int64_t r = (n + 255) / 256;
+    return r < 16 ? r : 16;
+}
+
+template <int HC>
+size_t coef_bytes(int64_t n) { return up256((size_t)n * Coef<HC>::kFloats * 4); }
+size_t mix_partial_bytes(int hc) {
+    return up256((size_t)kMaxBlocks * (8 * hc / 32) * ((2 + hc) * hc + 4) * 4);
+}
+
+template <int HC, bool K8>
+cudaError_t launch(const PreBackward &p, const DeviceInfo &di, cudaStream_t s) {
+    constexpr int MW = mix_warps<HC>(), MIX = Coef<HC>::kMix;
+    const int64_t nv = p.d / 8, nblk = kept_blocks(p.d), F = HC * p.d;
+    float *coef = reinterpret_cast<float *>(p.ws);
+    float *mp = reinterpret_cast<float *>(p.ws + coef_bytes<HC>(p.n));
+    float *dwp = reinterpret_cast<float *>(p.ws + coef_bytes<HC>(p.n) + mix_partial_bytes(HC));
+    int lg = 5;
+    while (lg < 8 && (1 << lg) < nv && (p.n >> (8 - lg)) < (int64_t)di.sms * 3) ++lg;
+    const int64_t groups = (p.n + (256 >> lg) - 1) / (256 >> lg);
+    const int64_t cap = di.sms * 3 < kMaxBlocks ? di.sms * 3 : kMaxBlocks;
+    const int blocks = (int)(groups < cap ? groups : cap);
+    const size_t smem = (size_t)MW * (2 * p.iters - 1) * 32 * 4;
+    if (smem > 48 * 1024) {
+        const cudaError_t e =
+            cudaFuncSetAttribute(k_mix_backward<HC, K8>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+    }
+    const uint4 *dy = reinterpret_cast<const uint4 *>(p.dy);
+    cudaError_t e = launch_overlapped(k_mix_backward<HC, K8>, dim3(blocks), dim3(256 + 32 * MW),
+                                      smem, s, p.n, nv, nblk, lg, p.iters, p.eps, p.norm_eps,
+                                      (float)F, dy, p.x, p.mixes, p.scale, p.base, p.dpost,
+                                      p.dcomb, coef, mp);
+    if (e != cudaSuccess) return e;
+    const int64_t want = (p.n * nv + 255) / 256, most = (int64_t)di.sms * 64;
+    e = launch_overlapped(k_dx<HC, K8>, dim3((unsigned)(want < most ? want : most)), dim3(256), 0,
+                          s, p.n, nv, nblk, dy, p.x, p.w,
+                          reinterpret_cast<const uint4 *>(p.dstream),
+                          reinterpret_cast<uint4 *>(p.dx), coef);
+    if (e != cudaSuccess) return e;
+    const int64_t ranges = dw_ranges(p.n), per = (p.n + ranges - 1) / ranges;
+    e = launch_overlapped(k_dw<HC, K8>, dim3((unsigned)((F + 127) / 128), (unsigned)ranges),
+                          dim3(128), 0, s, p.n, p.d, nblk, per, p.x, coef, dwp);
+    if (e != cudaSuccess) return e;
+    const int64_t count = MIX * F;
+    return launch_overlapped(k_sum, dim3((unsigned)((count + 255) / 256)), dim3(256), 0, s, count,
+                             (int)ranges, dwp, p.dw, MIX, blocks * MW, mp, p.dscale, p.dbase);
+}
+
+}  // namespace
+
+size_t pre_backward_bytes(int64_t n, int hc, int64_t d) {
+    const size_t coef = hc == 4 ? coef_bytes<4>(n) : coef_bytes<8>(n);
+    const size_t mix = (size_t)(2 + hc) * hc;
+    return coef + mix_partial_bytes(hc) + up256((size_t)dw_ranges(n) * mix * hc * d * 4);
+}
+
+cudaError_t launch_pre_backward(const PreBackward &p, const DeviceInfo &di, cudaStream_t s) {
+    const bool k8 = p.x.scales != nullptr;
+    if (p.hc == 4) return k8 ? launch<4, true>(p, di, s) : launch<4, false>(p, di, s);
+    return k8 ? launch<8, true>(p, di, s) : launch<8, false>(p, di, s);
+}
+
+}  // namespace hc
