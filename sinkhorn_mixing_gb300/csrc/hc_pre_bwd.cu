@@ -10,8 +10,10 @@
 //   dW = sum over tokens of du x;  ds = sum dz m per group;  db = sum dz
 // Nothing of a token's dx is known before its dpre is, which sums over the
 // whole row, so the work is cut there: k_mix_backward makes the per-token
-// coefficients, k_dx and k_dw use them, k_sum adds the partial sums of dW, ds
-// and db in a fixed order.
+// coefficients, k_dx_dw (hc_pre_bwd_main.cu) uses them, k_sum adds the partial
+// sums of dW, ds and db in a fixed order.
+#include <cuda_fp16.h>
+
 #include "hc_pre_bwd.h"
 
 namespace hc {
@@ -39,7 +41,8 @@ __global__ void __launch_bounds__(256 + 32 * mix_warps<HC>(), 3)
                    float norm_eps, float features, const uint4 *__restrict__ dy, Kept x,
                    const float *__restrict__ mixes, const float *__restrict__ scale,
                    const float *__restrict__ base, const float *__restrict__ dpost,
-                   const float *__restrict__ dcomb, float *__restrict__ coef,
+                   const float *__restrict__ dcomb, float *__restrict__ cf,
+                   uint16_t *__restrict__ du16, uint16_t *__restrict__ du3,
                    float *__restrict__ partial) {
     using CF = Coef<HC>;
     constexpr int MIX = CF::kMix, MW = mix_warps<HC>(), THREADS = 256 + 32 * MW;
@@ -162,12 +165,10 @@ __global__ void __launch_bounds__(256 + 32 * mix_warps<HC>(), 3)
             }
         }
         __syncwarp();
-        float *ct = coef + t * CF::kFloats;
+        float *ct = cf + t * CF::kCf;
         if (valid) {
 #pragma unroll
-            for (int k = 0; k < HC; k += 4)
-                *reinterpret_cast<float4 *>(ct + CF::kComb + j * HC + k) =
-                    make_float4(C[k], C[k + 1], C[k + 2], C[k + 3]);
+            for (int k = 0; k < HC; ++k) ct[k * HC + j] = C[k];
         }
         // backward through the steps
         for (int i = steps - 1; i >= 0; --i) {
@@ -225,16 +226,41 @@ __global__ void __launch_bounds__(256 + 32 * mix_warps<HC>(), 3)
 #pragma unroll
         for (int off = 1; off < HC; off <<= 1)
             dot_m += __shfl_xor_sync(0xFFFFFFFFu, dot_m, off);
-        if (valid) {
-            ct[j] = pre;
-            if (j < 4) ct[CF::kQ + j] = j == 0 ? -dot_m * r2 / features : 0.0f;
-            ct[CF::kDu + j] = dm0 * r;
-            ct[CF::kDu + HC + j] = dm1 * r;
-            const float f = s2 * r;
+        // du, and its forms for the products
+        const float du0 = dm0 * r, du1 = dm1 * r, f2 = s2 * r;
+        float du2[HC], top = fmaxf(fabsf(du0), fabsf(du1));
 #pragma unroll
-            for (int k = 0; k < HC; k += 4)
-                *reinterpret_cast<float4 *>(ct + CF::kDu + 2 * HC + j * HC + k) =
-                    make_float4(G[k] * f, G[k + 1] * f, G[k + 2] * f, G[k + 3] * f);
+        for (int k = 0; k < HC; ++k) {
+            du2[k] = G[k] * f2;
+            top = fmaxf(top, fabsf(du2[k]));
+        }
+#pragma unroll
+        for (int off = 1; off < HC; off <<= 1)
+            top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, off));
+        const int ex = min(max((int)(__float_as_uint(top) >> 23), 14), 253);
+        const float up = __uint_as_float((uint32_t)(267 - ex) << 23);
+        if (valid) {
+            ct[CF::kPre + j] = pre;
+            if (j < 4)
+                ct[CF::kQ + j] = j == 0   ? -dot_m * r2 / features
+                                 : j == 1 ? __uint_as_float((uint32_t)(ex - 13) << 23)
+                                          : 0.0f;
+            uint16_t *h16 = du16 + t * CF::kK, *h3 = du3 + t * CF::kParts;
+            auto put = [&](int i, float v) {
+                h16[i] = __half_as_ushort(__float2half_rn(v * up));
+#pragma unroll
+                for (int p = 0; p < 3; ++p) {
+                    const __nv_bfloat16 b = __float2bfloat16_rn(v);
+                    h3[p * MIX + i] = __bfloat16_as_ushort(b);
+                    v -= __bfloat162float(b);
+                }
+            };
+            put(j, du0);
+            put(HC + j, du1);
+#pragma unroll
+            for (int k = 0; k < HC; ++k) put(2 * HC + j * HC + k, du2[k]);
+            for (int i = MIX + j; i < CF::kK; i += HC) h16[i] = 0;
+            for (int i = 3 * MIX + j; i < CF::kParts; i += HC) h3[i] = 0;
             db0 += dz0, db1 += dz1;
 #pragma unroll
             for (int k = 0; k < HC; ++k) db2[k] += G[k];
@@ -264,128 +290,73 @@ __global__ void __launch_bounds__(256 + 32 * mix_warps<HC>(), 3)
     if (lane == 0) pt[MIX] = ds0, pt[MIX + 1] = ds1, pt[MIX + 2] = ds2;
 }
 
-// ------------------------------------------------------------------ k_dx
-// One lane, 8 channels of all copies of a token; W from the cache.
-template <int HC, bool K8>
-__global__ void __launch_bounds__(256) k_dx(int64_t n, int64_t nv, int64_t nblk,
-                                            const uint4 *__restrict__ dy, Kept x,
-                                            const float *__restrict__ w, const uint4 *g, uint4 *dx,
-                                            const float *__restrict__ coef) {
-    using CF = Coef<HC>;
-    griddep_wait_then_release();
-    const int64_t total = n * nv;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total;
-         i += (int64_t)gridDim.x * 256) {
-        const int64_t t = i / nv, v = i % nv;
-        const float *c = coef + t * CF::kFloats;
-        uint4 gv[HC];
-#pragma unroll
-        for (int k = 0; k < HC; ++k)
-            gv[k] = g != nullptr ? ld_stream(g + (t * HC + k) * nv + v) : make_uint4(0, 0, 0, 0);
-        float yf[8], f[8], acc[8];
-        unpack8(ld_stream(dy + t * nv + v), yf);
-        for (int j = 0; j < HC; ++j) {
-            KeptVec<K8> xv;
-            xv.load(x, t * HC + j, nv, nblk, v);
-            xv.values(f);
-            const float pj = __ldg(c + j), q = __ldg(c + CF::kQ);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) acc[e] = fmaf(q, f[e], pj * yf[e]);
-#pragma unroll
-            for (int k = 0; k < HC; ++k) {
-                unpack8(gv[k], f);
-                const float cjk = __ldg(c + CF::kComb + j * HC + k);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) acc[e] = fmaf(cjk, f[e], acc[e]);
-            }
-            for (int m = 0; m < CF::kMix; ++m) {
-                const float du = __ldg(c + CF::kDu + m);
-                const float4 *wp =
-                    reinterpret_cast<const float4 *>(w + ((int64_t)m * HC + j) * nv * 8 + v * 8);
-                const float4 a = __ldg(wp), b = __ldg(wp + 1);
-                acc[0] = fmaf(du, a.x, acc[0]), acc[1] = fmaf(du, a.y, acc[1]);
-                acc[2] = fmaf(du, a.z, acc[2]), acc[3] = fmaf(du, a.w, acc[3]);
-                acc[4] = fmaf(du, b.x, acc[4]), acc[5] = fmaf(du, b.y, acc[5]);
-                acc[6] = fmaf(du, b.z, acc[6]), acc[7] = fmaf(du, b.w, acc[7]);
-            }
-            st_stream(dx + (t * HC + j) * nv + v, pack8(acc));
-        }
-    }
-}
-
-// ------------------------------------------------------------------ k_dw
-// One thread, one feature, all mix numbers, a range of tokens.
-template <int HC, bool K8>
-__global__ void __launch_bounds__(128) k_dw(int64_t n, int64_t d, int64_t nblk, int64_t per,
-                                            Kept x, const float *__restrict__ coef,
-                                            float *__restrict__ partial) {
-    using CF = Coef<HC>;
-    griddep_wait_then_release();
-    const int64_t F = HC * d, f = (int64_t)blockIdx.x * 128 + threadIdx.x;
-    if (f >= F) return;
-    const int64_t t0 = blockIdx.y * per, t1 = min(n, t0 + per);
-    float acc[CF::kMix];
-#pragma unroll
-    for (int i = 0; i < CF::kMix; ++i) acc[i] = 0.0f;
-    for (int64_t t = t0; t < t1; ++t) {
-        float xf;
-        if (K8) {
-            float unused;
-            e4m3x2_to_float(static_cast<const uint8_t *>(x.data)[t * F + f], xf, unused);
-            xf *= kept_scale(x.scales[(t * HC + f / d) * nblk + (f % d) / kKeptBlock]);
-        } else {
-            xf = bf16lo(static_cast<const uint16_t *>(x.data)[t * F + f]);
-        }
-        const float *du = coef + t * CF::kFloats + CF::kDu;
-#pragma unroll
-        for (int i = 0; i < CF::kMix; ++i) acc[i] = fmaf(__ldg(du + i), xf, acc[i]);
-    }
-#pragma unroll
-    for (int i = 0; i < CF::kMix; ++i) partial[((int64_t)blockIdx.y * CF::kMix + i) * F + f] = acc[i];
-}
-
 // ----------------------------------------------------------------- k_sum
-__global__ void __launch_bounds__(256) k_sum(int64_t count, int ranges, const float *__restrict__ dwp,
-                                             float *__restrict__ dw, int mix, int rows,
+// dW from the partial sums of the blocks that worked on a slice of channels,
+// one block of threads per (slice, mix number); behind those, one warp per
+// column of k_mix_backward's partial sums.
+template <int HC>
+__global__ void __launch_bounds__(256) k_sum(Split sp, int64_t d, const float *__restrict__ dwp,
+                                             float *__restrict__ dw, int rows,
                                              const float *__restrict__ mp,
-                                             float *__restrict__ dscale, float *__restrict__ dbase) {
+                                             float *__restrict__ dscale,
+                                             float *__restrict__ dbase) {
+    constexpr int MIX = Coef<HC>::kMix, CH = Split::channels(HC), FT = HC * CH;
     griddep_wait_then_release();
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i < count) {
-        float a = 0.0f;
-        for (int r = 0; r < ranges; ++r) a += dwp[r * count + i];
-        dw[i] = a;
+    const int64_t b = blockIdx.x, dwb = sp.slices * MIX;
+    if (b < dwb) {
+        const int64_t s = b / MIX;
+        const int i = (int)(b % MIX);
+        const int64_t c0 = sp.block_of(s * sp.steps), c1 = sp.block_of((s + 1) * sp.steps - 1);
+        for (int m = threadIdx.x; m < FT; m += 256) {
+            const int64_t c = s * CH + m % CH;
+            if (c >= d) continue;
+            float a = 0.0f;
+            for (int64_t p = c0; p <= c1; ++p) a += dwp[((p + s) * MIX + i) * FT + m];
+            dw[((int64_t)i * HC + m / CH) * d + c] = a;
+        }
+        return;
     }
-    if (blockIdx.x == 0 && threadIdx.x < mix + 3) {
-        double a = 0.0;
-        for (int r = 0; r < rows; ++r) a += (double)mp[(int64_t)r * (mix + 4) + threadIdx.x];
-        if (threadIdx.x < mix)
-            dbase[threadIdx.x] = (float)a;
-        else
-            dscale[threadIdx.x - mix] = (float)a;
-    }
+    const int lane = threadIdx.x & 31, col = (int)(b - dwb) * 8 + (threadIdx.x >> 5);
+    if (col >= MIX + 3) return;
+    double a = 0.0;
+    for (int r = lane; r < rows; r += 32) a += (double)mp[(int64_t)r * (MIX + 4) + col];
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) a += __shfl_xor_sync(0xFFFFFFFFu, a, off);
+    if (lane == 0) (col < MIX ? dbase[col] : dscale[col - MIX]) = (float)a;
 }
 
 size_t up256(size_t b) { return (b + 255) / 256 * 256; }
 
-int64_t dw_ranges(int64_t n) {
-    const int64_t r = (n + 255) / 256;
-    return r < 16 ? r : 16;
-}
-
+// The workspace's parts, in this order.
+struct Parts {
+    size_t cf, du16, du3, mix, dw, end;
+};
 template <int HC>
-size_t coef_bytes(int64_t n) { return up256((size_t)n * Coef<HC>::kFloats * 4); }
-size_t mix_partial_bytes(int hc) {
-    return up256((size_t)kMaxBlocks * (8 * hc / 32) * ((2 + hc) * hc + 4) * 4);
+Parts parts(int64_t n, int64_t d) {
+    using CF = Coef<HC>;
+    Parts p;
+    p.cf = 0;
+    p.du16 = p.cf + up256((size_t)n * CF::kCf * 4);
+    p.du3 = p.du16 + up256((size_t)n * CF::kK * 2);
+    p.mix = p.du3 + up256((size_t)n * CF::kParts * 2);
+    p.dw = p.mix + up256((size_t)kMaxBlocks * mix_warps<HC>() * (CF::kMix + 4) * 4);
+    // a block crosses into another slice at most once per slice
+    const Split sp = Split::of(n, HC, d, Split::kMaxBlocks);
+    p.end = p.dw + up256((size_t)(sp.blocks + sp.slices) * CF::kMix * HC * Split::channels(HC) * 4);
+    return p;
 }
 
 template <int HC, bool K8>
 cudaError_t launch(const PreBackward &p, const DeviceInfo &di, cudaStream_t s) {
     constexpr int MW = mix_warps<HC>(), MIX = Coef<HC>::kMix;
     const int64_t nv = p.d / 8, nblk = kept_blocks(p.d), F = HC * p.d;
-    float *coef = reinterpret_cast<float *>(p.ws);
-    float *mp = reinterpret_cast<float *>(p.ws + coef_bytes<HC>(p.n));
-    float *dwp = reinterpret_cast<float *>(p.ws + coef_bytes<HC>(p.n) + mix_partial_bytes(HC));
+    const Parts at = parts<HC>(p.n, p.d);
+    MainArgs m;
+    m.cf = reinterpret_cast<float *>(p.ws + at.cf);
+    m.du16 = reinterpret_cast<uint16_t *>(p.ws + at.du16);
+    m.du3 = reinterpret_cast<uint16_t *>(p.ws + at.du3);
+    m.dwp = reinterpret_cast<float *>(p.ws + at.dw);
+    float *mp = reinterpret_cast<float *>(p.ws + at.mix);
     int lg = 5;
     while (lg < 8 && (1 << lg) < nv && (p.n >> (8 - lg)) < (int64_t)di.sms * 3) ++lg;
     const int64_t groups = (p.n + (256 >> lg) - 1) / (256 >> lg);
@@ -398,33 +369,23 @@ cudaError_t launch(const PreBackward &p, const DeviceInfo &di, cudaStream_t s) {
                                  cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
     }
-    const uint4 *dy = reinterpret_cast<const uint4 *>(p.dy);
-    cudaError_t e = launch_overlapped(k_mix_backward<HC, K8>, dim3(blocks), dim3(256 + 32 * MW),
-                                      smem, s, p.n, nv, nblk, lg, p.iters, p.eps, p.norm_eps,
-                                      (float)F, dy, p.x, p.mixes, p.scale, p.base, p.dpost,
-                                      p.dcomb, coef, mp);
+    cudaError_t e = launch_overlapped(
+        k_mix_backward<HC, K8>, dim3(blocks), dim3(256 + 32 * MW), smem, s, p.n, nv, nblk, lg,
+        p.iters, p.eps, p.norm_eps, (float)F, reinterpret_cast<const uint4 *>(p.dy), p.x, p.mixes,
+        p.scale, p.base, p.dpost, p.dcomb, m.cf, m.du16, m.du3, mp);
     if (e != cudaSuccess) return e;
-    const int64_t want = (p.n * nv + 255) / 256, most = (int64_t)di.sms * 64;
-    e = launch_overlapped(k_dx<HC, K8>, dim3((unsigned)(want < most ? want : most)), dim3(256), 0,
-                          s, p.n, nv, nblk, dy, p.x, p.w,
-                          reinterpret_cast<const uint4 *>(p.dstream),
-                          reinterpret_cast<uint4 *>(p.dx), coef);
+    m.split = Split::of(p.n, HC, p.d, di.sms < Split::kMaxBlocks ? di.sms : Split::kMaxBlocks);
+    e = launch_dx_dw(p, m, di, s);
     if (e != cudaSuccess) return e;
-    const int64_t ranges = dw_ranges(p.n), per = (p.n + ranges - 1) / ranges;
-    e = launch_overlapped(k_dw<HC, K8>, dim3((unsigned)((F + 127) / 128), (unsigned)ranges),
-                          dim3(128), 0, s, p.n, p.d, nblk, per, p.x, coef, dwp);
-    if (e != cudaSuccess) return e;
-    const int64_t count = MIX * F;
-    return launch_overlapped(k_sum, dim3((unsigned)((count + 255) / 256)), dim3(256), 0, s, count,
-                             (int)ranges, dwp, p.dw, MIX, blocks * MW, mp, p.dscale, p.dbase);
+    const int64_t grid = m.split.slices * MIX + (MIX + 3 + 7) / 8;
+    return launch_overlapped(k_sum<HC>, dim3((unsigned)grid), dim3(256), 0, s, m.split, p.d, m.dwp,
+                             p.dw, blocks * MW, mp, p.dscale, p.dbase);
 }
 
 }  // namespace
 
 size_t pre_backward_bytes(int64_t n, int hc, int64_t d) {
-    const size_t coef = hc == 4 ? coef_bytes<4>(n) : coef_bytes<8>(n);
-    const size_t mix = (size_t)(2 + hc) * hc;
-    return coef + mix_partial_bytes(hc) + up256((size_t)dw_ranges(n) * mix * hc * d * 4);
+    return hc == 4 ? parts<4>(n, d).end : parts<8>(n, d).end;
 }
 
 cudaError_t launch_pre_backward(const PreBackward &p, const DeviceInfo &di, cudaStream_t s) {

@@ -6,14 +6,23 @@
 
 namespace hc {
 
-// Per-token coefficients that the first kernel leaves for the second, in
-// floats: pre [HC], q, padding to HC + 4; comb [HC][HC]; du [(2+HC) HC].
+// What the first kernel leaves per token for the second.
+//   cf [kCf] float: comb transposed [k][j] (comb_jk of one k lie together),
+//     pre [HC], q, f, padding
+//   du16 [kK] fp16: du times a power of two 1/f of the token's own that puts
+//     its largest magnitude in [2^13, 2^14), zeros behind (2+HC) HC
+//   du3 [kParts] bf16: du = hi + mid + lo, three bf16 numbers (24 bits).
+//     HC = 4: [hi | mid | lo | zeros] of 24 each, in 80; HC = 8: 3 x 80.
 template <int HC>
 struct Coef {
     static constexpr int kMix = (2 + HC) * HC;
-    static constexpr int kQ = HC, kComb = HC + 4, kDu = HC + 4 + HC * HC;
-    static constexpr int kFloats = kDu + kMix;
-    static_assert(kFloats % 4 == 0, "rows of whole 16-byte pieces");
+    static constexpr int kPre = HC * HC, kQ = kPre + HC, kF = kQ + 1, kCf = kQ + 4;
+    static constexpr int kK = (kMix + 15) / 16 * 16;
+    static constexpr int kN = 80;                        // N of one product
+    static constexpr int kProducts = HC == 4 ? 1 : 3;
+    static constexpr int kParts = kN * kProducts;
+    static_assert(kCf % 4 == 0 && kK % 8 == 0 && kParts % 8 == 0, "rows of 16-byte pieces");
+    static_assert(HC == 4 ? 3 * kMix <= kN : kMix == kN, "three parts fit");
 };
 
 struct PreBackward {
@@ -30,9 +39,43 @@ struct PreBackward {
     uint8_t *ws;                           // pre_backward_bytes
 };
 
+// How the second kernel's work is cut: slices of channels, each walked in steps
+// of tokens; the steps of all slices in a row (slice-major) are dealt to the
+// blocks in equal runs, so every block has the same work whatever the shape.
+// Block c has steps [c * total / blocks, (c + 1) * total / blocks); the partial
+// sums that it leaves for slice s are number c + s, which no other pair has.
+struct Split {
+    static constexpr int kMaxBlocks = 160;
+    int64_t slices, steps, total, blocks;
+    static constexpr __host__ __device__ int channels(int hc) { return hc == 4 ? 128 : 64; }
+    static constexpr __host__ __device__ int tokens(int hc) { return hc == 4 ? 32 : 16; }
+    static Split of(int64_t n, int hc, int64_t d, int64_t most) {
+        Split s;
+        s.slices = (d + channels(hc) - 1) / channels(hc);
+        s.steps = (n + tokens(hc) - 1) / tokens(hc);
+        s.total = s.slices * s.steps;
+        s.blocks = s.total < most ? s.total : most;
+        return s;
+    }
+    // (total is below 2^46: n * hc * d is at most 2^58)
+    __host__ __device__ int64_t first(int64_t c) const { return c * total / blocks; }
+    __host__ __device__ int64_t block_of(int64_t step) const {
+        return ((step + 1) * blocks - 1) / total;
+    }
+};
+
+struct MainArgs {
+    Split split;
+    float *cf;
+    uint16_t *du16, *du3;
+    float *dwp;  // [blocks + slices][mix][hc * channels]
+};
+
 constexpr int kBackwardMaxIters = 256;  // Sinkhorn divisors kept in shared memory
 
 size_t pre_backward_bytes(int64_t n, int hc, int64_t d);
+cudaError_t launch_dx_dw(const PreBackward &p, const MainArgs &m, const DeviceInfo &di,
+                         cudaStream_t s);
 cudaError_t launch_pre_backward(const PreBackward &p, const DeviceInfo &di, cudaStream_t s);
 
 }  // namespace hc
