@@ -351,112 +351,144 @@ def hc_post_mixes_pre(out, residual, post, comb, w_mix, hc_scale, hc_base,
 
 KEPT_BLOCK = 32  # channels that share a scale byte (hcmix.h, hc_checkpoint)
 
+# The functions below run once per sublayer on the host's time, which for small
+# calls is most of theirs: shapes stay torch.Size, and each check is made once.
+_BF16, _F32, _F8, _U8 = torch.bfloat16, torch.float32, torch.float8_e4m3fn, torch.uint8
+
 
 def _sized(t, name, count, dtype, dev):
     _need(t, name, dtype, dev)
     if t.numel() != count:
         raise ValueError("%s must hold %d values, got %d" % (name, count, t.numel()))
+    return t.data_ptr()
+
+
+def _made(t, name, shape, dtype, dev, stream):
+    """An output: the caller's, checked, or a new one.  A tensor made here for a
+    stream other than the current one is not handed out again by the allocator
+    before that stream is done with it."""
+    if t is None:
+        t = torch.empty(shape, dtype=dtype, device=dev)
+        if stream is not None:
+            t.record_stream(stream)
+        return t
+    _need(t, name, dtype, dev)
+    if t.shape != shape:
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
     return t
-
-
-def _grad_out(t, name, shape, dtype, dev, stream):
-    """_out; a tensor made here for a stream other than the current one is not
-    handed out again by the allocator before that stream is done with it."""
-    made = t is None
-    t = _out(t, name, shape, dtype, dev)
-    if made and stream is not None:
-        t.record_stream(stream)
-    return t
-
-
-def _scale_shape(shape):
-    return tuple(shape[:-1]) + (-(-int(shape[-1]) // KEPT_BLOCK),)
 
 
 def _kept(t, name, shape, dev):
-    """A kept tensor of `shape`: bf16, or (codes, scales).  Returns the data
-    and the scales or None."""
+    """A kept tensor of `shape`, bf16 or (codes, scales): the pointers to its
+    data and to its scales (None)."""
     if isinstance(t, torch.Tensor):
-        _need(t, name, torch.bfloat16, dev)
-        if tuple(t.shape) != tuple(shape):
+        _need(t, name, _BF16, dev)
+        if t.shape != shape:
             raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
-        return t, None
+        return t.data_ptr(), None
     if not isinstance(t, (tuple, list)) or len(t) != 2:
         raise TypeError("%s must be a bf16 tensor or (codes, scales)" % name)
     codes, scales = t
-    for x, what, dtype, want in ((codes, "codes", torch.float8_e4m3fn, tuple(shape)),
-                                 (scales, "scales", torch.uint8, _scale_shape(shape))):
-        _need(x, "%s %s" % (name, what), dtype, dev)
-        if tuple(x.shape) != want:
-            raise ValueError("%s %s must have shape %s, got %s" % (name, what, want,
-                                                                   tuple(x.shape)))
-    return codes, scales
+    _need(codes, name + " codes", _F8, dev)
+    _need(scales, name + " scales", _U8, dev)
+    if codes.shape != shape:
+        raise ValueError("%s codes must have shape %s, got %s" % (name, tuple(shape),
+                                                                  tuple(codes.shape)))
+    if scales.shape != shape[:-1] + ((shape[-1] + KEPT_BLOCK - 1) // KEPT_BLOCK,):
+        raise ValueError("%s scales must have shape %s, got %s" % (
+            name, tuple(shape[:-1]) + (-(-shape[-1] // KEPT_BLOCK),), tuple(scales.shape)))
+    return codes.data_ptr(), scales.data_ptr()
 
 
-def _rows(t):
-    if t.dim() < 1:
+def _rows_of(t):
+    shape = t.shape
+    if len(shape) < 1:
         raise ValueError("a row of channels at least is needed")
-    d = int(t.shape[-1])
+    d = shape[-1]
     n = 1
-    for s in t.shape[:-1]:
-        n *= int(s)
-    return n, d
+    for s in shape[:-1]:
+        n *= s
+    return shape, n, d
+
+
+def _tokens_of(t):
+    shape = t.shape
+    if len(shape) < 2:
+        raise ValueError("a stream must be [..., hc, d]")
+    n = 1
+    for s in shape[:-2]:
+        n *= s
+    return shape, n, shape[-2], shape[-1]
+
+
+_get_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _run(name, dev, stream, *args):
+    """The C entry point `name` on dev's current (or the given) stream."""
+    fn = getattr(_lib if _lib is not None else lib(), name)
+    if stream is not None:
+        raw = stream.cuda_stream
+    elif _raw_stream is not None:
+        raw = _raw_stream(dev.index)
+    else:
+        raw = torch.cuda.current_stream(dev).cuda_stream
+    status = fn(*args, raw) if _get_device() == dev.index else _call(dev, fn, *args, raw)
+    if status != HC_OK:
+        raise HcError(status, name)
 
 
 def hc_checkpoint(x, codes=None, scales=None, stream=None):
     """x [..., d] bf16 -> codes [..., d] float8_e4m3fn, scales [..., ceil(d / 32)]
     uint8: a channel's value is code * 2^(scale - 127)."""
-    _need(x, "x", torch.bfloat16)
+    _need(x, "x", _BF16)
     dev = x.device
-    n, d = _rows(x)
-    codes = _grad_out(codes, "codes", tuple(x.shape), torch.float8_e4m3fn, dev, stream)
-    scales = _grad_out(scales, "scales", _scale_shape(x.shape), torch.uint8, dev, stream)
-    _check(_call(dev, lib().hc_checkpoint, n, d, _ptr(x), _ptr(codes), _ptr(scales),
-                 _stream(dev, stream)), "hc_checkpoint")
+    shape, n, d = _rows_of(x)
+    codes = _made(codes, "codes", shape, _F8, dev, stream)
+    scales = _made(scales, "scales", shape[:-1] + ((d + KEPT_BLOCK - 1) // KEPT_BLOCK,), _U8, dev,
+                   stream)
+    _run("hc_checkpoint", dev, stream, n, d, x.data_ptr(), codes.data_ptr(), scales.data_ptr())
     return codes, scales
 
 
 def hc_restore(codes, scales, x=None, stream=None):
     """codes [..., d], scales [..., ceil(d / 32)] of hc_checkpoint -> x [..., d] bf16."""
-    _need(codes, "codes", torch.float8_e4m3fn)
+    _need(codes, "codes", _F8)
     dev = codes.device
-    n, d = _rows(codes)
-    _kept((codes, scales), "x", tuple(codes.shape), dev)
-    x = _grad_out(x, "x", tuple(codes.shape), torch.bfloat16, dev, stream)
-    _check(_call(dev, lib().hc_restore, n, d, _ptr(codes), _ptr(scales), _ptr(x),
-                 _stream(dev, stream)), "hc_restore")
+    shape, n, d = _rows_of(codes)
+    cp, sp = _kept((codes, scales), "x", shape, dev)
+    x = _made(x, "x", shape, _BF16, dev, stream)
+    _run("hc_restore", dev, stream, n, d, cp, sp, x.data_ptr())
     return x
 
 
 def hc_pre_restore(codes, scales, pre, y=None, stream=None):
     """hc_pre of a kept stream: codes [..., hc, d], scales, pre [..., hc] -> y [..., d] bf16."""
-    _need(codes, "codes", torch.float8_e4m3fn)
+    _need(codes, "codes", _F8)
     dev = codes.device
-    lead, n, hc, d = _stream_dims(codes)
-    _kept((codes, scales), "x", tuple(codes.shape), dev)
-    _sized(pre, "pre", n * hc, torch.float32, dev)
-    y = _grad_out(y, "y", lead + (d,), torch.bfloat16, dev, stream)
-    _check(_call(dev, lib().hc_pre_restore, n, hc, d, _ptr(codes), _ptr(scales), _ptr(pre),
-                 _ptr(y), _stream(dev, stream)), "hc_pre_restore")
+    shape, n, hc, d = _tokens_of(codes)
+    cp, sp = _kept((codes, scales), "x", shape, dev)
+    pp = _sized(pre, "pre", n * hc, _F32, dev)
+    y = _made(y, "y", shape[:-2] + (d,), _BF16, dev, stream)
+    _run("hc_pre_restore", dev, stream, n, hc, d, cp, sp, pp, y.data_ptr())
     return y
 
 
 def hc_post_checkpoint(out, residual, post, comb, y=None, codes=None, scales=None, stream=None):
     """hc_post that also keeps the new stream in 8 bits (y may be residual itself).
     Returns (y, codes, scales)."""
-    _need(residual, "residual", torch.bfloat16)
+    _need(residual, "residual", _BF16)
     dev = residual.device
-    lead, n, hc, d = _stream_dims(residual)
-    _sized(out, "out", n * d, torch.bfloat16, dev)
-    _sized(post, "post", n * hc, torch.float32, dev)
-    _sized(comb, "comb", n * hc * hc, torch.float32, dev)
-    shape = lead + (hc, d)
-    y = _grad_out(y, "y", shape, torch.bfloat16, dev, stream)
-    codes = _grad_out(codes, "codes", shape, torch.float8_e4m3fn, dev, stream)
-    scales = _grad_out(scales, "scales", _scale_shape(shape), torch.uint8, dev, stream)
-    _check(_call(dev, lib().hc_post_checkpoint, n, hc, d, _ptr(out), _ptr(residual), _ptr(post),
-                 _ptr(comb), _ptr(y), _ptr(codes), _ptr(scales), _stream(dev, stream)),
-           "hc_post_checkpoint")
+    shape, n, hc, d = _tokens_of(residual)
+    op = _sized(out, "out", n * d, _BF16, dev)
+    pp = _sized(post, "post", n * hc, _F32, dev)
+    cb = _sized(comb, "comb", n * hc * hc, _F32, dev)
+    y = _made(y, "y", shape, _BF16, dev, stream)
+    codes = _made(codes, "codes", shape, _F8, dev, stream)
+    scales = _made(scales, "scales", shape[:-1] + ((d + KEPT_BLOCK - 1) // KEPT_BLOCK,), _U8, dev,
+                   stream)
+    _run("hc_post_checkpoint", dev, stream, n, hc, d, op, residual.data_ptr(), pp, cb,
+         y.data_ptr(), codes.data_ptr(), scales.data_ptr())
     return y, codes, scales
 
 
@@ -465,21 +497,22 @@ def hc_post_backward(dy, out, residual, post, comb, want_dresidual: bool = False
     """Gradients of hc_post from dy [..., hc, d] bf16.  out [..., d] and residual
     [..., hc, d] are bf16 tensors or (codes, scales) of hc_checkpoint.
     Returns (dout, dpost, dcomb, dresidual-or-None); dresidual may be dy itself."""
-    _need(dy, "dy", torch.bfloat16)
+    _need(dy, "dy", _BF16)
     dev = dy.device
-    lead, n, hc, d = _stream_dims(dy)
-    od, osc = _kept(out, "out", lead + (d,), dev)
-    rd, rsc = _kept(residual, "residual", lead + (hc, d), dev)
-    _sized(post, "post", n * hc, torch.float32, dev)
-    _sized(comb, "comb", n * hc * hc, torch.float32, dev)
-    dout = _grad_out(dout, "dout", lead + (d,), torch.bfloat16, dev, stream)
-    dpost = _grad_out(dpost, "dpost", lead + (hc,), torch.float32, dev, stream)
-    dcomb = _grad_out(dcomb, "dcomb", lead + (hc, hc), torch.float32, dev, stream)
+    shape, n, hc, d = _tokens_of(dy)
+    lead = shape[:-2]
+    op, osp = _kept(out, "out", lead + (d,), dev)
+    rp, rsp = _kept(residual, "residual", shape, dev)
+    pp = _sized(post, "post", n * hc, _F32, dev)
+    cb = _sized(comb, "comb", n * hc * hc, _F32, dev)
+    dout = _made(dout, "dout", lead + (d,), _BF16, dev, stream)
+    dpost = _made(dpost, "dpost", lead + (hc,), _F32, dev, stream)
+    dcomb = _made(dcomb, "dcomb", lead + (hc, hc), _F32, dev, stream)
     if want_dresidual or dresidual is not None:
-        dresidual = _grad_out(dresidual, "dresidual", lead + (hc, d), torch.bfloat16, dev, stream)
-    _check(_call(dev, lib().hc_post_backward, n, hc, d, _ptr(dy), _ptr(od), _ptr(osc), _ptr(rd),
-                 _ptr(rsc), _ptr(post), _ptr(comb), _ptr(dout), _ptr(dpost), _ptr(dcomb),
-                 _ptr(dresidual), _stream(dev, stream)), "hc_post_backward")
+        dresidual = _made(dresidual, "dresidual", shape, _BF16, dev, stream)
+    _run("hc_post_backward", dev, stream, n, hc, d, dy.data_ptr(), op, osp, rp, rsp, pp, cb,
+         dout.data_ptr(), dpost.data_ptr(), dcomb.data_ptr(),
+         None if dresidual is None else dresidual.data_ptr())
     return dout, dpost, dcomb, dresidual
 
 
@@ -497,36 +530,36 @@ def hc_mixes_pre_backward(dy, x, mixes, w_mix, hc_scale, hc_base, dpost, dcomb, 
     stream that hc_post carried past the sublayer.  x [..., hc, d] is a bf16 tensor or
     (codes, scales); mixes is what hc_mixes_pre returned.
     Returns (dx, dw_mix, dscale, dbase); dx may be dstream itself."""
-    _need(dy, "dy", torch.bfloat16)
+    _need(dy, "dy", _BF16)
     dev = dy.device
-    data = x if isinstance(x, torch.Tensor) else x[0] if isinstance(x, (tuple, list)) and x else x
+    data = x[0] if isinstance(x, (tuple, list)) and x else x
     if not isinstance(data, torch.Tensor):
         raise TypeError("x must be a bf16 tensor or (codes, scales)")
-    lead, n, hc, d = _stream_dims(data)
-    xd, xsc = _kept(x, "x", lead + (hc, d), dev)
-    mix = (2 + hc) * hc
-    if tuple(dy.shape) != lead + (d,):
-        raise ValueError("dy must have shape %s, got %s" % (lead + (d,), tuple(dy.shape)))
-    _sized(mixes, "mixes", n * mix, torch.float32, dev)
-    _sized(w_mix, "w_mix", mix * hc * d, torch.float32, dev)
-    _sized(hc_scale, "hc_scale", 3, torch.float32, dev)
-    _sized(hc_base, "hc_base", mix, torch.float32, dev)
-    _sized(dpost, "dpost", n * hc, torch.float32, dev)
-    _sized(dcomb, "dcomb", n * hc * hc, torch.float32, dev)
-    if dstream is not None:
-        _sized(dstream, "dstream", n * hc * d, torch.bfloat16, dev)
-    dx = _grad_out(dx, "dx", lead + (hc, d), torch.bfloat16, dev, stream)
-    dw_mix = _grad_out(dw_mix, "dw_mix", (mix, hc * d), torch.float32, dev, stream)
-    dscale = _grad_out(dscale, "dscale", (3,), torch.float32, dev, stream)
-    dbase = _grad_out(dbase, "dbase", (mix,), torch.float32, dev, stream)
-    wbytes = hc_mixes_pre_backward_bytes(n, hc, d)
-    workspace = _grad_out(workspace, "workspace", (wbytes,), torch.uint8, dev, stream) \
-        if workspace is None else _need(workspace, "workspace", torch.uint8, dev)
-    _check(_call(dev, lib().hc_mixes_pre_backward, n, hc, d, int(sinkhorn_iters), float(eps),
-                 float(norm_eps), _ptr(dy), _ptr(xd), _ptr(xsc), _ptr(mixes), _ptr(w_mix),
-                 _ptr(hc_scale), _ptr(hc_base), _ptr(dpost), _ptr(dcomb), _ptr(dstream), _ptr(dx),
-                 _ptr(dw_mix), _ptr(dscale), _ptr(dbase), _ptr(workspace), workspace.numel(),
-                 _stream(dev, stream)), "hc_mixes_pre_backward")
+    shape, n, hc, d = _tokens_of(data)
+    xp, xsp = _kept(x, "x", shape, dev)
+    mix, F = (2 + hc) * hc, hc * d
+    if dy.shape != shape[:-2] + (d,):
+        raise ValueError("dy must have shape %s, got %s" % (tuple(shape[:-2]) + (d,),
+                                                            tuple(dy.shape)))
+    mp = _sized(mixes, "mixes", n * mix, _F32, dev)
+    wp = _sized(w_mix, "w_mix", mix * F, _F32, dev)
+    sp = _sized(hc_scale, "hc_scale", 3, _F32, dev)
+    bp = _sized(hc_base, "hc_base", mix, _F32, dev)
+    pp = _sized(dpost, "dpost", n * hc, _F32, dev)
+    cp = _sized(dcomb, "dcomb", n * hc * hc, _F32, dev)
+    gp = None if dstream is None else _sized(dstream, "dstream", n * F, _BF16, dev)
+    dx = _made(dx, "dx", shape, _BF16, dev, stream)
+    dw_mix = _made(dw_mix, "dw_mix", (mix, F), _F32, dev, stream)
+    dscale = _made(dscale, "dscale", (3,), _F32, dev, stream)
+    dbase = _made(dbase, "dbase", (mix,), _F32, dev, stream)
+    if workspace is None:
+        workspace = _made(None, "workspace", (hc_mixes_pre_backward_bytes(n, hc, d),), _U8, dev,
+                          stream)
+    else:
+        _need(workspace, "workspace", _U8, dev)
+    _run("hc_mixes_pre_backward", dev, stream, n, hc, d, sinkhorn_iters, eps, norm_eps,
+         dy.data_ptr(), xp, xsp, mp, wp, sp, bp, pp, cp, gp, dx.data_ptr(), dw_mix.data_ptr(),
+         dscale.data_ptr(), dbase.data_ptr(), workspace.data_ptr(), workspace.numel())
     return dx, dw_mix, dscale, dbase
 
 

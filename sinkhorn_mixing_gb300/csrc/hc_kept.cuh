@@ -122,6 +122,12 @@ struct KeptVec {  // 8 channels as loaded
     }
     __device__ __forceinline__ void zero() { v = make_uint4(0, 0, 0, 0); }
     __device__ __forceinline__ void values(float f[8]) const { unpack8(v, f); }
+    // the channels in pairs and unscaled; returns their scale
+    __device__ __forceinline__ float pairs(uint64_t f[4]) const {
+        f[0] = bf16x2_to_f32x2(v.x), f[1] = bf16x2_to_f32x2(v.y);
+        f[2] = bf16x2_to_f32x2(v.z), f[3] = bf16x2_to_f32x2(v.w);
+        return 1.0f;
+    }
 };
 
 template <>
@@ -139,6 +145,13 @@ struct KeptVec<true> {
         e4m3x8_to_float(c, f);
 #pragma unroll
         for (int e = 0; e < 8; ++e) f[e] *= s;
+    }
+    __device__ __forceinline__ float pairs(uint64_t f[4]) const {
+        float u[8];
+        e4m3x8_to_float(c, u);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) f[e] = pack2(u[2 * e], u[2 * e + 1]);
+        return kept_scale(b);
     }
 };
 

@@ -41,8 +41,7 @@ __global__ void __launch_bounds__(256 + 32 * mix_warps<HC>(), 3)
                    float norm_eps, float features, const uint4 *__restrict__ dy, Kept x,
                    const float *__restrict__ mixes, const float *__restrict__ scale,
                    const float *__restrict__ base, const float *__restrict__ dpost,
-                   const float *__restrict__ dcomb, float *__restrict__ cf,
-                   uint16_t *__restrict__ du16, uint16_t *__restrict__ du3,
+                   const float *__restrict__ dcomb, uint8_t *__restrict__ rec,
                    float *__restrict__ partial) {
     using CF = Coef<HC>;
     constexpr int MIX = CF::kMix, MW = mix_warps<HC>(), THREADS = 256 + 32 * MW;
@@ -68,16 +67,21 @@ __global__ void __launch_bounds__(256 + 32 * mix_warps<HC>(), 3)
                     KeptVec<K8> xv[HC];
 #pragma unroll
                     for (int j = 0; j < HC; ++j) xv[j].load(x, t * HC + j, nv, nblk, v);
-                    float yf[8], f[8];
-                    unpack8(yv, yf);
+                    const uint64_t y2[4] = {bf16x2_to_f32x2(yv.x), bf16x2_to_f32x2(yv.y),
+                                            bf16x2_to_f32x2(yv.z), bf16x2_to_f32x2(yv.w)};
 #pragma unroll
                     for (int j = 0; j < HC; ++j) {
-                        xv[j].values(f);
+                        // a vector lies in one block: its scale comes after its sums
+                        uint64_t f[4];
+                        const float sc = xv[j].pairs(f);
+                        uint64_t dot = fmul2(f[0], y2[0]), sq = fmul2(f[0], f[0]);
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            acc[j] = fmaf(f[e], yf[e], acc[j]);
-                            acc[HC] = fmaf(f[e], f[e], acc[HC]);
+                        for (int e = 1; e < 4; ++e) {
+                            ffma2(dot, f[e], y2[e]);
+                            ffma2(sq, f[e], f[e]);
                         }
+                        acc[j] = K8 ? fmaf(sc, sum2(dot), acc[j]) : acc[j] + sum2(dot);
+                        acc[HC] = K8 ? fmaf(sc * sc, sum2(sq), acc[HC]) : acc[HC] + sum2(sq);
                     }
                 }
             }
@@ -165,10 +169,11 @@ __global__ void __launch_bounds__(256 + 32 * mix_warps<HC>(), 3)
             }
         }
         __syncwarp();
-        float *ct = cf + t * CF::kCf;
+        uint8_t *rt = rec + t * CF::kBytes;
+        float2 *ct = reinterpret_cast<float2 *>(rt);
         if (valid) {
 #pragma unroll
-            for (int k = 0; k < HC; ++k) ct[k * HC + j] = C[k];
+            for (int k = 0; k < HC; ++k) ct[k * HC + j] = make_float2(C[k], C[k]);
         }
         // backward through the steps
         for (int i = steps - 1; i >= 0; --i) {
@@ -240,12 +245,13 @@ __global__ void __launch_bounds__(256 + 32 * mix_warps<HC>(), 3)
         const int ex = min(max((int)(__float_as_uint(top) >> 23), 14), 253);
         const float up = __uint_as_float((uint32_t)(267 - ex) << 23);
         if (valid) {
-            ct[CF::kPre + j] = pre;
-            if (j < 4)
-                ct[CF::kQ + j] = j == 0   ? -dot_m * r2 / features
-                                 : j == 1 ? __uint_as_float((uint32_t)(ex - 13) << 23)
-                                          : 0.0f;
-            uint16_t *h16 = du16 + t * CF::kK, *h3 = du3 + t * CF::kParts;
+            ct[CF::kPre + j] = make_float2(pre, pre);
+            if (j < 2) {
+                const float v = j == 0 ? -dot_m * r2 / features
+                                       : __uint_as_float((uint32_t)(ex - 13) << 23);
+                ct[CF::kQ + j] = make_float2(v, v);
+            }
+            uint16_t *h16 = reinterpret_cast<uint16_t *>(rt + CF::kPairBytes), *h3 = h16 + CF::kK;
             auto put = [&](int i, float v) {
                 h16[i] = __half_as_ushort(__float2half_rn(v * up));
 #pragma unroll
@@ -329,16 +335,14 @@ size_t up256(size_t b) { return (b + 255) / 256 * 256; }
 
 // The workspace's parts, in this order.
 struct Parts {
-    size_t cf, du16, du3, mix, dw, end;
+    size_t rec, mix, dw, end;
 };
 template <int HC>
 Parts parts(int64_t n, int64_t d) {
     using CF = Coef<HC>;
     Parts p;
-    p.cf = 0;
-    p.du16 = p.cf + up256((size_t)n * CF::kCf * 4);
-    p.du3 = p.du16 + up256((size_t)n * CF::kK * 2);
-    p.mix = p.du3 + up256((size_t)n * CF::kParts * 2);
+    p.rec = 0;
+    p.mix = up256((size_t)n * CF::kBytes);
     p.dw = p.mix + up256((size_t)kMaxBlocks * mix_warps<HC>() * (CF::kMix + 4) * 4);
     // a block crosses into another slice at most once per slice
     const Split sp = Split::of(n, HC, d, Split::kMaxBlocks);
@@ -352,9 +356,7 @@ cudaError_t launch(const PreBackward &p, const DeviceInfo &di, cudaStream_t s) {
     const int64_t nv = p.d / 8, nblk = kept_blocks(p.d), F = HC * p.d;
     const Parts at = parts<HC>(p.n, p.d);
     MainArgs m;
-    m.cf = reinterpret_cast<float *>(p.ws + at.cf);
-    m.du16 = reinterpret_cast<uint16_t *>(p.ws + at.du16);
-    m.du3 = reinterpret_cast<uint16_t *>(p.ws + at.du3);
+    m.rec = p.ws + at.rec;
     m.dwp = reinterpret_cast<float *>(p.ws + at.dw);
     float *mp = reinterpret_cast<float *>(p.ws + at.mix);
     int lg = 5;
@@ -372,7 +374,7 @@ cudaError_t launch(const PreBackward &p, const DeviceInfo &di, cudaStream_t s) {
     cudaError_t e = launch_overlapped(
         k_mix_backward<HC, K8>, dim3(blocks), dim3(256 + 32 * MW), smem, s, p.n, nv, nblk, lg,
         p.iters, p.eps, p.norm_eps, (float)F, reinterpret_cast<const uint4 *>(p.dy), p.x, p.mixes,
-        p.scale, p.base, p.dpost, p.dcomb, m.cf, m.du16, m.du3, mp);
+        p.scale, p.base, p.dpost, p.dcomb, m.rec, mp);
     if (e != cudaSuccess) return e;
     m.split = Split::of(p.n, HC, p.d, di.sms < Split::kMaxBlocks ? di.sms : Split::kMaxBlocks);
     e = launch_dx_dw(p, m, di, s);

@@ -6,9 +6,9 @@
 
 namespace hc {
 
-// What the first kernel leaves per token for the second.
-//   cf [kCf] float: comb transposed [k][j] (comb_jk of one k lie together),
-//     pre [HC], q, f, padding
+// What the first kernel leaves per token for the second, one record of bytes:
+//   coefficients, each twice in a row (two-wide FMAs take a pair): comb
+//     transposed [k][j] (comb_jk of one k lie together), pre [HC], q, f
 //   du16 [kK] fp16: du times a power of two 1/f of the token's own that puts
 //     its largest magnitude in [2^13, 2^14), zeros behind (2+HC) HC
 //   du3 [kParts] bf16: du = hi + mid + lo, three bf16 numbers (24 bits).
@@ -16,12 +16,15 @@ namespace hc {
 template <int HC>
 struct Coef {
     static constexpr int kMix = (2 + HC) * HC;
-    static constexpr int kPre = HC * HC, kQ = kPre + HC, kF = kQ + 1, kCf = kQ + 4;
+    static constexpr int kPre = HC * HC, kQ = kPre + HC, kF = kQ + 1;  // in pairs
     static constexpr int kK = (kMix + 15) / 16 * 16;
     static constexpr int kN = 80;                        // N of one product
     static constexpr int kProducts = HC == 4 ? 1 : 3;
     static constexpr int kParts = kN * kProducts;
-    static_assert(kCf % 4 == 0 && kK % 8 == 0 && kParts % 8 == 0, "rows of 16-byte pieces");
+    static constexpr int kPairBytes = (kF + 1) * 8, kKBytes = kK * 2, kPartBytes = kParts * 2;
+    static constexpr int kBytes = kPairBytes + kKBytes + kPartBytes;
+    static_assert(kPairBytes % 16 == 0 && kKBytes % 16 == 0 && kPartBytes % 16 == 0,
+                  "16-byte pieces");
     static_assert(HC == 4 ? 3 * kMix <= kN : kMix == kN, "three parts fit");
 };
 
@@ -66,8 +69,7 @@ struct Split {
 
 struct MainArgs {
     Split split;
-    float *cf;
-    uint16_t *du16, *du3;
+    uint8_t *rec;  // [n][Coef::kBytes]
     float *dwp;  // [blocks + slices][mix][hc * channels]
 };
 

@@ -17,6 +17,7 @@
 // tiles come through a two-stage ring of 16-byte asynchronous copies, the next
 // step's loads running under this one's arithmetic.
 #include <cuda_fp16.h>
+#include <type_traits>
 
 #include "hc_pre_bwd.h"
 #include "hc_ptx.cuh"
@@ -29,16 +30,17 @@ using namespace ptx;
 struct Args {
     Split split;
     int64_t n, d, nblk;
-    const uint16_t *dy;
+    const uint8_t *dy;      // bf16
     const uint8_t *x, *xs;  // bf16 rows or codes, scales
     const float *w;
-    const uint16_t *g;      // may be null
-    uint16_t *dx;
-    const float *cf;
-    const uint16_t *du16, *du3;
+    const uint8_t *g;       // bf16; may be null
+    uint8_t *dx;            // bf16
+    const uint8_t *rec;
     float *dwp;
     unsigned int *err;
 };
+
+constexpr int kDrain = 16;  // steps between moves of dW's running sums
 
 template <int HC, bool K8>
 struct Cfg {
@@ -48,18 +50,22 @@ struct Cfg {
     // a warp: 16 tokens, 16 channels, 4 copies; a lane of it 2 tokens, 4 channels
     static constexpr int MT = T / 16, GROUPS = CH / 16, JQ = HC / 4, WARPS = MT * GROUPS * JQ;
     static constexpr int THREADS = 32 * WARPS, MTILES = FT / 128;
+    static constexpr int PW = MTILES * 4 / WARPS;  // tiles of dW whose lanes a warp reads
+    static constexpr int SUMS = MTILES * CF::kN;   // TMEM columns of the drained sums
+    static_assert(SUMS + MTILES / PW * CF::kMix <= 512, "TMEM");
     // Row pitches: a token's row is moved on by as many bytes as the lanes of one token read at
     // once, so that the lanes of neighbouring tokens meet in no bank.
     static constexpr int GP = HC * CH * 2 + 32, YP = CH * 2 + 32, XP = HC * CH + 16;
-    static constexpr int CP = HC == 4 ? CF::kCf * 4 + 16 : CF::kCf * 4, AP = CF::kK * 2 + 16;
+    static constexpr int CP = CF::kPairBytes, AP = CF::kKBytes + 16;
     // x as the M operand: 8 channels x 8 tokens in 128 bytes (channels along 16 bytes), the
     // blocks of a channel group's tokens in a row
     static constexpr int OT = T / 8 * 128, OBYTES = FT / 8 * OT;
     static constexpr int BT = T / 8 * 128, BBYTES = CF::kParts / 8 * BT;
     // stage
     static constexpr int SG = 0, SY = SG + T * GP, SX = SY + T * YP;
-    static constexpr int SS = SX + (K8 ? T * XP : OBYTES);  // scales
-    static constexpr int SC = SS + (K8 ? T * HC * CH / 32 : 0), SA = SC + T * CP;
+    static constexpr int SS = SX + (K8 ? T * XP : OBYTES);  // scales, each twice
+    static constexpr int SCALES = T * HC * CH / 32;
+    static constexpr int SC = SS + (K8 ? SCALES * 8 : 0), SA = SC + T * CP;
     static constexpr int STAGE = (SA + T * AP + 127) / 128 * 128;
     // the block's memory
     static constexpr int BRING = K8 ? 3 : 2;
@@ -71,17 +77,16 @@ struct Cfg {
     static constexpr uint32_t IDESC = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 15) | (1u << 16) |
                                       ((uint32_t)(CF::kN >> 3) << 17) | (8u << 24);
     static_assert(SMEM <= 232448, "shared memory");
-    static_assert(T * HC * CH / 32 <= THREADS, "a scale byte per thread");
+    static_assert(SCALES <= THREADS, "a scale byte per thread");
 };
 
-__device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool in) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-                 "r"(in ? 16 : 0)
+// Asynchronous copies of 16 (8) bytes of which `bytes` are read, zeros behind.
+__device__ __forceinline__ void cp16(uint32_t dst, const uint8_t *src, uint32_t bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
                  : "memory");
 }
-__device__ __forceinline__ void cp8(uint32_t dst, const void *src, bool in) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src),
-                 "r"(in ? 8 : 0)
+__device__ __forceinline__ void cp8(uint32_t dst, const uint8_t *src, uint32_t bytes) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes)
                  : "memory");
 }
 __device__ __forceinline__ void cp_wait_all() {
@@ -97,21 +102,58 @@ __device__ __forceinline__ uint32_t lds32(uint32_t a) {
     asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
     return v;
 }
-__device__ __forceinline__ float4 lds_f4(uint32_t a) {
-    const uint4 v = lds128(a);
-    return make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z),
-                       __uint_as_float(v.w));
-}
 __device__ __forceinline__ void sts64(uint32_t a, uint32_t x, uint32_t y) {
     asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(a), "r"(x), "r"(y) : "memory");
 }
+// c = a b (first) or c += a b
+template <bool FIRST>
 __device__ __forceinline__ void mma_f16(float c[4], const uint32_t a[4], uint32_t b0,
                                         uint32_t b1) {
+    if (FIRST)
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+            "{%8, %9}, {%10, %10, %10, %10};"
+            : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
+    else
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+            "{%8, %9}, {%0, %1, %2, %3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const float v[8]) {
     asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-        "{%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+        "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+        "r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])),
+        "r"(__float_as_uint(v[3])), "r"(__float_as_uint(v[4])), "r"(__float_as_uint(v[5])),
+        "r"(__float_as_uint(v[6])), "r"(__float_as_uint(v[7]))
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() {
+    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+// the values of loads that have been waited for, not to be used before
+template <int N>
+__device__ __forceinline__ void arrived(float v[N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) asm volatile("" : "+f"(v[i]));
+}
+__device__ __forceinline__ void lds_pairs(uint32_t a, uint64_t &x, uint64_t &y) {
+    asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(x), "=l"(y) : "r"(a));
+}
+__device__ __forceinline__ uint32_t pack_pair(uint64_t v) {
+    float lo, hi;
+    unpack2(v, lo, hi);
+    return pack_bf16x2(lo, hi);
+}
+// a streaming store where `in` is not 0, without a branch around it
+__device__ __forceinline__ void stg64_if(uint8_t *p, uint32_t x, uint32_t y, uint32_t in) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %3, 0;\n\t@p st.global.cs.v2.u32 [%0], {%1, %2};\n\t}" ::"l"(
+            p),
+        "r"(x), "r"(y), "r"(in)
+        : "memory");
 }
 // Shared-memory matrix descriptor without swizzle, the M or N axis along the
 // 16-byte rows of 8 x 8 blocks: `mn` bytes to the next 8 of that axis, `k` to
@@ -189,6 +231,7 @@ __global__ void __launch_bounds__(Cfg<HC, K8>::THREADS, 1) k_dx_dw(Args a) {
         const int ex = min(max((int)(__float_as_uint(top) >> 23), 14), 253);
         const float wup = __uint_as_float((uint32_t)(267 - ex) << 23);
         const float wdown = __uint_as_float((uint32_t)(ex - 13) << 23);
+        const uint64_t wdown2 = pack2(wdown, wdown);
         for (int q = tid; q < CF::kK * C::FT; q += C::THREADS) {
             const int i = q / C::FT, m = q % C::FT, j = m / C::CH, c = m % C::CH;
             float v = 0.0f;
@@ -206,76 +249,107 @@ __global__ void __launch_bounds__(Cfg<HC, K8>::THREADS, 1) k_dx_dw(Args a) {
             started = true;
         }
 
-        // ---- loads of one step's tiles
-        auto load = [&](int64_t s, int64_t rel) {
+        // ---- loads of one step's tiles.  A thread's pieces of 16 bytes lie at one column of
+        // every GT-th row (YT-th, XT-th), so a pointer per tensor walks over them, and the columns
+        // past the slice's end read 0 bytes at column 0.
+        constexpr int GT = C::THREADS / (C::FT / 8), YT = C::THREADS / (C::CH / 8);
+        constexpr int XV = C::FT / 16, XT = C::THREADS / XV;
+        constexpr int RV = CF::kBytes / 16, R1 = CF::kPairBytes / 16, R2 = R1 + CF::kKBytes / 16;
+        constexpr int RN = (C::T * RV + C::THREADS - 1) / C::THREADS;
+        const int gt = tid / (C::FT / 8), gv = tid % (C::FT / 8);
+        const int gk = gv / (C::CH / 8), gc = gv % (C::CH / 8) * 8;
+        const int yt = tid / (C::CH / 8), yc = tid % (C::CH / 8) * 8;
+        const int xt = tid / XV, xv0 = tid % XV, xk = xv0 / (C::CH / 16), xc = xv0 % (C::CH / 16) * 16;
+        const uint32_t gsz = gc < width ? 16 : 0, ysz = yc < width ? 16 : 0;
+        const bool wide = K8 && a.d % 16 == 0;  // 16 codes are 16-byte aligned
+        const uint32_t xsz = !K8 ? gsz : wide ? (xc < width ? 16 : 0) : gsz / 2;
+        const int64_t gstep = GT * F * 2;
+        const int64_t gat = gt * F + (gsz ? gk * a.d + gc : 0) + ch0;
+        const uint8_t *gp = a.g + (s0 * C::T * F + gat) * 2;
+        const uint8_t *yp = a.dy + ((s0 * C::T + yt) * a.d + ch0 + (ysz ? yc : 0)) * 2;
+        const int64_t xstep = wide ? XT * F : K8 ? GT * F : gstep;
+        const uint8_t *xp = !K8    ? a.x + (s0 * C::T * F + gat) * 2
+                            : wide ? a.x + (s0 * C::T + xt) * F + (xsz ? xk * a.d + xc : 0) + ch0
+                                   : a.x + s0 * C::T * F + gat;
+        const uint8_t *rp = a.rec + s0 * C::T * CF::kBytes + tid * 16;
+        uint32_t rdst[RN];  // in the stage, or (from C::STAGE on) in the ring of du3
+#pragma unroll
+        for (int i = 0; i < RN; ++i) {
+            const int q = i * C::THREADS + tid, t = q / RV, v = q % RV;
+            rdst[i] = v < R1   ? C::SC + t * C::CP + v * 16
+                      : v < R2 ? C::SA + t * C::AP + (v - R1) * 16
+                               : C::STAGE + (v - R2) * C::BT + t / 8 * 128 + t % 8 * 16;
+        }
+        // `whole`: all C::T tokens exist, else the first `left`
+        auto load_rows = [&](int64_t s, int64_t rel, auto whole, int left) {
+            constexpr bool W = decltype(whole)::value;
             const uint32_t st = sb + (uint32_t)(s & 1) * C::STAGE;
-            const uint32_t bt = sb + C::OB + (uint32_t)(rel % C::BRING) * C::BBYTES;
-            const int64_t t0 = s * C::T;
-            const int left = (int)min((int64_t)C::T, a.n - t0);
-            auto rows = [&](int per, auto place) {
-                for (int q = tid; q < C::T * per; q += C::THREADS) place(q / per, q % per);
-            };
-            if (a.g != nullptr)
-                rows(C::FT / 8, [&](int t, int v) {
-                    const int k = v / (C::CH / 8), c = v % (C::CH / 8) * 8;
-                    const bool in = t < left && c < width;
-                    const uint16_t *src = a.g + (t0 + t) * F + k * a.d + ch0 + c;
-                    cp16(st + C::SG + t * C::GP + v * 16, in ? src : a.g, in);
-                });
-            rows(C::CH / 8, [&](int t, int v) {
-                const bool in = t < left && v * 8 < width;
-                const uint16_t *src = a.dy + (t0 + t) * a.d + ch0 + v * 8;
-                cp16(st + C::SY + t * C::YP + v * 16, in ? src : a.dy, in);
-            });
-            if (!K8) {
-                rows(C::FT / 8, [&](int t, int v) {
-                    const int j = v / (C::CH / 8), c = v % (C::CH / 8) * 8;
-                    const bool in = t < left && c < width;
-                    const uint8_t *src = a.x + ((t0 + t) * F + j * a.d + ch0 + c) * 2;
-                    cp16(st + C::SX + v * C::OT + t / 8 * 128 + t % 8 * 16, in ? src : a.x, in);
-                });
-            } else if (a.d % 16 == 0) {
-                rows(C::FT / 16, [&](int t, int v) {
-                    const int j = v / (C::CH / 16), c = v % (C::CH / 16) * 16;
-                    const bool in = t < left && c < width;
-                    const uint8_t *src = a.x + (t0 + t) * F + j * a.d + ch0 + c;
-                    cp16(st + C::SX + t * C::XP + v * 16, in ? src : a.x, in);
-                });
-            } else {
-                rows(C::FT / 8, [&](int t, int v) {
-                    const int j = v / (C::CH / 8), c = v % (C::CH / 8) * 8;
-                    const bool in = t < left && c < width;
-                    const uint8_t *src = a.x + (t0 + t) * F + j * a.d + ch0 + c;
-                    cp8(st + C::SX + t * C::XP + v * 8, in ? src : a.x, in);
-                });
+            const uint32_t bt =
+                sb + C::OB + (uint32_t)(rel % C::BRING) * C::BBYTES - C::STAGE;
+            if (a.g != nullptr) {
+                const uint8_t *p = gp;
+#pragma unroll
+                for (int i = 0; i < C::T / GT; ++i, p += gstep) {
+                    const bool in = W || gt + i * GT < left;
+                    cp16(st + C::SG + (gt + i * GT) * C::GP + gv * 16, in ? p : a.g, in ? gsz : 0);
+                }
             }
-            rows(CF::kCf / 4, [&](int t, int v) {
-                const bool in = t < left;
-                cp16(st + C::SC + t * C::CP + v * 16,
-                     in ? a.cf + (t0 + t) * CF::kCf + v * 4 : a.cf, in);
-            });
-            rows(CF::kK / 8, [&](int t, int v) {
-                const bool in = t < left;
-                cp16(st + C::SA + t * C::AP + v * 16,
-                     in ? a.du16 + (t0 + t) * CF::kK + v * 8 : a.du16, in);
-            });
-            rows(CF::kParts / 8, [&](int t, int v) {
-                const bool in = t < left;
-                cp16(bt + v * C::BT + t / 8 * 128 + t % 8 * 16,
-                     in ? a.du3 + (t0 + t) * CF::kParts + v * 8 : a.du3, in);
-            });
+            {
+                const uint8_t *p = xp;
+                const int n = wide ? C::T / XT : C::T / GT;
+#pragma unroll
+                for (int i = 0; i < C::T / GT; ++i, p += xstep) {
+                    if (i >= n) break;
+                    const int t = wide ? xt + i * XT : gt + i * GT;
+                    const bool in = W || t < left;
+                    const uint8_t *src = in ? p : a.x;
+                    const uint32_t sz = in ? xsz : 0;
+                    if (!K8)
+                        cp16(st + C::SX + gv * C::OT + t / 8 * 128 + t % 8 * 16, src, sz);
+                    else if (wide)
+                        cp16(st + C::SX + t * C::XP + xv0 * 16, src, sz);
+                    else
+                        cp8(st + C::SX + t * C::XP + gv * 8, src, sz);
+                }
+            }
+            static_assert(YT >= C::T, "one piece of dy a thread");
+            if (YT == C::T || yt < C::T) {
+                const bool in = W || yt < left;
+                cp16(st + C::SY + yt * C::YP + yc * 2, in ? yp : a.dy, in ? ysz : 0);
+            }
+#pragma unroll
+            for (int i = 0; i < RN; ++i) {
+                const int q = i * C::THREADS + tid;
+                const bool in = W || q / RV < left;
+                if (q < C::T * RV)
+                    cp16(rdst[i] + (rdst[i] < C::STAGE ? st : bt),
+                         in ? rp + i * C::THREADS * 16 : a.rec, in ? 16 : 0);
+            }
+            gp += C::T * F * 2, yp += C::T * a.d * 2, xp += C::T * F * (K8 ? 1 : 2);
+            rp += C::T * CF::kBytes;
         };
-        // the scale byte of (token, copy, block) = tid of step s
+        auto load = [&](int64_t s, int64_t rel) {  // steps in order
+            const int64_t left = a.n - s * C::T;
+            if (left >= C::T)
+                load_rows(s, rel, std::true_type(), C::T);
+            else
+                load_rows(s, rel, std::false_type(), (int)left);
+        };
+        // the scale byte of (token, block, copy) = tid of the next step
+        const int sct = tid / (HC * (C::CH / 32)), scb = tid / HC % (C::CH / 32), scj = tid % HC;
+        const bool sin = K8 && sct < C::T && scb * 32 < width;
+        const uint8_t *sp =
+            a.xs + ((s0 * C::T + (sin ? sct : 0)) * HC + scj) * a.nblk + ch0 / 32 + (sin ? scb : 0);
         auto load_scale = [&](int64_t s) -> uint32_t {
-            constexpr int B = C::CH / 32;
-            const int t = tid / (HC * B), j = tid / B % HC, b = tid % B;
-            const int64_t tok = s * C::T + t;
-            if (!K8 || t >= C::T || tok >= a.n || b * 32 >= width) return 0;
-            return __ldg(a.xs + (tok * HC + j) * a.nblk + ch0 / 32 + b);
+            uint32_t v = 0;
+            if (sin && s * C::T + sct < a.n) v = __ldg(sp);
+            sp += C::T * HC * a.nblk;
+            return v;
         };
         auto keep_scale = [&](int64_t s, uint32_t v) {
-            if (K8 && tid < C::T * HC * C::CH / 32)
-                smem[(s & 1) * C::STAGE + C::SS + tid] = (uint8_t)v;
+            const uint32_t f = __float_as_uint(kept_scale(v));
+            if (K8 && tid < C::SCALES)
+                sts64(sb + (uint32_t)(s & 1) * C::STAGE + C::SS + tid * 8, f, f);
         };
         // dW += du^T x of the step `rel` of this run: one thread issues
         auto issue = [&](int64_t s, int64_t rel) {
@@ -291,19 +365,77 @@ __global__ void __launch_bounds__(Cfg<HC, K8>::THREADS, 1) k_dx_dw(Args a) {
                         mma_bf16(tmem + m * CF::kN,
                                  mn_desc(xo + m * 16 * C::OT + ks * 256, 128, C::OT),
                                  mn_desc(bo + p * (CF::kN / 8) * C::BT + ks * 256, 128, C::BT),
-                                 C::IDESC, rel > 0 || ks > 0 || p > 0);
+                                 C::IDESC, rel % kDrain != 0 || ks > 0 || p > 0);
             mma_commit(bar);
         };
 
+        // The tensor core rounds its running sums toward zero, which over many steps adds up to
+        // more than binary32's own rounding.  So every kDrain steps the sums move on: into TMEM
+        // columns of their own, or (a warp's second tile at HC = 8) registers, added there with
+        // rounding to nearest; the products then start anew.  `out` takes the result instead.
+        float more[C::PW > 1 ? C::MIX : 1];
+        auto drain = [&](bool first, float *out) {
+#pragma unroll
+            for (int q = 0; q < C::PW; ++q) {
+                const int m = (warp >> 2) + q * (C::WARPS / 4);
+                const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);
+                const uint32_t ta = lanes + m * CF::kN, ts = lanes + C::SUMS + m * C::MIX;
+#pragma unroll
+                for (int c = 0; c < C::MIX; c += 8) {
+                    float v[8], u[8], w[8], sum[8];
+                    tmem_ld8(ta + c, v);
+                    if (CF::kProducts == 1) {
+                        tmem_ld8(ta + C::MIX + c, u);
+                        tmem_ld8(ta + 2 * C::MIX + c, w);
+                    }
+                    if (!first && q == 0) tmem_ld8(ts + c, sum);
+                    tmem_ld_wait();
+                    arrived<8>(v);
+                    if (CF::kProducts == 1) {
+                        arrived<8>(u);
+                        arrived<8>(w);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) v[e] += u[e] + w[e];
+                    }
+                    if (!first && q == 0) arrived<8>(sum);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        if (q > 0) sum[e] = more[c + e];
+                        if (!first) v[e] += sum[e];
+                        if (q > 0) more[c + e] = v[e];
+                    }
+                    if (out != nullptr) {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            out[(int64_t)(c + e) * C::FT + m * 128 + (warp & 3) * 32 + lane] = v[e];
+                    } else if (q == 0) {
+                        tmem_st8(ts + c, v);
+                    }
+                }
+            }
+            tmem_st_wait();
+        };
+
+        uint8_t *dxp =
+            a.dx + ((s0 * C::T + mt * 16 + tg) * F + jq * 4 * a.d + ch0 + (cl < width ? cl : 0)) * 2;
         load(s0, 0);
         keep_scale(s0, load_scale(s0));
         for (int64_t s = s0; s < s1; ++s) {
             const int64_t rel = s - s0;
+            const bool full = rel > 0 && rel % kDrain == 0;
             cp_wait_all();
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             tc_fence_before();
             __syncthreads();  // step s has landed; all are done with step s - 1
-            if (!K8 && rel > 0) products_done();  // of step s - 1, whose x is loaded over
+            if (!K8 && rel > 0) {
+                products_done();  // of step s - 1, whose x is loaded over
+                if (full) {
+                    tc_fence_after();
+                    drain(rel == kDrain, nullptr);
+                    tc_fence_before();
+                    __syncthreads();
+                }
+            }
             if (tid == 0 && (!K8 || rel > 0)) {
                 tc_fence_after();
                 issue(K8 ? s - 1 : s, K8 ? rel - 1 : rel);
@@ -318,12 +450,6 @@ __global__ void __launch_bounds__(Cfg<HC, K8>::THREADS, 1) k_dx_dw(Args a) {
             // ---- du W
             const uint32_t st = sb + (uint32_t)(s & 1) * C::STAGE;
             float acc[4][2][4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-#pragma unroll
-                for (int p = 0; p < 2; ++p)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) acc[j][p][e] = 0.0f;
             uint32_t af[C::KS][4];
 #pragma unroll
             for (int ks = 0; ks < C::KS; ++ks) {
@@ -342,88 +468,87 @@ __global__ void __launch_bounds__(Cfg<HC, K8>::THREADS, 1) k_dx_dw(Args a) {
                         ((((jq * 4 + j) * C::GROUPS + grp) * 2 + p) * 32 + lane) * C::WREG * 4;
                     if (C::KS == 2) {
                         const uint4 b = lds128(wa);
-                        mma_f16(acc[j][p], af[0], b.x, b.y);
-                        mma_f16(acc[j][p], af[C::KS - 1], b.z, b.w);
+                        mma_f16<true>(acc[j][p], af[0], b.x, b.y);
+                        mma_f16<false>(acc[j][p], af[C::KS - 1], b.z, b.w);
                     } else {
 #pragma unroll
                         for (int ks = 0; ks < C::KS; ++ks) {
                             const uint2 b = lds64(wa + ks * 8);
-                            mma_f16(acc[j][p], af[ks], b.x, b.y);
+                            if (ks == 0)
+                                mma_f16<true>(acc[j][p], af[ks], b.x, b.y);
+                            else
+                                mma_f16<false>(acc[j][p], af[ks], b.x, b.y);
                         }
                     }
                 }
 
-            // ---- the other terms, token by token
+            // ---- the other terms, token by token, two channels wide
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int t = mt * 16 + h * 8 + tg;
-                const int64_t tok = s * C::T + t;
-                const uint32_t cfa = st + C::SC + t * C::CP;
-                float v[4][4];
-                const float4 qf = lds_f4(cfa + CF::kQ * 4);  // q, f
-                const float f = qf.y * wdown;
+                const uint32_t cfa = st + C::SC + t * C::CP + jq * 32;
+                uint64_t v[4][2], qq, ff;
+                lds_pairs(st + C::SC + t * C::CP + CF::kQ * 8, qq, ff);
+                ff = fmul2(ff, wdown2);
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) v[j][e] = acc[j][e >> 1][2 * h + (e & 1)] * f;
+                    for (int p = 0; p < 2; ++p)
+                        v[j][p] = fmul2(pack2(acc[j][p][2 * h], acc[j][p][2 * h + 1]), ff);
+                auto add = [&](uint32_t coef, const uint2 &u) {  // v_j += coef_j u
+                    uint64_t c[4];
+                    lds_pairs(coef, c[0], c[1]);
+                    lds_pairs(coef + 16, c[2], c[3]);
+                    const uint64_t lo = bf16x2_to_f32x2(u.x), hi = bf16x2_to_f32x2(u.y);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        ffma2(v[j][0], c[j], lo);
+                        ffma2(v[j][1], c[j], hi);
+                    }
+                };
                 if (a.g != nullptr) {
 #pragma unroll
-                    for (int k = 0; k < HC; ++k) {
-                        const uint2 u = lds64(st + C::SG + t * C::GP + (k * C::CH + cl) * 2);
-                        const float4 c = lds_f4(cfa + (k * HC + jq * 4) * 4);
-                        const float gv[4] = {bf16lo(u.x), bf16hi(u.x), bf16lo(u.y), bf16hi(u.y)};
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            v[0][e] = fmaf(c.x, gv[e], v[0][e]);
-                            v[1][e] = fmaf(c.y, gv[e], v[1][e]);
-                            v[2][e] = fmaf(c.z, gv[e], v[2][e]);
-                            v[3][e] = fmaf(c.w, gv[e], v[3][e]);
-                        }
-                    }
+                    for (int k = 0; k < HC; ++k)
+                        add(cfa + k * HC * 8, lds64(st + C::SG + t * C::GP + (k * C::CH + cl) * 2));
                 }
-                {
-                    const uint2 u = lds64(st + C::SY + t * C::YP + cl * 2);
-                    const float4 c = lds_f4(cfa + (CF::kPre + jq * 4) * 4);
-                    const float yv[4] = {bf16lo(u.x), bf16hi(u.x), bf16lo(u.y), bf16hi(u.y)};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        v[0][e] = fmaf(c.x, yv[e], v[0][e]);
-                        v[1][e] = fmaf(c.y, yv[e], v[1][e]);
-                        v[2][e] = fmaf(c.z, yv[e], v[2][e]);
-                        v[3][e] = fmaf(c.w, yv[e], v[3][e]);
-                    }
-                }
+                add(cfa + CF::kPre * 8, lds64(st + C::SY + t * C::YP + cl * 2));
                 // x, last: its operand is free once the products of step s - 1 are done
                 if (K8 && h == 0) products_done();
-                const bool in = tok < a.n && cl < width;
+                const uint32_t in = cl < width && (s * C::T + t < a.n);
+                uint8_t *p = dxp + h * 16 * F;
+                uint64_t sc[4];
+                if (K8) {
+                    const uint32_t sa = st + C::SS + ((t * (C::CH / 32) + cl / 32) * HC + jq * 4) * 8;
+                    lds_pairs(sa, sc[0], sc[1]);
+                    lds_pairs(sa + 16, sc[2], sc[3]);
+                }
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
+                for (int j = 0; j < 4; ++j, p += a.d * 2) {
                     const int jj = jq * 4 + j;
                     const uint32_t oa = (jj * (C::CH / 8) + grp * 2 + (tl >> 1)) * C::OT + t / 8 * 128 +
                                         t % 8 * 16 + (tl & 1) * 8;
-                    float xv[4];
+                    uint64_t xv[2];
                     if (K8) {
-                        const uint32_t c8 = lds32(st + C::SX + t * C::XP + jj * C::CH + cl);
-                        const float sc = kept_scale(
-                            smem[(s & 1) * C::STAGE + C::SS + (t * HC + jj) * (C::CH / 32) + cl / 32]);
-                        e4m3x4_to_float(c8, xv);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) xv[e] *= sc;
-                        sts64(sb + C::OO + oa, pack_bf16x2(xv[0], xv[1]), pack_bf16x2(xv[2], xv[3]));
+                        float f[4];
+                        e4m3x4_to_float(lds32(st + C::SX + t * C::XP + jj * C::CH + cl), f);
+                        xv[0] = fmul2(pack2(f[0], f[1]), sc[j]);
+                        xv[1] = fmul2(pack2(f[2], f[3]), sc[j]);
+                        sts64(sb + C::OO + oa, pack_pair(xv[0]), pack_pair(xv[1]));
                     } else {
                         const uint2 u = lds64(st + C::SX + oa);
-                        xv[0] = bf16lo(u.x), xv[1] = bf16hi(u.x);
-                        xv[2] = bf16lo(u.y), xv[3] = bf16hi(u.y);
+                        xv[0] = bf16x2_to_f32x2(u.x), xv[1] = bf16x2_to_f32x2(u.y);
                     }
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) v[j][e] = fmaf(qf.x, xv[e], v[j][e]);
-                    if (in)
-                        __stcs(reinterpret_cast<uint2 *>(a.dx + tok * F + jj * a.d + ch0 + cl),
-                               make_uint2(pack_bf16x2(v[j][0], v[j][1]),
-                                          pack_bf16x2(v[j][2], v[j][3])));
+                    ffma2(v[j][0], qq, xv[0]);
+                    ffma2(v[j][1], qq, xv[1]);
+                    stg64_if(p, pack_pair(v[j][0]), pack_pair(v[j][1]), in);
                 }
             }
+            dxp += C::T * F * 2;
             if (s + 1 < s1) keep_scale(s + 1, next_scale);
+            if (K8 && full) {  // the products up to step s - 1 are done
+                tc_fence_after();
+                drain(rel == kDrain, nullptr);
+            }
         }
         if (K8) {  // the last step's products
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -437,24 +562,7 @@ __global__ void __launch_bounds__(Cfg<HC, K8>::THREADS, 1) k_dx_dw(Args a) {
         }
         products_done();
         tc_fence_after();
-
-        // ---- this run's dW: lanes are features, columns the mix numbers
-        float *out = a.dwp + (blockIdx.x + slice) * (int64_t)C::MIX * C::FT;
-        for (int m = warp >> 2; m < C::MTILES; m += C::WARPS / 4) {
-            const uint32_t ta = tmem + m * CF::kN + ((uint32_t)(warp & 3) << 21);
-            float *of = out + m * 128 + (warp & 3) * 32 + lane;
-            float v[CF::kN];
-#pragma unroll
-            for (int q = 0; q < CF::kN / 16; ++q) tmem_ld16(ta + q * 16, v + q * 16);
-            tmem_ld_wait();
-#pragma unroll
-            for (int i = 0; i < CF::kN; ++i) asm volatile("" : "+f"(v[i]));  // used after the wait
-#pragma unroll
-            for (int i = 0; i < C::MIX; ++i)
-                of[(int64_t)i * C::FT] =
-                    CF::kProducts == 1 ? v[i] + (v[(C::MIX + i) % CF::kN] + v[(2 * C::MIX + i) % CF::kN])
-                                       : v[i];
-        }
+        drain(s1 - s0 <= kDrain, a.dwp + (blockIdx.x + slice) * (int64_t)C::MIX * C::FT);
         tc_fence_before();
         __syncthreads();  // before W, the operands and the sums are written anew
         tc_fence_after();
@@ -475,8 +583,9 @@ cudaError_t launch(const PreBackward &p, const MainArgs &m, const DeviceInfo &di
     Args a;
     a.split = m.split;
     a.n = p.n, a.d = p.d, a.nblk = kept_blocks(p.d);
-    a.dy = p.dy, a.x = static_cast<const uint8_t *>(p.x.data), a.xs = p.x.scales, a.w = p.w;
-    a.g = p.dstream, a.dx = p.dx, a.cf = m.cf, a.du16 = m.du16, a.du3 = m.du3, a.dwp = m.dwp;
+    a.dy = reinterpret_cast<const uint8_t *>(p.dy), a.x = static_cast<const uint8_t *>(p.x.data), a.xs = p.x.scales, a.w = p.w;
+    a.g = reinterpret_cast<const uint8_t *>(p.dstream);
+    a.dx = reinterpret_cast<uint8_t *>(p.dx), a.rec = m.rec, a.dwp = m.dwp;
     a.err = di.err_word;
     return launch_overlapped(k_dx_dw<HC, K8>, dim3((unsigned)m.split.blocks), dim3(C::THREADS),
                              (size_t)C::SMEM, s, a);
