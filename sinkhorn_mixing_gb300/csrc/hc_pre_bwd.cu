@@ -35,14 +35,51 @@ __host__ __device__ constexpr int mix_warps() { return 8 * HC / 32; }
 // (HC numbers) in shared memory, and going back, the matrix before the step is
 // the one after it times them.  For C' = C / den, den = sum C + eps over the
 // row (or column):  dC = (dC' - sum dC' C') / den.
+// Where a token's record is (Coef): one after the other, or in tiles.
+template <int HC>
+struct Record {
+    using CF = Coef<HC>;
+    uint8_t *coef, *tile;
+    int r;  // row in the tile, or -1
+    __device__ __forceinline__ Record(uint8_t *rec, int64_t t, bool tiled) {
+        if (tiled) {
+            tile = rec + t / kTileTokens * CF::kTileBytes;
+            r = (int)(t % kTileTokens);
+            coef = tile + r * CF::kPairBytes;
+            tile += kTileTokens * CF::kPairBytes + r % 8 * 16;
+        } else {
+            coef = rec + t * CF::kBytes;
+            tile = coef + CF::kPairBytes;
+            r = -1;
+        }
+    }
+    __device__ __forceinline__ void put16(int i, uint16_t v) const {
+        if (r < 0) {
+            reinterpret_cast<uint16_t *>(tile)[i] = v;
+            return;
+        }
+        uint8_t *p = tile + (r / 8 * (CF::kK / 8) + i / 8) * 128 + i % 8 * 2;
+        *reinterpret_cast<uint16_t *>(p) = v;
+        *reinterpret_cast<uint16_t *>(p + kTileTokens * CF::kKBytes) = v;
+    }
+    __device__ __forceinline__ void put3(int i, uint16_t v) const {
+        if (r < 0) {
+            reinterpret_cast<uint16_t *>(tile + CF::kKBytes)[i] = v;
+            return;
+        }
+        *reinterpret_cast<uint16_t *>(tile + 2 * kTileTokens * CF::kKBytes +
+                                      (i / 8 * (kTileTokens / 8) + r / 8) * 128 + i % 8 * 2) = v;
+    }
+};
+
 template <int HC, bool K8>
 __global__ void __launch_bounds__(256 + 32 * mix_warps<HC>(), 3)
-    k_mix_backward(int64_t n, int64_t nv, int64_t nblk, int lg, int iters, float eps,
+    k_mix_backward(int64_t n, int64_t npad, int64_t nv, int64_t nblk, int lg, int iters, float eps,
                    float norm_eps, float features, const uint4 *__restrict__ dy, Kept x,
                    const float *__restrict__ mixes, const float *__restrict__ scale,
                    const float *__restrict__ base, const float *__restrict__ dpost,
                    const float *__restrict__ dcomb, uint8_t *__restrict__ rec,
-                   float *__restrict__ partial) {
+                   int tiled, float *__restrict__ partial) {
     using CF = Coef<HC>;
     constexpr int MIX = CF::kMix, MW = mix_warps<HC>(), THREADS = 256 + 32 * MW;
     __shared__ float sums[2][8][HC + 1];
@@ -50,7 +87,7 @@ __global__ void __launch_bounds__(256 + 32 * mix_warps<HC>(), 3)
     griddep_wait_then_release();
     const int tpb = 256 >> lg, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     auto meet = [] { asm volatile("bar.sync 1, %0;" ::"n"(THREADS) : "memory"); };
-    const int64_t groups = (n + tpb - 1) / tpb;
+    const int64_t groups = (npad + tpb - 1) / tpb;  // npad > n: records of zeros behind
 
     if (warp < 8) {
         const int lanes = 1 << lg, slot = threadIdx.x >> lg, l = threadIdx.x & (lanes - 1);
@@ -169,8 +206,9 @@ __global__ void __launch_bounds__(256 + 32 * mix_warps<HC>(), 3)
             }
         }
         __syncwarp();
-        uint8_t *rt = rec + t * CF::kBytes;
-        float2 *ct = reinterpret_cast<float2 *>(rt);
+        const bool pad = slot < tpb && !valid && grp * tpb + slot < npad;
+        const Record<HC> to(rec, pad ? grp * tpb + slot : t, tiled != 0);
+        float2 *ct = reinterpret_cast<float2 *>(to.coef);
         if (valid) {
 #pragma unroll
             for (int k = 0; k < HC; ++k) ct[k * HC + j] = make_float2(C[k], C[k]);
@@ -251,13 +289,12 @@ __global__ void __launch_bounds__(256 + 32 * mix_warps<HC>(), 3)
                                        : __uint_as_float((uint32_t)(ex - 13) << 23);
                 ct[CF::kQ + j] = make_float2(v, v);
             }
-            uint16_t *h16 = reinterpret_cast<uint16_t *>(rt + CF::kPairBytes), *h3 = h16 + CF::kK;
             auto put = [&](int i, float v) {
-                h16[i] = __half_as_ushort(__float2half_rn(v * up));
+                to.put16(i, __half_as_ushort(__float2half_rn(v * up)));
 #pragma unroll
                 for (int p = 0; p < 3; ++p) {
                     const __nv_bfloat16 b = __float2bfloat16_rn(v);
-                    h3[p * MIX + i] = __bfloat16_as_ushort(b);
+                    to.put3(p * MIX + i, __bfloat16_as_ushort(b));
                     v -= __bfloat162float(b);
                 }
             };
@@ -265,12 +302,16 @@ __global__ void __launch_bounds__(256 + 32 * mix_warps<HC>(), 3)
             put(HC + j, du1);
 #pragma unroll
             for (int k = 0; k < HC; ++k) put(2 * HC + j * HC + k, du2[k]);
-            for (int i = MIX + j; i < CF::kK; i += HC) h16[i] = 0;
-            for (int i = 3 * MIX + j; i < CF::kParts; i += HC) h3[i] = 0;
+            for (int i = MIX + j; i < CF::kK; i += HC) to.put16(i, 0);
+            for (int i = 3 * MIX + j; i < CF::kParts; i += HC) to.put3(i, 0);
             db0 += dz0, db1 += dz1;
 #pragma unroll
             for (int k = 0; k < HC; ++k) db2[k] += G[k];
             ds0 = fmaf(dz0, m0, ds0), ds1 = fmaf(dz1, m1, ds1), ds2 += c2;
+        } else if (pad) {
+            for (int i = j; i < CF::kPairBytes / 8; i += HC) ct[i] = make_float2(0.0f, 0.0f);
+            for (int i = j; i < CF::kK; i += HC) to.put16(i, 0);
+            for (int i = j; i < CF::kParts; i += HC) to.put3(i, 0);
         }
     }
     // over the tokens of the warp; the scales' sums over the rows as well
@@ -306,7 +347,8 @@ __global__ void __launch_bounds__(256) k_sum(Split sp, int64_t d, const float *_
                                              const float *__restrict__ mp,
                                              float *__restrict__ dscale,
                                              float *__restrict__ dbase) {
-    constexpr int MIX = Coef<HC>::kMix, CH = Split::channels(HC), FT = HC * CH;
+    constexpr int MIX = Coef<HC>::kMix;
+    const int CH = (int)sp.channels, FT = HC * CH;
     griddep_wait_then_release();
     const int64_t b = blockIdx.x, dwb = sp.slices * MIX;
     if (b < dwb) {
@@ -341,12 +383,21 @@ template <int HC>
 Parts parts(int64_t n, int64_t d) {
     using CF = Coef<HC>;
     Parts p;
+    // enough for either kernel that makes dx and dW
+    const size_t tiles = (size_t)((n + kTileTokens - 1) / kTileTokens) * CF::kTileBytes;
+    const size_t rows = (size_t)n * CF::kBytes;
     p.rec = 0;
-    p.mix = up256((size_t)n * CF::kBytes);
+    p.mix = up256(HC == 4 && tiles > rows ? tiles : rows);
     p.dw = p.mix + up256((size_t)kMaxBlocks * mix_warps<HC>() * (CF::kMix + 4) * 4);
-    // a block crosses into another slice at most once per slice
-    const Split sp = Split::of(n, HC, d, Split::kMaxBlocks);
-    p.end = p.dw + up256((size_t)(sp.blocks + sp.slices) * CF::kMix * HC * Split::channels(HC) * 4);
+    auto partial = [](const Split &sp) {
+        return (size_t)(sp.blocks + sp.slices) * CF::kMix * HC * sp.channels * 4;
+    };
+    size_t most = partial(split_dx_dw(n, HC, d, Split::kMaxBlocks));
+    if (HC == 4) {
+        const size_t other = partial(split_dx_dw_tma(n, d, Split::kMaxBlocks));
+        if (other > most) most = other;
+    }
+    p.end = p.dw + up256(most);
     return p;
 }
 
@@ -361,7 +412,9 @@ cudaError_t launch(const PreBackward &p, const DeviceInfo &di, cudaStream_t s) {
     float *mp = reinterpret_cast<float *>(p.ws + at.mix);
     int lg = 5;
     while (lg < 8 && (1 << lg) < nv && (p.n >> (8 - lg)) < (int64_t)di.sms * 3) ++lg;
-    const int64_t groups = (p.n + (256 >> lg) - 1) / (256 >> lg);
+    const bool tiled = dx_dw_tma_takes(p);
+    const int64_t npad = tiled ? (p.n + kTileTokens - 1) / kTileTokens * kTileTokens : p.n;
+    const int64_t groups = (npad + (256 >> lg) - 1) / (256 >> lg);
     const int64_t cap = di.sms * 3 < kMaxBlocks ? di.sms * 3 : kMaxBlocks;
     const int blocks = (int)(groups < cap ? groups : cap);
     const size_t smem = (size_t)MW * (2 * p.iters - 1) * 32 * 4;
@@ -372,12 +425,13 @@ cudaError_t launch(const PreBackward &p, const DeviceInfo &di, cudaStream_t s) {
         if (e != cudaSuccess) return e;
     }
     cudaError_t e = launch_overlapped(
-        k_mix_backward<HC, K8>, dim3(blocks), dim3(256 + 32 * MW), smem, s, p.n, nv, nblk, lg,
+        k_mix_backward<HC, K8>, dim3(blocks), dim3(256 + 32 * MW), smem, s, p.n, npad, nv, nblk, lg,
         p.iters, p.eps, p.norm_eps, (float)F, reinterpret_cast<const uint4 *>(p.dy), p.x, p.mixes,
-        p.scale, p.base, p.dpost, p.dcomb, m.rec, mp);
+        p.scale, p.base, p.dpost, p.dcomb, m.rec, (int)tiled, mp);
     if (e != cudaSuccess) return e;
-    m.split = Split::of(p.n, HC, p.d, di.sms < Split::kMaxBlocks ? di.sms : Split::kMaxBlocks);
-    e = launch_dx_dw(p, m, di, s);
+    const int64_t sms = di.sms < Split::kMaxBlocks ? di.sms : Split::kMaxBlocks;
+    m.split = tiled ? split_dx_dw_tma(p.n, p.d, sms) : split_dx_dw(p.n, HC, p.d, sms);
+    e = tiled ? launch_dx_dw_tma(p, m, di, s) : launch_dx_dw(p, m, di, s);
     if (e != cudaSuccess) return e;
     const int64_t grid = m.split.slices * MIX + (MIX + 3 + 7) / 8;
     return launch_overlapped(k_sum<HC>, dim3((unsigned)grid), dim3(256), 0, s, m.split, p.d, m.dwp,

@@ -1,0 +1,41 @@
+// hc_pre_bwd.cuh -- device helpers shared by the two kernels that make dx and dW.
+#pragma once
+
+#include "hc_ptx.cuh"
+
+namespace hc {
+namespace ptx {
+
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const float v[8]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+        "r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])),
+        "r"(__float_as_uint(v[3])), "r"(__float_as_uint(v[4])), "r"(__float_as_uint(v[5])),
+        "r"(__float_as_uint(v[6])), "r"(__float_as_uint(v[7]))
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() {
+    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+// the values of loads that have been waited for, not to be used before
+template <int N>
+__device__ __forceinline__ void arrived(float v[N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) asm volatile("" : "+f"(v[i]));
+}
+__device__ __forceinline__ void lds_pairs(uint32_t a, uint64_t &x, uint64_t &y) {
+    asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(x), "=l"(y) : "r"(a));
+}
+__device__ __forceinline__ uint32_t pack_pair(uint64_t v) {
+    float lo, hi;
+    unpack2(v, lo, hi);
+    return pack_bf16x2(lo, hi);
+}
+
+}  // namespace ptx
+}  // namespace hc

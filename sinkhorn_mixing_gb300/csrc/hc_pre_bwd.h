@@ -13,6 +13,8 @@ namespace hc {
 //     its largest magnitude in [2^13, 2^14), zeros behind (2+HC) HC
 //   du3 [kParts] bf16: du = hi + mid + lo, three bf16 numbers (24 bits).
 //     HC = 4: [hi | mid | lo | zeros] of 24 each, in 80; HC = 8: 3 x 80.
+constexpr int kTileTokens = 64;
+
 template <int HC>
 struct Coef {
     static constexpr int kMix = (2 + HC) * HC;
@@ -23,6 +25,9 @@ struct Coef {
     static constexpr int kParts = kN * kProducts;
     static constexpr int kPairBytes = (kF + 1) * 8, kKBytes = kK * 2, kPartBytes = kParts * 2;
     static constexpr int kBytes = kPairBytes + kKBytes + kPartBytes;
+    // For the TMA kernel the records of kTileTokens tokens lie as its shared memory has them:
+    // their coefficients, then du16 twice and du3 in blocks of 8 x 16 bytes (Tiled).
+    static constexpr int kTileBytes = kTileTokens * (kPairBytes + 2 * kKBytes + kPartBytes);
     static_assert(kPairBytes % 16 == 0 && kKBytes % 16 == 0 && kPartBytes % 16 == 0,
                   "16-byte pieces");
     static_assert(HC == 4 ? 3 * kMix <= kN : kMix == kN, "three parts fit");
@@ -49,13 +54,12 @@ struct PreBackward {
 // sums that it leaves for slice s are number c + s, which no other pair has.
 struct Split {
     static constexpr int kMaxBlocks = 160;
-    int64_t slices, steps, total, blocks;
-    static constexpr __host__ __device__ int channels(int hc) { return hc == 4 ? 128 : 64; }
-    static constexpr __host__ __device__ int tokens(int hc) { return hc == 4 ? 32 : 16; }
-    static Split of(int64_t n, int hc, int64_t d, int64_t most) {
+    int64_t slices, steps, total, blocks, channels;
+    static Split of(int64_t n, int64_t d, int channels, int tokens, int64_t most) {
         Split s;
-        s.slices = (d + channels(hc) - 1) / channels(hc);
-        s.steps = (n + tokens(hc) - 1) / tokens(hc);
+        s.channels = channels;
+        s.slices = (d + channels - 1) / channels;
+        s.steps = (n + tokens - 1) / tokens;
         s.total = s.slices * s.steps;
         s.blocks = s.total < most ? s.total : most;
         return s;
@@ -69,13 +73,18 @@ struct Split {
 
 struct MainArgs {
     Split split;
-    uint8_t *rec;  // [n][Coef::kBytes]
+    uint8_t *rec;  // per token, or per tile of tokens (Coef)
     float *dwp;  // [blocks + slices][mix][hc * channels]
 };
 
 constexpr int kBackwardMaxIters = 256;  // Sinkhorn divisors kept in shared memory
 
 size_t pre_backward_bytes(int64_t n, int hc, int64_t d);
+Split split_dx_dw(int64_t n, int hc, int64_t d, int64_t most);
+Split split_dx_dw_tma(int64_t n, int64_t d, int64_t most);
+bool dx_dw_tma_takes(const PreBackward &p);
+cudaError_t launch_dx_dw_tma(const PreBackward &p, const MainArgs &m, const DeviceInfo &di,
+                             cudaStream_t s);
 cudaError_t launch_dx_dw(const PreBackward &p, const MainArgs &m, const DeviceInfo &di,
                          cudaStream_t s);
 cudaError_t launch_pre_backward(const PreBackward &p, const DeviceInfo &di, cudaStream_t s);

@@ -19,8 +19,8 @@
 #include <cuda_fp16.h>
 #include <type_traits>
 
+#include "hc_pre_bwd.cuh"
 #include "hc_pre_bwd.h"
-#include "hc_ptx.cuh"
 
 namespace hc {
 namespace {
@@ -45,7 +45,7 @@ constexpr int kDrain = 16;  // steps between moves of dW's running sums
 template <int HC, bool K8>
 struct Cfg {
     using CF = Coef<HC>;
-    static constexpr int T = Split::tokens(HC), CH = Split::channels(HC), FT = HC * CH;
+    static constexpr int T = HC == 4 ? 32 : 16, CH = HC == 4 ? 128 : 64, FT = HC * CH;
     static constexpr int MIX = CF::kMix, KS = CF::kK / 16;
     // a warp: 16 tokens, 16 channels, 4 copies; a lane of it 2 tokens, 4 channels
     static constexpr int MT = T / 16, GROUPS = CH / 16, JQ = HC / 4, WARPS = MT * GROUPS * JQ;
@@ -92,11 +92,6 @@ __device__ __forceinline__ void cp8(uint32_t dst, const uint8_t *src, uint32_t b
 __device__ __forceinline__ void cp_wait_all() {
     asm volatile("cp.async.wait_all;" ::: "memory");
 }
-__device__ __forceinline__ uint2 lds64(uint32_t a) {
-    uint2 v;
-    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
-    return v;
-}
 __device__ __forceinline__ uint32_t lds32(uint32_t a) {
     uint32_t v;
     asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
@@ -121,31 +116,6 @@ __device__ __forceinline__ void mma_f16(float c[4], const uint32_t a[4], uint32_
             "{%8, %9}, {%0, %1, %2, %3};"
             : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const float v[8]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
-        "r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])),
-        "r"(__float_as_uint(v[3])), "r"(__float_as_uint(v[4])), "r"(__float_as_uint(v[5])),
-        "r"(__float_as_uint(v[6])), "r"(__float_as_uint(v[7]))
-        : "memory");
-}
-__device__ __forceinline__ void tmem_st_wait() {
-    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-}
-// the values of loads that have been waited for, not to be used before
-template <int N>
-__device__ __forceinline__ void arrived(float v[N]) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) asm volatile("" : "+f"(v[i]));
-}
-__device__ __forceinline__ void lds_pairs(uint32_t a, uint64_t &x, uint64_t &y) {
-    asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(x), "=l"(y) : "r"(a));
-}
-__device__ __forceinline__ uint32_t pack_pair(uint64_t v) {
-    float lo, hi;
-    unpack2(v, lo, hi);
-    return pack_bf16x2(lo, hi);
 }
 // a streaming store where `in` is not 0, without a branch around it
 __device__ __forceinline__ void stg64_if(uint8_t *p, uint32_t x, uint32_t y, uint32_t in) {
@@ -592,6 +562,11 @@ cudaError_t launch(const PreBackward &p, const MainArgs &m, const DeviceInfo &di
 }
 
 }  // namespace
+
+Split split_dx_dw(int64_t n, int hc, int64_t d, int64_t most) {
+    return hc == 4 ? Split::of(n, d, Cfg<4, true>::CH, Cfg<4, true>::T, most)
+                   : Split::of(n, d, Cfg<8, true>::CH, Cfg<8, true>::T, most);
+}
 
 cudaError_t launch_dx_dw(const PreBackward &p, const MainArgs &m, const DeviceInfo &di,
                          cudaStream_t s) {

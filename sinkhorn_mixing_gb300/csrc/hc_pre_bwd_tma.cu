@@ -1,0 +1,522 @@
+// hc_pre_bwd_tma.cu -- dx and dW of hc_mixes_pre's gradient at hc = 4, streamed
+// by TMA (hc_pre_bwd.cu has the formulas; hc_pre_bwd_main.cu does the other
+// shapes).
+//
+// A block owns 64 channels of all four copies (256 features) and walks over
+// tokens in steps of 64 (Split).  Both products run on tcgen05:
+//   du W    [64 tokens, 256 features], K = 24: one product a step into TMEM,
+//     fp16 operands times powers of two (as in hc_pre_bwd_main.cu).  The 64
+//     tokens stand in the 128 rows twice, so that all four warps of a quadrant
+//     group find them in the lanes they can read.
+//   du^T x  [256 features, 24], K = tokens: sums over the steps in TMEM, x as
+//     kept in bf16 (codes are widened into an operand tile on the way), du in
+//     three bf16 parts.
+// The rest is per token and channel: a lane is one token, and its coefficients
+// serve 8 channels of 4 copies.  dx goes over the stage's gradient tile and out
+// by a TMA store.
+// Roles: warps 0-15 compute, warp 16 loads (one thread), warp 17 issues the
+// products, warp 18 stores.  Two stages; every wait has a limit, and after one
+// ran out all roles run through without acting, so that all barriers are met.
+#include <cuda_fp16.h>
+
+#include "hc_pre_bwd.cuh"
+#include "hc_pre_bwd.h"
+
+namespace hc {
+namespace {
+
+using namespace ptx;
+using CF = Coef<4>;
+
+constexpr int T = kTileTokens, CH = 64, FT = 4 * CH, MIX = 24;
+constexpr int kComputeWarps = 16, kThreads = 32 * (kComputeWarps + 3);
+constexpr int kDrain = 8;  // steps between moves of dW's running sums (32 products each)
+
+template <bool K8>
+struct Lay {
+    static constexpr int X = T * FT * (K8 ? 1 : 2), OX = T * FT * 2, OY = OX + X;
+    static constexpr int OR = OY + T * CH * 2, STAGE = OR + CF::kTileBytes;
+    static constexpr int OO = 2 * STAGE;                       // x as an operand (K8)
+    static constexpr int OW = OO + (K8 ? T * FT * 2 : 0);      // W, 32 halves a feature
+    static constexpr int OS = OW + FT * 64;                    // scales [2][2 blocks][T][4]
+    static constexpr int OE = OS + (K8 ? 2 * 2 * T * 16 : 0);  // barriers, flags, maxima
+    static constexpr int SMEM = OE + 256;
+    static_assert(STAGE % 1024 == 0 && OW % 1024 == 0, "swizzled tiles");
+    static_assert(SMEM <= 232448, "shared memory");
+};
+
+enum Bar { kFull = 0, kEmpty = 16, kD1Full = 32, kD1Free = 40, kGate = 48, kD2Done = 56, kOut = 64 };
+constexpr int kAbort = 80, kTmem = 84, kCalm = 88, kMaxima = 96;
+constexpr int kD2 = 256, kSums = kD2 + 2 * CF::kN;  // TMEM columns; du W has 0..255
+static_assert(kSums + 2 * MIX <= 512, "TMEM");
+
+constexpr uint32_t kIdescW = (1u << 4) | ((uint32_t)(FT >> 3) << 17) | (8u << 24);  // fp16
+constexpr uint32_t kIdescX = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 15) | (1u << 16) |
+                             ((uint32_t)(CF::kN >> 3) << 17) | (8u << 24);          // bf16
+
+struct Args {
+    Split split;
+    int64_t n, d, nblk;
+    const uint8_t *xs;
+    const float *w;
+    const uint8_t *rec;
+    float *dwp;
+    unsigned int *err;
+    int has_g;
+};
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, int c0, int c1,
+                                            int c2, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, int c0, int c1, int c2,
+                                             uint32_t src) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+            reinterpret_cast<uint64_t>(map)),
+        "r"(c0), "r"(c1), "r"(c2), "r"(src)
+        : "memory");
+}
+__device__ __forceinline__ void bulk_load(uint32_t dst, const uint8_t *src, uint32_t bytes,
+                                          uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+            dst),
+        "l"(src), "r"(bytes), "r"(bar)
+        : "memory");
+}
+template <int ID, int N>
+__device__ __forceinline__ void meet() {
+    asm volatile("bar.sync %0, %1;" ::"n"(ID), "n"(N) : "memory");
+}
+
+// Matrix descriptors.  rows16: blocks of 8 x 16 bytes without swizzle, `k` bytes
+// to the next block along K, `mn` along M or N.  tiles128: rows of 128 bytes
+// (64 features) with 128-byte swizzle, rows along K; 64 tokens to the next 64
+// features.
+__device__ __forceinline__ uint64_t rows16(uint32_t saddr, uint32_t k, uint32_t mn) {
+    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(k >> 4) << 16) |
+           ((uint64_t)(mn >> 4) << 32) | ((uint64_t)1 << 46);
+}
+__device__ __forceinline__ uint64_t tiles128(uint32_t saddr) {
+    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(T * 128 >> 4) << 16) |
+           ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+
+// Walks the runs of steps of this block: f(slice, first step, past the last).
+template <typename Fn>
+__device__ __forceinline__ void over_runs(const Split &sp, Fn f) {
+    int64_t step = sp.first(blockIdx.x);
+    const int64_t end = sp.first(blockIdx.x + 1);
+    while (step < end) {
+        const int64_t slice = step / sp.steps, s0 = step - slice * sp.steps;
+        const int64_t s1 = min(sp.steps, s0 + (end - step));
+        f(slice, s0, s1);
+        step += s1 - s0;
+    }
+}
+
+template <bool K8>
+__global__ void __launch_bounds__(kThreads, 1)
+    k_dx_dw_tma(const __grid_constant__ CUtensorMap map_g, const __grid_constant__ CUtensorMap map_x,
+                const __grid_constant__ CUtensorMap map_y,
+                const __grid_constant__ CUtensorMap map_dx, Args a) {
+    using L = Lay<K8>;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const uint32_t sb = su32(smem), eb = sb + L::OE;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    volatile int *abort = reinterpret_cast<int *>(smem + L::OE + kAbort);
+    volatile int *calm = reinterpret_cast<int *>(smem + L::OE + kCalm);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::OE + kTmem);
+    float *maxima = reinterpret_cast<float *>(smem + L::OE + kMaxima);  // per warp
+
+    if (tid == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(eb + kFull + 8 * i, 1);
+            mbar_init(eb + kEmpty + 8 * i, 2);
+            mbar_init(eb + kOut + 8 * i, kComputeWarps);
+        }
+        mbar_init(eb + kD1Full, 1);
+        mbar_init(eb + kD1Free, kComputeWarps);
+        mbar_init(eb + kGate, kComputeWarps);
+        mbar_init(eb + kD2Done, 1);
+        *abort = 0;
+        *calm = 0;
+        if ((sb & 1023u) != 0) {  // swizzled tiles need it
+            atomicOr(a.err, kErrSmemLayout);
+            *abort = 1;
+        }
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 0) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         su32(tmem_slot)),
+                     "r"(512)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    auto wait = [&](uint32_t bar, uint32_t parity) {
+        return wait_bar<false>(eb + bar, parity & 1, abort, a.err);
+    };
+    auto stage = [&](int64_t it) { return sb + (uint32_t)(it & 1) * L::STAGE; };
+    int64_t it = 0;  // steps of this block so far: stage it & 1, its use it >> 1
+
+    if (warp == kComputeWarps) {
+        // ------------------------------------------------------- loads
+        if (lane == 0) {
+            griddep_wait_then_release();
+            asm volatile("fence.proxy.async;" ::: "memory");  // records were plain stores
+            over_runs(a.split, [&](int64_t slice, int64_t s0, int64_t s1) {
+                for (int64_t s = s0; s < s1; ++s, ++it) {
+                    const uint32_t slot = (uint32_t)(it & 1) * 8;
+                    if (it >= 2 && !wait(kEmpty + slot, (uint32_t)(it >> 1) - 1)) continue;
+                    if (*abort) continue;
+                    const uint32_t st = stage(it), bar = eb + kFull + slot;
+                    mbar_expect_tx(bar, L::X + T * CH * 2 + CF::kTileBytes +
+                                            (a.has_g ? T * FT * 2 : 0));
+                    const int c = (int)slice * CH, t = (int)(s * T);
+                    if (a.has_g) tma_load_3d(st, &map_g, c, t, 0, bar);
+                    tma_load_3d(st + L::OX, &map_x, c, t, 0, bar);
+                    bulk_load(st + L::OR, a.rec + s * CF::kTileBytes, CF::kTileBytes, bar);
+                    tma_load_2d(st + L::OY, &map_y, c, t, bar);
+                }
+            });
+            if (*abort)  // what was loaded has to land before this block ends
+                for (int64_t i = it > 2 ? it - 2 : 0; i < it; ++i)
+                    wait_bar<false>(eb + kFull + (uint32_t)(i & 1) * 8, (uint32_t)(i >> 1) & 1, calm,
+                                    a.err, 1000000);
+        }
+    } else if (warp == kComputeWarps + 1) {
+        // ---------------------------------------------------- products
+        over_runs(a.split, [&](int64_t, int64_t s0, int64_t s1) {
+            meet<2, 32 * (kComputeWarps + 1)>();  // W of this slice is there
+            if (lane == 0) {
+                auto du_w = [&](int64_t i) {
+                    bool ok = wait(kFull + (uint32_t)(i & 1) * 8, (uint32_t)(i >> 1));
+                    if (i > 0) ok = wait(kD1Free, (uint32_t)(i - 1)) && ok;
+                    if (!ok) return;
+                    tc_fence_after();
+                    const uint32_t ao = stage(i) + L::OR + T * CF::kPairBytes;
+#pragma unroll
+                    for (int ks = 0; ks < CF::kK / 16; ++ks)
+                        mma_bf16(tmem, rows16(ao + ks * 256, 128, 512),
+                                 rows16(sb + L::OW + ks * 256, 128, 512), kIdescW, ks > 0);
+                    mma_commit(eb + kD1Full);
+                };
+                du_w(it);
+                for (int64_t s = s0; s < s1; ++s, ++it) {
+                    if (s + 1 < s1) du_w(it + 1);
+                    if (!wait(kGate, (uint32_t)it)) continue;
+                    tc_fence_after();
+                    const uint32_t xo = K8 ? sb + L::OO : stage(it) + L::OX;
+                    const uint32_t bo =
+                        stage(it) + L::OR + T * CF::kPairBytes + 2 * T * CF::kKBytes;
+#pragma unroll
+                    for (int ks = 0; ks < T / 16; ++ks)
+#pragma unroll
+                        for (int m = 0; m < 2; ++m)
+                            mma_bf16(tmem + kD2 + m * CF::kN,
+                                     tiles128(xo + m * 2 * T * 128 + ks * 2048),
+                                     rows16(bo + ks * 256, 128, T / 8 * 128), kIdescX,
+                                     (s - s0) % kDrain != 0 || ks > 0);
+                    mma_commit(eb + kD2Done);
+                    mma_commit(eb + kEmpty + (uint32_t)(it & 1) * 8);
+                }
+            }
+            __syncwarp();
+        });
+        if (lane == 0 && *abort) {  // products in flight read shared memory
+            mma_commit(eb + kD1Full);
+            mma_commit(eb + kD2Done);
+            const uint64_t t0 = gtimer();
+            while (gtimer() - t0 < 1000000) {
+            }
+        }
+    } else if (warp == kComputeWarps + 2) {
+        // ------------------------------------------------------ stores
+        if (lane == 0) {
+            over_runs(a.split, [&](int64_t slice, int64_t s0, int64_t s1) {
+                for (int64_t s = s0; s < s1; ++s, ++it) {
+                    const uint32_t slot = (uint32_t)(it & 1) * 8;
+                    if (!wait(kOut + slot, (uint32_t)(it >> 1))) continue;
+                    tma_store_3d(&map_dx, (int)slice * CH, (int)(s * T), 0, stage(it));
+                    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                    asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                    mbar_arrive(eb + kEmpty + slot);
+                }
+            });
+            asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+        }
+    } else {
+        // ----------------------------------------------------- compute
+        // lane's token of the step, and the warp's 8 channels
+        const int tl = (warp & 1) * 32 + lane, cg = (warp >> 2) * 2 + (warp >> 1 & 1);
+        const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);
+        const uint32_t row = (uint32_t)tl * 128 + (uint32_t)((cg ^ (tl & 7)) << 4);
+        const uint32_t row8 =
+            (uint32_t)tl * 64 + (uint32_t)(((cg >> 1) ^ (tl >> 1 & 3)) << 4) + (cg & 1) * 8;
+        const int64_t F = 4 * a.d;
+        auto arrive = [&](uint32_t bar) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(eb + bar);
+        };
+        bool started = false;
+        over_runs(a.split, [&](int64_t slice, int64_t s0, int64_t s1) {
+            const int64_t ch0 = slice * CH;
+            const int width = (int)min((int64_t)CH, a.d - ch0);
+            // ---- the slice of W in fp16, its largest magnitude brought to [2^13, 2^14): 8 x 8
+            // blocks [feature group][mix group][feature][mix]
+            float top = 0.0f;
+            for (int q = tid; q < MIX * FT; q += 32 * kComputeWarps) {
+                const int i = q / FT, m = q % FT, c = m % CH;
+                if (c < width)
+                    top = fmaxf(top, fabsf(__ldg(a.w + (int64_t)i * F + m / CH * a.d + ch0 + c)));
+            }
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1)
+                top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, off));
+            if (lane == 0) maxima[warp] = top;
+            meet<1, 32 * kComputeWarps>();
+            top = maxima[lane % kComputeWarps];
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1)
+                top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, off));
+            const int ex = min(max((int)(__float_as_uint(top) >> 23), 14), 253);
+            const float wup = __uint_as_float((uint32_t)(267 - ex) << 23);
+            const float wdown = __uint_as_float((uint32_t)(ex - 13) << 23);
+            const uint64_t wdown2 = pack2(wdown, wdown);
+            for (int q = tid; q < CF::kK * FT; q += 32 * kComputeWarps) {
+                const int i = q / FT, m = q % FT, c = m % CH;
+                float v = 0.0f;
+                if (i < MIX && c < width) v = __ldg(a.w + (int64_t)i * F + m / CH * a.d + ch0 + c);
+                *reinterpret_cast<__half *>(smem + L::OW + m / 8 * 512 + i / 8 * 128 + m % 8 * 16 +
+                                            i % 8 * 2) = __float2half_rn(v * wup);
+            }
+            if (!started) {
+                griddep_wait_then_release();
+                started = true;
+            }
+
+            // ---- scales: one a thread, a step ahead, shared through [block][token][copy]
+            const int sct = tid >> 3, scj = tid >> 1 & 3, scb = tid & 1;
+            const bool sin = K8 && scb * 32 < width;
+            const uint8_t *sp = a.xs + ((s0 * T + sct) * 4 + scj) * a.nblk + ch0 / 32 + scb;
+            auto load_scale = [&](int64_t s) -> uint32_t {
+                uint32_t v = 0;
+                if (sin && s * T + sct < a.n) v = __ldg(sp);
+                sp += T * 4 * a.nblk;
+                return v;
+            };
+            auto keep_scale = [&](int64_t i, uint32_t v) {
+                if (K8)
+                    *reinterpret_cast<float *>(smem + L::OS + (i & 1) * (2 * T * 16) +
+                                               (scb * T + sct) * 16 + scj * 4) = kept_scale(v);
+            };
+            // dW's sums so far move on (see hc_pre_bwd_main.cu); `out`: the run's result.  A
+            // warp reads 32 lanes of one tile, 16 or 8 of the 24 mix numbers.
+            auto drain = [&](bool first, float *out) {
+                const int m = warp >> 2 & 1, c0 = warp >> 3 ? 16 : 0, c1 = warp >> 3 ? 24 : 16;
+                const uint32_t ta = lanes + kD2 + m * CF::kN, ts = lanes + kSums + m * MIX;
+#pragma unroll 1
+                for (int c = c0; c < c1; c += 8) {
+                    float v[8], u[8], w[8], sum[8];
+                    tmem_ld8(ta + c, v);
+                    tmem_ld8(ta + MIX + c, u);
+                    tmem_ld8(ta + 2 * MIX + c, w);
+                    if (!first) tmem_ld8(ts + c, sum);
+                    tmem_ld_wait();
+                    arrived<8>(v);
+                    arrived<8>(u);
+                    arrived<8>(w);
+                    if (!first) arrived<8>(sum);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        v[e] += u[e] + w[e];
+                        if (!first) v[e] += sum[e];
+                    }
+                    if (out != nullptr) {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            out[(int64_t)(c + e) * FT + m * 128 + (warp & 3) * 32 + lane] = v[e];
+                    } else {
+                        tmem_st8(ts + c, v);
+                    }
+                }
+                tmem_st_wait();
+            };
+
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            keep_scale(it, load_scale(s0));
+            meet<2, 32 * (kComputeWarps + 1)>();
+            for (int64_t s = s0; s < s1; ++s, ++it) {
+                const uint32_t st = stage(it), slot = (uint32_t)(it & 1) * 8;
+                uint32_t next_scale = 0;
+                if (K8 && s + 1 < s1) next_scale = load_scale(s + 1);
+                wait(kFull + slot, (uint32_t)(it >> 1));
+                wait(kD1Full, (uint32_t)it);
+                tc_fence_after();
+                // ---- du W of this token
+                uint64_t v[4][4], qq, ff;
+                const uint32_t cfa = st + L::OR + tl * CF::kPairBytes;
+                {
+                    float acc[4][8];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) tmem_ld8(lanes + j * CH + cg * 8, acc[j]);
+                    lds_pairs(cfa + CF::kQ * 8, qq, ff);
+                    ff = fmul2(ff, wdown2);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) arrived<8>(acc[j]);
+                    tc_fence_before();
+                    arrive(kD1Free);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+#pragma unroll
+                        for (int p = 0; p < 4; ++p)
+                            v[j][p] = fmul2(pack2(acc[j][2 * p], acc[j][2 * p + 1]), ff);
+                }
+                // ---- x, and its operand once the products before have been through it
+                if (it > 0) wait(kD2Done, (uint32_t)it - 1);
+                if (s > s0 && (s - s0) % kDrain == 0) {
+                    tc_fence_after();
+                    drain(s - s0 == kDrain, nullptr);
+                    tc_fence_before();
+                }
+                if (K8) meet<1, 32 * kComputeWarps>();  // all scales of the step are there
+                float4 sc;
+                if (K8) {
+                    const uint4 u = lds128(sb + L::OS + (uint32_t)(it & 1) * (2 * T * 16) +
+                                           ((cg >> 2) * T + tl) * 16);
+                    sc = make_float4(__uint_as_float(u.x), __uint_as_float(u.y),
+                                     __uint_as_float(u.z), __uint_as_float(u.w));
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    uint64_t xv[4];
+                    if (K8) {
+                        const float f1 = j == 0 ? sc.x : j == 1 ? sc.y : j == 2 ? sc.z : sc.w;
+                        const uint64_t f2 = pack2(f1, f1);
+                        float f[8];
+                        e4m3x8_to_float(lds64(st + L::OX + j * T * 64 + row8), f);
+#pragma unroll
+                        for (int p = 0; p < 4; ++p)
+                            xv[p] = fmul2(pack2(f[2 * p], f[2 * p + 1]), f2);
+                        sts128(sb + L::OO + j * T * 128 + row,
+                               make_uint4(pack_pair(xv[0]), pack_pair(xv[1]), pack_pair(xv[2]),
+                                          pack_pair(xv[3])));
+                    } else {
+                        const uint4 u = lds128(st + L::OX + j * T * 128 + row);
+                        xv[0] = bf16x2_to_f32x2(u.x), xv[1] = bf16x2_to_f32x2(u.y);
+                        xv[2] = bf16x2_to_f32x2(u.z), xv[3] = bf16x2_to_f32x2(u.w);
+                    }
+#pragma unroll
+                    for (int p = 0; p < 4; ++p) ffma2(v[j][p], qq, xv[p]);
+                }
+                if (K8) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                arrive(kGate);
+                // ---- the stream's gradient through comb, and y's through pre
+                auto add = [&](uint32_t coef, const uint4 &u) {
+                    uint64_t c[4];
+                    lds_pairs(coef, c[0], c[1]);
+                    lds_pairs(coef + 16, c[2], c[3]);
+                    const uint64_t b[4] = {bf16x2_to_f32x2(u.x), bf16x2_to_f32x2(u.y),
+                                           bf16x2_to_f32x2(u.z), bf16x2_to_f32x2(u.w)};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+#pragma unroll
+                        for (int p = 0; p < 4; ++p) ffma2(v[j][p], c[j], b[p]);
+                };
+                if (a.has_g) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) add(cfa + k * 32, lds128(st + k * T * 128 + row));
+                }
+                add(cfa + CF::kPre * 8, lds128(st + L::OY + row));
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    sts128(st + j * T * 128 + row,
+                           make_uint4(pack_pair(v[j][0]), pack_pair(v[j][1]), pack_pair(v[j][2]),
+                                      pack_pair(v[j][3])));
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                arrive(kOut + slot);
+                keep_scale(it + 1, next_scale);
+            }
+            wait(kD2Done, (uint32_t)it - 1);
+            tc_fence_after();
+            drain(s1 - s0 <= kDrain, a.dwp + (blockIdx.x + slice) * (int64_t)MIX * FT);
+            tc_fence_before();
+            meet<1, 32 * kComputeWarps>();  // before maxima and W are written anew
+        });
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 0)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512)
+                     : "memory");
+}
+
+// [hc][n][d] view of a stream: boxes of 64 channels, 64 tokens, all copies.
+bool stream_map(CUtensorMap *map, const void *p, bool bytes, int64_t n, int64_t d) {
+    const cuuint64_t es = bytes ? 1 : 2;
+    const cuuint64_t dim[3] = {(cuuint64_t)d, (cuuint64_t)n, 4};
+    const cuuint64_t stride[2] = {(cuuint64_t)(4 * d) * es, (cuuint64_t)d * es};
+    const cuuint32_t box[3] = {CH, T, 4}, one[3] = {1, 1, 1};
+    return tensor_map_encoder()(
+               map, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+               const_cast<void *>(p), dim, stride, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               bytes ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool K8>
+cudaError_t launch(const PreBackward &p, const MainArgs &m, const DeviceInfo &di, cudaStream_t s) {
+    using L = Lay<K8>;
+    const cudaError_t e = cudaFuncSetAttribute(
+        k_dx_dw_tma<K8>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM);
+    if (e != cudaSuccess) return e;
+    CUtensorMap g, x, y, dx;
+    const cuuint64_t dim[2] = {(cuuint64_t)p.d, (cuuint64_t)p.n};
+    const cuuint64_t stride[1] = {(cuuint64_t)p.d * 2};
+    const cuuint32_t box[2] = {CH, T}, one[2] = {1, 1};
+    if (!stream_map(&dx, p.dx, false, p.n, p.d) || !stream_map(&x, p.x.data, K8, p.n, p.d) ||
+        !stream_map(&g, p.dstream != nullptr ? p.dstream : p.dx, false, p.n, p.d) ||
+        tensor_map_encoder()(&y, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+                             const_cast<uint16_t *>(p.dy), dim, stride, box, one,
+                             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return cudaErrorInvalidValue;
+    Args a;
+    a.split = m.split;
+    a.n = p.n, a.d = p.d, a.nblk = kept_blocks(p.d);
+    a.xs = p.x.scales, a.w = p.w, a.rec = m.rec, a.dwp = m.dwp, a.err = di.err_word;
+    a.has_g = p.dstream != nullptr;
+    return launch_overlapped(k_dx_dw_tma<K8>, dim3((unsigned)m.split.blocks), dim3(kThreads),
+                             (size_t)L::SMEM, s, g, x, y, dx, a);
+}
+
+}  // namespace
+
+Split split_dx_dw_tma(int64_t n, int64_t d, int64_t most) { return Split::of(n, d, CH, T, most); }
+
+bool dx_dw_tma_takes(const PreBackward &p) {
+    return p.hc == 4 && p.d >= CH && p.n < (int64_t(1) << 31) && forced_path() != kPathGeneral &&
+           (p.x.scales == nullptr || p.d % 16 == 0) && tensor_map_encoder() != nullptr;
+}
+
+cudaError_t launch_dx_dw_tma(const PreBackward &p, const MainArgs &m, const DeviceInfo &di,
+                             cudaStream_t s) {
+    return p.x.scales != nullptr ? launch<true>(p, m, di, s) : launch<false>(p, m, di, s);
+}
+
+}  // namespace hc

@@ -289,6 +289,20 @@ def test_mixes_pre_backward(hc, copies, n, d, k8):
     check_pre(run_pre(hc, c), c)
 
 
+@pytest.mark.parametrize("n,d", [(2, 64), (63, 80), (64, 96), (65, 128), (700, 144), (1100, 192),
+                                 (3000, 5120)])
+@pytest.mark.parametrize("k8", [True, False])
+def test_mixes_pre_backward_streamed(hc, monkeypatch, n, d, k8):
+    # shapes that the TMA kernel takes, and the general path on the same inputs
+    c = pre_case(hc, n, 4, d, k8)
+    got = run_pre(hc, c)
+    check_pre(got, c)
+    monkeypatch.setenv("HCMIX_PATH", "general")
+    other = run_pre(hc, c)
+    check_pre(other, c)
+    assert torch.equal(got[2], other[2]) and torch.equal(got[3], other[3])
+
+
 @pytest.mark.parametrize("copies", [4, 8])
 @pytest.mark.parametrize("iters", [1, 2, 50, 256])
 def test_mixes_pre_backward_iters(hc, copies, iters):
