@@ -13,10 +13,10 @@
 namespace hc {
 namespace {
 
-// Slot i stands for vector i % per of row i / per; per is the row's vector
-// count rounded up to whole blocks (4), so a group of four lanes never spans
-// two rows, and a row's last slots may lie past its end.  At most 2^31 slots
-// a launch: larger tensors take several.
+// Slot i stands for vector i % per of row i / per (in k_checkpoint: a pair of
+// vectors); per covers whole blocks (4 vectors), so the lanes of a block never
+// span two rows, and a row's last slots may lie past its end.  At most 2^31
+// slots a launch: larger tensors take several.
 struct Slots {
     uint32_t count;       // rows * per
     uint32_t per;         // slots per row
@@ -31,12 +31,12 @@ struct Slots {
 
 // With l = ceil(log2 per) and mul = ceil(2^(31+l) / per) the product's error
 // is below 2^l * 2^31 / 2^(31+l) / per, so the quotient is exact for i < 2^31.
-Slots make_slots(int64_t rows, int64_t d) {
+Slots make_slots(int64_t rows, int64_t d, int per_block = 4) {
     Slots s;
     s.nv = (uint32_t)(d / 8);
-    s.per = (uint32_t)(kept_blocks(d) * 4);
+    s.per = (uint32_t)(kept_blocks(d) * per_block);
     s.count = (uint32_t)(rows * s.per);
-    int l = 2;
+    int l = 1;
     while ((int64_t(1) << l) < s.per) ++l;
     s.mul = (uint32_t)(((uint64_t(1) << (31 + l)) + s.per - 1) / s.per);
     s.shift = (uint32_t)(l - 1);
@@ -55,6 +55,9 @@ cudaError_t by_pieces(int64_t rows, int64_t d, Fn f) {
 }
 
 // ---------------------------------------------------------- k_checkpoint
+// A lane takes 16 channels where the other kernels take 8: two lanes a block,
+// one shuffle, and 16 bytes of codes a store (65,536 tokens of 4 x 5120: see
+// the figures in the design notes).  A row's last lane may have 8.
 template <int U>
 __global__ void __launch_bounds__(256) k_checkpoint(Slots sl, int64_t nblk,
                                                     const uint4 *__restrict__ x,
@@ -63,23 +66,35 @@ __global__ void __launch_bounds__(256) k_checkpoint(Slots sl, int64_t nblk,
     griddep_wait_then_release();
     const uint32_t lane = threadIdx.x & 31;
     const uint32_t step = gridDim.x * 256u * U;
+    const bool wide = sl.nv % 2 == 0;  // then 16 codes are 16-byte aligned
     for (uint32_t i0 = (blockIdx.x * 256u + (threadIdx.x & ~31u)) * U; i0 < sl.count; i0 += step) {
-        uint4 r[U];
+        uint4 r[U][2];
         int64_t row[U];
         uint32_t v[U];
 #pragma unroll
         for (int a = 0; a < U; ++a) {
             sl.at(i0 + 32 * a + lane, row[a], v[a]);
+            v[a] *= 2;
             if (i0 + 32 * a + lane >= sl.count) v[a] = sl.nv;
-            r[a] = v[a] < sl.nv ? ld_stream(x + row[a] * sl.nv + v[a]) : make_uint4(0, 0, 0, 0);
+            const uint4 *p = x + row[a] * sl.nv + v[a];
+            r[a][0] = v[a] < sl.nv ? ld_stream(p) : make_uint4(0, 0, 0, 0);
+            r[a][1] = v[a] + 1 < sl.nv ? ld_stream(p + 1) : make_uint4(0, 0, 0, 0);
         }
 #pragma unroll
         for (int a = 0; a < U; ++a) {
-            uint32_t byte;
-            const uint2 c = kept_quantise(r[a], byte);
+            uint32_t m = max(kept_largest(r[a][0]), kept_largest(r[a][1]));
+            m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+            const uint32_t byte = kept_scale_byte(m);
+            const uint2 lo = kept_codes(r[a][0], byte), hi = kept_codes(r[a][1], byte);
             if (v[a] < sl.nv) {
-                __stcs(codes + row[a] * sl.nv + v[a], c);
-                if ((lane & 3) == 0) scales[row[a] * nblk + (v[a] >> 2)] = (uint8_t)byte;
+                uint2 *p = codes + row[a] * sl.nv + v[a];
+                if (wide) {
+                    __stcs(reinterpret_cast<uint4 *>(p), make_uint4(lo.x, lo.y, hi.x, hi.y));
+                } else {
+                    __stcs(p, lo);
+                    if (v[a] + 1 < sl.nv) __stcs(p + 1, hi);
+                }
+                if ((lane & 1) == 0) scales[row[a] * nblk + (v[a] >> 2)] = (uint8_t)byte;
             }
         }
     }
@@ -165,7 +180,7 @@ __global__ void __launch_bounds__(256) k_pre_restore(Slots sl, int64_t nblk, Kep
 // loaded per vector, row by row of comb: they hit the first-level cache, and
 // only the accumulators stay in registers.
 template <int HC>
-__global__ void __launch_bounds__(256) k_post_checkpoint(Slots sl, int64_t nblk,
+__global__ void __launch_bounds__(256, HC == 4 ? 3 : 2) k_post_checkpoint(Slots sl, int64_t nblk,
                                                          const uint4 *__restrict__ out,
                                                          const uint4 *res,
                                                          const float *__restrict__ post,
@@ -245,8 +260,8 @@ cudaError_t launch_checkpoint(int64_t rows, int64_t d, const uint16_t *x, uint8_
                               uint8_t *scales, const DeviceInfo &di, cudaStream_t s) {
     const int64_t nblk = kept_blocks(d);
     return by_pieces(rows, d, [&](int64_t r0, int64_t nr) {
-        const Slots sl = make_slots(nr, d);
-        return launch_overlapped(k_checkpoint<4>, stream_grid(sl, 4, di.sms, 8), dim3(256), 0, s,
+        const Slots sl = make_slots(nr, d, 2);
+        return launch_overlapped(k_checkpoint<2>, stream_grid(sl, 2, di.sms, 8), dim3(256), 0, s,
                                  sl, nblk, reinterpret_cast<const uint4 *>(x + r0 * d),
                                  reinterpret_cast<uint2 *>(codes + r0 * d), scales + r0 * nblk);
     });

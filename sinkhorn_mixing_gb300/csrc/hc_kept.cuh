@@ -84,14 +84,8 @@ __device__ __forceinline__ uint32_t kept_largest(uint4 &v) {
     return max(m & 0xFFFFu, m >> 16);
 }
 
-// Quantises the 8 channels of `v` of one lane: the four lanes of an aligned
-// group hold one block.  All lanes of the warp take part; a lane past the
-// row's end passes zeros.  Returns the codes; `byte` is the block's scale.
-__device__ __forceinline__ uint2 kept_quantise(uint4 v, uint32_t &byte) {
-    uint32_t m = kept_largest(v);
-    m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-    m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-    byte = kept_scale_byte(m);
+// The codes of the 8 channels of `v` under the scale byte `byte`.
+__device__ __forceinline__ uint2 kept_codes(const uint4 &v, uint32_t byte) {
     const float inv = __uint_as_float((254u - byte) << 23);
     float f[8];
     unpack8(v, f);
@@ -104,6 +98,17 @@ __device__ __forceinline__ uint2 kept_quantise(uint4 v, uint32_t &byte) {
     }
     return make_uint2(float_to_e4m3x4(f[0], f[1], f[2], f[3]),
                       float_to_e4m3x4(f[4], f[5], f[6], f[7]));
+}
+
+// Quantises the 8 channels of `v` of one lane: the four lanes of an aligned
+// group hold one block.  All lanes of the warp take part; a lane past the
+// row's end passes zeros.  Returns the codes; `byte` is the block's scale.
+__device__ __forceinline__ uint2 kept_quantise(uint4 v, uint32_t &byte) {
+    uint32_t m = kept_largest(v);
+    m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+    m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+    byte = kept_scale_byte(m);
+    return kept_codes(v, byte);
 }
 
 // A kept tensor's rows, bf16 (K8 = false) or codes and scales (K8 = true), in

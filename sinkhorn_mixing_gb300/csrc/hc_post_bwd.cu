@@ -12,6 +12,32 @@
 namespace hc {
 namespace {
 
+// Sums a[0..N) over the warp's lanes, each sum ending in one lane (a few of
+// them in each): a step halves what a lane carries, so N + 5 shuffles do what a
+// butterfly per value does in 5 N.  On return a[0..K) of a lane are sums
+// base .. base + count - 1.
+template <int N, int OFF>
+struct Scatter {
+    static constexpr int H = (N + 1) / 2;
+    static constexpr int K = Scatter<H, OFF / 2>::K;
+    static __device__ __forceinline__ void run(float *a, int lane, int &base, int &count) {
+        const bool up = (lane & OFF) != 0;
+#pragma unroll
+        for (int i = 0; i < H; ++i) {
+            const float lo = a[i], hi = H + i < N ? a[H + i] : 0.0f;
+            a[i] = (up ? hi : lo) + __shfl_xor_sync(0xFFFFFFFFu, up ? lo : hi, OFF);
+        }
+        base += up ? H : 0;
+        count = up ? max(count - H, 0) : min(count, H);
+        Scatter<H, OFF / 2>::run(a, lane, base, count);
+    }
+};
+template <int N>
+struct Scatter<N, 0> {
+    static constexpr int K = N;
+    static __device__ __forceinline__ void run(float *, int, int &, int &) {}
+};
+
 // 2^lg lanes share a token (32 at least): one warp, or several whose sums
 // meet in shared memory; 256 threads hold 256 >> lg tokens.
 //
@@ -109,15 +135,11 @@ __global__ void __launch_bounds__(256, HC == 4 ? 2 : 1)
 #pragma unroll
             for (int p = 0; p < KP; ++p)
                 unpack2(acc[j][p], sum[j * HC + 2 * p], sum[j * HC + 2 * p + 1]);
+        int base = 0, count = NS;
+        Scatter<NS, 16>::run(sum, lane, base, count);
 #pragma unroll
-        for (int i = 0; i < NS; ++i)
-#pragma unroll
-            for (int off = 16; off > 0; off >>= 1)
-                sum[i] += __shfl_xor_sync(0xFFFFFFFFu, sum[i], off);
-        if (lane == 0) {
-#pragma unroll
-            for (int i = 0; i < NS; ++i) red[warp][i] = sum[i];
-        }
+        for (int i = 0; i < Scatter<NS, 16>::K; ++i)
+            if (i < count) red[warp][base + i] = sum[i];
         __syncthreads();
         if (t < n) {
             for (int i = l; i < NS; i += lanes) {
@@ -141,7 +163,7 @@ cudaError_t launch(int64_t n, int64_t d, const uint4 *g, const Kept &out, const 
     // a warp per token where the tokens fill the GPU, else more of them, so
     // long as each lane keeps a vector of its own
     int lg = 5;
-    while (lg < 8 && (1 << lg) < nv && (n >> (8 - lg)) < (int64_t)di.sms * 4) ++lg;
+    while (lg < 8 && (2 << lg) <= nv && (n >> (8 - lg)) < (int64_t)di.sms * 4) ++lg;
     const int64_t want = (n + (256 >> lg) - 1) / (256 >> lg), cap = (int64_t)di.sms * 64;
     const dim3 grid((unsigned)(want < cap ? want : cap));
     auto *kernel = dres != nullptr ? &k_post_backward<HC, R8, O8, true>

@@ -350,16 +350,19 @@ __global__ void __launch_bounds__(256) k_sum(Split sp, int64_t d, const float *_
     constexpr int MIX = Coef<HC>::kMix;
     const int CH = (int)sp.channels, FT = HC * CH;
     griddep_wait_then_release();
-    const int64_t b = blockIdx.x, dwb = sp.slices * MIX;
+    const int64_t b = blockIdx.x, dwb = sp.bands * sp.wide * MIX;
     if (b < dwb) {
         const int64_t s = b / MIX;
         const int i = (int)(b % MIX);
-        const int64_t c0 = sp.block_of(s * sp.steps), c1 = sp.block_of((s + 1) * sp.steps - 1);
+        const int64_t band = s / sp.wide, w = s % sp.wide;
+        const int64_t c0 = sp.team_of(band * sp.steps),
+                      c1 = sp.team_of((band + 1) * sp.steps - 1);
         for (int m = threadIdx.x; m < FT; m += 256) {
             const int64_t c = s * CH + m % CH;
             if (c >= d) continue;
             float a = 0.0f;
-            for (int64_t p = c0; p <= c1; ++p) a += dwp[((p + s) * MIX + i) * FT + m];
+            for (int64_t p = c0; p <= c1; ++p)
+                a += dwp[(((p + band) * sp.wide + w) * MIX + i) * FT + m];
             dw[((int64_t)i * HC + m / CH) * d + c] = a;
         }
         return;
@@ -390,7 +393,7 @@ Parts parts(int64_t n, int64_t d) {
     p.mix = up256(HC == 4 && tiles > rows ? tiles : rows);
     p.dw = p.mix + up256((size_t)kMaxBlocks * mix_warps<HC>() * (CF::kMix + 4) * 4);
     auto partial = [](const Split &sp) {
-        return (size_t)(sp.blocks + sp.slices) * CF::kMix * HC * sp.channels * 4;
+        return (size_t)sp.partials() * CF::kMix * HC * sp.channels * 4;
     };
     size_t most = partial(split_dx_dw(n, HC, d, Split::kMaxBlocks));
     if (HC == 4) {
@@ -433,7 +436,7 @@ cudaError_t launch(const PreBackward &p, const DeviceInfo &di, cudaStream_t s) {
     m.split = tiled ? split_dx_dw_tma(p.n, p.d, sms) : split_dx_dw(p.n, HC, p.d, sms);
     e = tiled ? launch_dx_dw_tma(p, m, di, s) : launch_dx_dw(p, m, di, s);
     if (e != cudaSuccess) return e;
-    const int64_t grid = m.split.slices * MIX + (MIX + 3 + 7) / 8;
+    const int64_t grid = m.split.bands * m.split.wide * MIX + (MIX + 3 + 7) / 8;
     return launch_overlapped(k_sum<HC>, dim3((unsigned)grid), dim3(256), 0, s, m.split, p.d, m.dwp,
                              p.dw, blocks * MW, mp, p.dscale, p.dbase);
 }

@@ -47,34 +47,45 @@ struct PreBackward {
     uint8_t *ws;                           // pre_backward_bytes
 };
 
-// How the second kernel's work is cut: slices of channels, each walked in steps
-// of tokens; the steps of all slices in a row (slice-major) are dealt to the
-// blocks in equal runs, so every block has the same work whatever the shape.
-// Block c has steps [c * total / blocks, (c + 1) * total / blocks); the partial
-// sums that it leaves for slice s are number c + s, which no other pair has.
+// How the work on dx and dW is cut: slices of channels, each walked in steps of
+// tokens.  A team of `wide` blocks walks over the same tokens side by side in
+// `wide` neighbouring slices (a band), so that what they read and write of a row
+// at about the same time is one piece of up to 1 KB: DRAM serves pieces of 128
+// bytes at little more than half its rate.  The steps of all bands in a row
+// (band-major) are dealt to the teams in equal runs, so every block has the same
+// work whatever the shape.  Team c has steps [c * total / teams,
+// (c + 1) * total / teams); the partial sums that its block w leaves for band s
+// are number (c + s) * wide + w, which no other block has.
 struct Split {
     static constexpr int kMaxBlocks = 160;
-    int64_t slices, steps, total, blocks, channels;
+    int64_t bands, steps, total, teams;
+    int channels, wide;
     static Split of(int64_t n, int64_t d, int channels, int tokens, int64_t most) {
         Split s;
+        const int64_t slices = (d + channels - 1) / channels;
         s.channels = channels;
-        s.slices = (d + channels - 1) / channels;
+        // the widest team that leaves at most 1/16 of its slices empty
+        s.wide = 4;
+        while (s.wide > 1 && (slices + s.wide - 1) / s.wide * s.wide * 16 > slices * 17) s.wide /= 2;
+        s.bands = (slices + s.wide - 1) / s.wide;
         s.steps = (n + tokens - 1) / tokens;
-        s.total = s.slices * s.steps;
-        s.blocks = s.total < most ? s.total : most;
+        s.total = s.bands * s.steps;
+        s.teams = s.total < most / s.wide ? s.total : most / s.wide;
         return s;
     }
     // (total is below 2^46: n * hc * d is at most 2^58)
-    __host__ __device__ int64_t first(int64_t c) const { return c * total / blocks; }
-    __host__ __device__ int64_t block_of(int64_t step) const {
-        return ((step + 1) * blocks - 1) / total;
+    __host__ __device__ int64_t first(int64_t c) const { return c * total / teams; }
+    __host__ __device__ int64_t team_of(int64_t step) const {
+        return ((step + 1) * teams - 1) / total;
     }
+    __host__ __device__ int64_t blocks() const { return teams * wide; }
+    __host__ __device__ int64_t partials() const { return (teams + bands) * wide; }
 };
 
 struct MainArgs {
     Split split;
     uint8_t *rec;  // per token, or per tile of tokens (Coef)
-    float *dwp;  // [blocks + slices][mix][hc * channels]
+    float *dwp;  // [Split::partials()][mix][hc * channels]
 };
 
 constexpr int kBackwardMaxIters = 256;  // Sinkhorn divisors kept in shared memory

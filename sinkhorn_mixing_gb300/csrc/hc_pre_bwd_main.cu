@@ -172,14 +172,17 @@ __global__ void __launch_bounds__(Cfg<HC, K8>::THREADS, 1) k_dx_dw(Args a) {
     };
 
     bool started = false;  // has this kernel waited for the one before it
-    int64_t step = a.split.first(blockIdx.x);
-    const int64_t end = a.split.first(blockIdx.x + 1);
+    const int64_t team = blockIdx.x / a.split.wide, place = blockIdx.x % a.split.wide;
+    int64_t step = a.split.first(team);
+    const int64_t end = a.split.first(team + 1);
     while (step < end) {
-        const int64_t slice = step / a.split.steps;
-        const int64_t s0 = step - slice * a.split.steps;
+        const int64_t band = step / a.split.steps;
+        const int64_t s0 = step - band * a.split.steps;
         const int64_t s1 = min(a.split.steps, s0 + (end - step));
-        const int64_t ch0 = slice * C::CH;
-        const int width = (int)min((int64_t)C::CH, a.d - ch0);
+        // (a band's last slices may lie behind the last channel: nothing there is read or kept)
+        const int64_t slice = band * a.split.wide + place;
+        const int64_t ch0 = slice * C::CH < a.d ? slice * C::CH : 0;
+        const int width = (int)max((int64_t)0, min((int64_t)C::CH, a.d - slice * C::CH));
 
         // ---- the slice of W, in fp16 times a power of two that brings its largest magnitude
         // to [2^13, 2^14), laid out as the products' B fragments
@@ -532,7 +535,7 @@ __global__ void __launch_bounds__(Cfg<HC, K8>::THREADS, 1) k_dx_dw(Args a) {
         }
         products_done();
         tc_fence_after();
-        drain(s1 - s0 <= kDrain, a.dwp + (blockIdx.x + slice) * (int64_t)C::MIX * C::FT);
+        drain(s1 - s0 <= kDrain, a.dwp + ((team + band) * a.split.wide + place) * C::MIX * C::FT);
         tc_fence_before();
         __syncthreads();  // before W, the operands and the sums are written anew
         tc_fence_after();
@@ -557,7 +560,7 @@ cudaError_t launch(const PreBackward &p, const MainArgs &m, const DeviceInfo &di
     a.g = reinterpret_cast<const uint8_t *>(p.dstream);
     a.dx = reinterpret_cast<uint8_t *>(p.dx), a.rec = m.rec, a.dwp = m.dwp;
     a.err = di.err_word;
-    return launch_overlapped(k_dx_dw<HC, K8>, dim3((unsigned)m.split.blocks), dim3(C::THREADS),
+    return launch_overlapped(k_dx_dw<HC, K8>, dim3((unsigned)m.split.blocks()), dim3(C::THREADS),
                              (size_t)C::SMEM, s, a);
 }
 

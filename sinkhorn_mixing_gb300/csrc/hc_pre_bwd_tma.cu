@@ -107,15 +107,17 @@ __device__ __forceinline__ uint64_t tiles128(uint32_t saddr) {
            ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
 
-// Walks the runs of steps of this block: f(slice, first step, past the last).
+// Walks the runs of steps of this block: f(slice, partial sums, first step,
+// past the last).
 template <typename Fn>
 __device__ __forceinline__ void over_runs(const Split &sp, Fn f) {
-    int64_t step = sp.first(blockIdx.x);
-    const int64_t end = sp.first(blockIdx.x + 1);
+    const int64_t team = blockIdx.x / sp.wide, place = blockIdx.x % sp.wide;
+    int64_t step = sp.first(team);
+    const int64_t end = sp.first(team + 1);
     while (step < end) {
-        const int64_t slice = step / sp.steps, s0 = step - slice * sp.steps;
+        const int64_t band = step / sp.steps, s0 = step - band * sp.steps;
         const int64_t s1 = min(sp.steps, s0 + (end - step));
-        f(slice, s0, s1);
+        f(band * sp.wide + place, (team + band) * sp.wide + place, s0, s1);
         step += s1 - s0;
     }
 }
@@ -174,7 +176,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) {
             griddep_wait_then_release();
             asm volatile("fence.proxy.async;" ::: "memory");  // records were plain stores
-            over_runs(a.split, [&](int64_t slice, int64_t s0, int64_t s1) {
+            over_runs(a.split, [&](int64_t slice, int64_t, int64_t s0, int64_t s1) {
                 for (int64_t s = s0; s < s1; ++s, ++it) {
                     const uint32_t slot = (uint32_t)(it & 1) * 8;
                     if (it >= 2 && !wait(kEmpty + slot, (uint32_t)(it >> 1) - 1)) continue;
@@ -196,7 +198,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp == kComputeWarps + 1) {
         // ---------------------------------------------------- products
-        over_runs(a.split, [&](int64_t, int64_t s0, int64_t s1) {
+        over_runs(a.split, [&](int64_t, int64_t, int64_t s0, int64_t s1) {
             meet<2, 32 * (kComputeWarps + 1)>();  // W of this slice is there
             if (lane == 0) {
                 auto du_w = [&](int64_t i) {
@@ -243,11 +245,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == kComputeWarps + 2) {
         // ------------------------------------------------------ stores
         if (lane == 0) {
-            over_runs(a.split, [&](int64_t slice, int64_t s0, int64_t s1) {
+            over_runs(a.split, [&](int64_t slice, int64_t, int64_t s0, int64_t s1) {
                 for (int64_t s = s0; s < s1; ++s, ++it) {
                     const uint32_t slot = (uint32_t)(it & 1) * 8;
                     if (!wait(kOut + slot, (uint32_t)(it >> 1))) continue;
-                    tma_store_3d(&map_dx, (int)slice * CH, (int)(s * T), 0, stage(it));
+                    if (slice * CH < a.d)  // else behind the last channel (Split)
+                        tma_store_3d(&map_dx, (int)slice * CH, (int)(s * T), 0, stage(it));
                     asm volatile("cp.async.bulk.commit_group;" ::: "memory");
                     asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
                     mbar_arrive(eb + kEmpty + slot);
@@ -269,7 +272,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) mbar_arrive(eb + bar);
         };
         bool started = false;
-        over_runs(a.split, [&](int64_t slice, int64_t s0, int64_t s1) {
+        over_runs(a.split, [&](int64_t slice, int64_t partial, int64_t s0, int64_t s1) {
             const int64_t ch0 = slice * CH;
             const int width = (int)min((int64_t)CH, a.d - ch0);
             // ---- the slice of W in fp16, its largest magnitude brought to [2^13, 2^14): 8 x 8
@@ -450,7 +453,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             wait(kD2Done, (uint32_t)it - 1);
             tc_fence_after();
-            drain(s1 - s0 <= kDrain, a.dwp + (blockIdx.x + slice) * (int64_t)MIX * FT);
+            drain(s1 - s0 <= kDrain, a.dwp + partial * MIX * FT);
             tc_fence_before();
             meet<1, 32 * kComputeWarps>();  // before maxima and W are written anew
         });
@@ -474,7 +477,8 @@ bool stream_map(CUtensorMap *map, const void *p, bool bytes, int64_t n, int64_t 
                map, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
                const_cast<void *>(p), dim, stride, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
                bytes ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
-               CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               // more than a row of the box: what lies behind is read by the team's next block
+               bytes ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -501,7 +505,7 @@ cudaError_t launch(const PreBackward &p, const MainArgs &m, const DeviceInfo &di
     a.n = p.n, a.d = p.d, a.nblk = kept_blocks(p.d);
     a.xs = p.x.scales, a.w = p.w, a.rec = m.rec, a.dwp = m.dwp, a.err = di.err_word;
     a.has_g = p.dstream != nullptr;
-    return launch_overlapped(k_dx_dw_tma<K8>, dim3((unsigned)m.split.blocks), dim3(kThreads),
+    return launch_overlapped(k_dx_dw_tma<K8>, dim3((unsigned)m.split.blocks()), dim3(kThreads),
                              (size_t)L::SMEM, s, g, x, y, dx, a);
 }
 
