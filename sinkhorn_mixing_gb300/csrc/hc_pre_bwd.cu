@@ -79,7 +79,7 @@ __global__ void __launch_bounds__(256 + 32 * mix_warps<HC>(), 3)
                    const float *__restrict__ mixes, const float *__restrict__ scale,
                    const float *__restrict__ base, const float *__restrict__ dpost,
                    const float *__restrict__ dcomb, uint8_t *__restrict__ rec,
-                   int tiled, float *__restrict__ partial) {
+                   int tiled, uint8_t *__restrict__ scales, float *__restrict__ partial) {
     using CF = Coef<HC>;
     constexpr int MIX = CF::kMix, MW = mix_warps<HC>(), THREADS = 256 + 32 * MW;
     __shared__ float sums[2][8][HC + 1];
@@ -120,6 +120,22 @@ __global__ void __launch_bounds__(256 + 32 * mix_warps<HC>(), 3)
                         acc[j] = K8 ? fmaf(sc, sum2(dot), acc[j]) : acc[j] + sum2(dot);
                         acc[HC] = K8 ? fmaf(sc * sc, sum2(sq), acc[HC]) : acc[HC] + sum2(sq);
                     }
+                }
+            }
+            if (HC == 4 && K8 && scales != nullptr && t < n) {
+                // The scales once more, by slices of 64 channels: k_dx_dw_tma reads a slice of
+                // many tokens, and as x has them that would be 2 bytes from each of many rows.
+                const int64_t slices = (nv + 7) / 8;
+                uint2 *to = reinterpret_cast<uint2 *>(scales) + t % kTileTokens +
+                            t / kTileTokens * slices * kTileTokens;
+                for (int64_t c = l; c < slices; c += lanes) {
+                    uint32_t v[HC];
+#pragma unroll
+                    for (int j = 0; j < HC; ++j) {
+                        const uint8_t *p = x.scales + (t * HC + j) * nblk + 2 * c;
+                        v[j] = __ldg(p) | (2 * c + 1 < nblk ? (uint32_t)__ldg(p + 1) << 8 : 0u);
+                    }
+                    to[c * kTileTokens] = make_uint2(v[0] | v[1] << 16, v[2] | v[3] << 16);
                 }
             }
             __syncwarp();
@@ -338,33 +354,34 @@ __global__ void __launch_bounds__(256 + 32 * mix_warps<HC>(), 3)
 }
 
 // ----------------------------------------------------------------- k_sum
-// dW from the partial sums of the blocks that worked on a slice of channels,
-// one block of threads per (slice, mix number); behind those, one warp per
-// column of k_mix_backward's partial sums.
+// dW from the partial sums of the teams that worked on a band, four features a
+// thread; behind those blocks, one warp per column of k_mix_backward's partial
+// sums.
 template <int HC>
-__global__ void __launch_bounds__(256) k_sum(Split sp, int64_t d, const float *__restrict__ dwp,
+__global__ void __launch_bounds__(256) k_sum(Split sp, int64_t d, int per_slice,
+                                             const float *__restrict__ dwp,
                                              float *__restrict__ dw, int rows,
                                              const float *__restrict__ mp,
                                              float *__restrict__ dscale,
                                              float *__restrict__ dbase) {
     constexpr int MIX = Coef<HC>::kMix;
-    const int CH = (int)sp.channels, FT = HC * CH;
+    const int CH = sp.channels, FT = HC * CH;
     griddep_wait_then_release();
-    const int64_t b = blockIdx.x, dwb = sp.bands * sp.wide * MIX;
+    const int64_t b = blockIdx.x, dwb = sp.bands * sp.wide * per_slice;
     if (b < dwb) {
-        const int64_t s = b / MIX;
-        const int i = (int)(b % MIX);
-        const int64_t band = s / sp.wide, w = s % sp.wide;
-        const int64_t c0 = sp.team_of(band * sp.steps),
-                      c1 = sp.team_of((band + 1) * sp.steps - 1);
-        for (int m = threadIdx.x; m < FT; m += 256) {
-            const int64_t c = s * CH + m % CH;
-            if (c >= d) continue;
-            float a = 0.0f;
-            for (int64_t p = c0; p <= c1; ++p)
-                a += dwp[(((p + band) * sp.wide + w) * MIX + i) * FT + m];
-            dw[((int64_t)i * HC + m / CH) * d + c] = a;
+        const int64_t s = b / per_slice, band = s / sp.wide, w = s % sp.wide;
+        const int e = ((int)(b % per_slice) * 256 + (int)threadIdx.x) * 4;
+        const int i = e / FT, m = e % FT;
+        const int64_t c = s * CH + m % CH;
+        if (i >= MIX || c >= d) return;
+        const int64_t c0 = sp.team_of(band * sp.steps), c1 = sp.team_of((band + 1) * sp.steps - 1);
+        float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int64_t p = c0; p <= c1; ++p) {
+            const float4 v = *reinterpret_cast<const float4 *>(
+                dwp + ((p + band) * sp.wide + w) * MIX * FT + e);
+            sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
         }
+        *reinterpret_cast<float4 *>(dw + ((int64_t)i * HC + m / CH) * d + c) = sum;
         return;
     }
     const int lane = threadIdx.x & 31, col = (int)(b - dwb) * 8 + (threadIdx.x >> 5);
@@ -380,7 +397,7 @@ size_t up256(size_t b) { return (b + 255) / 256 * 256; }
 
 // The workspace's parts, in this order.
 struct Parts {
-    size_t rec, mix, dw, end;
+    size_t rec, scales, mix, dw, end;
 };
 template <int HC>
 Parts parts(int64_t n, int64_t d) {
@@ -390,7 +407,10 @@ Parts parts(int64_t n, int64_t d) {
     const size_t tiles = (size_t)((n + kTileTokens - 1) / kTileTokens) * CF::kTileBytes;
     const size_t rows = (size_t)n * CF::kBytes;
     p.rec = 0;
-    p.mix = up256(HC == 4 && tiles > rows ? tiles : rows);
+    p.scales = up256(HC == 4 && tiles > rows ? tiles : rows);
+    p.mix = p.scales + (HC == 4 ? up256((size_t)((n + kTileTokens - 1) / kTileTokens) *
+                                        ((d + 63) / 64) * kTileTokens * 8)
+                                : 0);
     p.dw = p.mix + up256((size_t)kMaxBlocks * mix_warps<HC>() * (CF::kMix + 4) * 4);
     auto partial = [](const Split &sp) {
         return (size_t)sp.partials() * CF::kMix * HC * sp.channels * 4;
@@ -411,6 +431,7 @@ cudaError_t launch(const PreBackward &p, const DeviceInfo &di, cudaStream_t s) {
     const Parts at = parts<HC>(p.n, p.d);
     MainArgs m;
     m.rec = p.ws + at.rec;
+    m.scales = p.ws + at.scales;
     m.dwp = reinterpret_cast<float *>(p.ws + at.dw);
     float *mp = reinterpret_cast<float *>(p.ws + at.mix);
     int lg = 5;
@@ -430,15 +451,16 @@ cudaError_t launch(const PreBackward &p, const DeviceInfo &di, cudaStream_t s) {
     cudaError_t e = launch_overlapped(
         k_mix_backward<HC, K8>, dim3(blocks), dim3(256 + 32 * MW), smem, s, p.n, npad, nv, nblk, lg,
         p.iters, p.eps, p.norm_eps, (float)F, reinterpret_cast<const uint4 *>(p.dy), p.x, p.mixes,
-        p.scale, p.base, p.dpost, p.dcomb, m.rec, (int)tiled, mp);
+        p.scale, p.base, p.dpost, p.dcomb, m.rec, (int)tiled, tiled ? m.scales : nullptr, mp);
     if (e != cudaSuccess) return e;
     const int64_t sms = di.sms < Split::kMaxBlocks ? di.sms : Split::kMaxBlocks;
     m.split = tiled ? split_dx_dw_tma(p.n, p.d, sms) : split_dx_dw(p.n, HC, p.d, sms);
     e = tiled ? launch_dx_dw_tma(p, m, di, s) : launch_dx_dw(p, m, di, s);
     if (e != cudaSuccess) return e;
-    const int64_t grid = m.split.bands * m.split.wide * MIX + (MIX + 3 + 7) / 8;
-    return launch_overlapped(k_sum<HC>, dim3((unsigned)grid), dim3(256), 0, s, m.split, p.d, m.dwp,
-                             p.dw, blocks * MW, mp, p.dscale, p.dbase);
+    const int per_slice = (MIX * HC * m.split.channels / 4 + 255) / 256;
+    const int64_t grid = m.split.bands * m.split.wide * per_slice + (MIX + 3 + 7) / 8;
+    return launch_overlapped(k_sum<HC>, dim3((unsigned)grid), dim3(256), 0, s, m.split, p.d,
+                             per_slice, m.dwp, p.dw, blocks * MW, mp, p.dscale, p.dbase);
 }
 
 }  // namespace

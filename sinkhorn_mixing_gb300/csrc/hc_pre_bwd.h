@@ -84,7 +84,8 @@ struct Split {
 
 struct MainArgs {
     Split split;
-    uint8_t *rec;  // per token, or per tile of tokens (Coef)
+    uint8_t *rec;     // per token, or per tile of tokens (Coef)
+    uint8_t *scales;  // x's scale bytes for the TMA kernel, [tile][64-channel slice][token][copy][2]
     float *dwp;  // [Split::partials()][mix][hc * channels]
 };
 

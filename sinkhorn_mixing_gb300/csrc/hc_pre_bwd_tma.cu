@@ -12,8 +12,9 @@
 //     kept in bf16 (codes are widened into an operand tile on the way), du in
 //     three bf16 parts.
 // The rest is per token and channel: a lane is one token, and its coefficients
-// serve 8 channels of 4 copies.  dx goes over the stage's gradient tile and out
-// by a TMA store.
+// serve 8 channels of 4 copies.  dx leaves by a TMA store, from the stage's
+// gradient tile; of codes, that tile takes the widened x instead and dx has a
+// tile of its own, so that the stage is free once the products are done.
 // Roles: warps 0-15 compute, warp 16 loads (one thread), warp 17 issues the
 // products, warp 18 stores.  Two stages; every wait has a limit, and after one
 // ran out all roles run through without acting, so that all barriers are met.
@@ -36,7 +37,7 @@ template <bool K8>
 struct Lay {
     static constexpr int X = T * FT * (K8 ? 1 : 2), OX = T * FT * 2, OY = OX + X;
     static constexpr int OR = OY + T * CH * 2, STAGE = OR + CF::kTileBytes;
-    static constexpr int OO = 2 * STAGE;                       // x as an operand (K8)
+    static constexpr int OO = 2 * STAGE;                       // dx on its way out (K8)
     static constexpr int OW = OO + (K8 ? T * FT * 2 : 0);      // W, 32 halves a feature
     static constexpr int OS = OW + FT * 64;                    // scales [2][2 blocks][T][4]
     static constexpr int OE = OS + (K8 ? 2 * 2 * T * 16 : 0);  // barriers, flags, maxima
@@ -46,6 +47,7 @@ struct Lay {
 };
 
 enum Bar { kFull = 0, kEmpty = 16, kD1Full = 32, kD1Free = 40, kGate = 48, kD2Done = 56, kOut = 64 };
+constexpr int kOutFree = 168;
 constexpr int kAbort = 80, kTmem = 84, kCalm = 88, kMaxima = 96;
 constexpr int kD2 = 256, kSums = kD2 + 2 * CF::kN;  // TMEM columns; du W has 0..255
 static_assert(kSums + 2 * MIX <= 512, "TMEM");
@@ -56,8 +58,8 @@ constexpr uint32_t kIdescX = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 15) | (
 
 struct Args {
     Split split;
-    int64_t n, d, nblk;
-    const uint8_t *xs;
+    int64_t n, d;
+    const uint8_t *xs;  // [steps][slices][T][4 copies][2 blocks], one slice's of a step together
     const float *w;
     const uint8_t *rec;
     float *dwp;
@@ -88,6 +90,17 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const uint8_t *src, uint
             dst),
         "l"(src), "r"(bytes), "r"(bar)
         : "memory");
+}
+// Has the barrier's phase of this parity ended?  Does not wait.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
 }
 template <int ID, int N>
 __device__ __forceinline__ void meet() {
@@ -139,13 +152,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(eb + kFull + 8 * i, 1);
-            mbar_init(eb + kEmpty + 8 * i, 2);
+            mbar_init(eb + kEmpty + 8 * i, K8 ? 1 : 2);  // products; and the store
             mbar_init(eb + kOut + 8 * i, kComputeWarps);
         }
         mbar_init(eb + kD1Full, 1);
         mbar_init(eb + kD1Free, kComputeWarps);
         mbar_init(eb + kGate, kComputeWarps);
         mbar_init(eb + kD2Done, 1);
+        mbar_init(eb + kOutFree, 1);
         *abort = 0;
         *calm = 0;
         if ((sb & 1023u) != 0) {  // swizzled tiles need it
@@ -165,9 +179,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    // wait_bar reads the timer, which takes long, so the waits of a healthy run end before it
     auto wait = [&](uint32_t bar, uint32_t parity) {
+#pragma unroll 1
+        for (int i = 0; i < 64; ++i)
+            if (mbar_try(eb + bar, parity & 1)) return true;
         return wait_bar<false>(eb + bar, parity & 1, abort, a.err);
     };
+    auto test = [&](uint32_t bar, uint32_t parity) { return mbar_test(eb + bar, parity & 1); };
     auto stage = [&](int64_t it) { return sb + (uint32_t)(it & 1) * L::STAGE; };
     int64_t it = 0;  // steps of this block so far: stage it & 1, its use it >> 1
 
@@ -201,37 +220,58 @@ __global__ void __launch_bounds__(kThreads, 1)
         over_runs(a.split, [&](int64_t, int64_t, int64_t s0, int64_t s1) {
             meet<2, 32 * (kComputeWarps + 1)>();  // W of this slice is there
             if (lane == 0) {
-                auto du_w = [&](int64_t i) {
-                    bool ok = wait(kFull + (uint32_t)(i & 1) * 8, (uint32_t)(i >> 1));
-                    if (i > 0) ok = wait(kD1Free, (uint32_t)(i - 1)) && ok;
-                    if (!ok) return;
-                    tc_fence_after();
-                    const uint32_t ao = stage(i) + L::OR + T * CF::kPairBytes;
+                // Both products of a step as soon as each can go: du^T x must not wait for the
+                // next step's tiles (its stage would not be loaded meanwhile), nor du W of the
+                // next step for this one's operand.
+                const int64_t i0 = it, end = it + (s1 - s0);
+                int64_t next = it;  // step of du W; `it` that of du^T x
+                uint64_t since = 0;  // the timer at the first of many idle rounds
+                uint32_t rounds = 0;
+                while (it < end) {
+                    bool idle = true;
+                    if (next < end && next <= it + 1 &&
+                        test(kFull + (uint32_t)(next & 1) * 8, (uint32_t)(next >> 1)) &&
+                        (next == 0 || test(kD1Free, (uint32_t)(next - 1)))) {
+                        tc_fence_after();
+                        const uint32_t ao = stage(next) + L::OR + T * CF::kPairBytes;
 #pragma unroll
-                    for (int ks = 0; ks < CF::kK / 16; ++ks)
-                        mma_bf16(tmem, rows16(ao + ks * 256, 128, 512),
-                                 rows16(sb + L::OW + ks * 256, 128, 512), kIdescW, ks > 0);
-                    mma_commit(eb + kD1Full);
-                };
-                du_w(it);
-                for (int64_t s = s0; s < s1; ++s, ++it) {
-                    if (s + 1 < s1) du_w(it + 1);
-                    if (!wait(kGate, (uint32_t)it)) continue;
-                    tc_fence_after();
-                    const uint32_t xo = K8 ? sb + L::OO : stage(it) + L::OX;
-                    const uint32_t bo =
-                        stage(it) + L::OR + T * CF::kPairBytes + 2 * T * CF::kKBytes;
+                        for (int ks = 0; ks < CF::kK / 16; ++ks)
+                            mma_bf16(tmem, rows16(ao + ks * 256, 128, 512),
+                                     rows16(sb + L::OW + ks * 256, 128, 512), kIdescW, ks > 0);
+                        mma_commit(eb + kD1Full);
+                        ++next;
+                        idle = false;
+                    }
+                    if (it < next && test(kGate, (uint32_t)it)) {
+                        tc_fence_after();
+                        const uint32_t xo = stage(it) + (K8 ? 0 : L::OX);
+                        const uint32_t bo =
+                            stage(it) + L::OR + T * CF::kPairBytes + 2 * T * CF::kKBytes;
 #pragma unroll
-                    for (int ks = 0; ks < T / 16; ++ks)
+                        for (int ks = 0; ks < T / 16; ++ks)
 #pragma unroll
-                        for (int m = 0; m < 2; ++m)
-                            mma_bf16(tmem + kD2 + m * CF::kN,
-                                     tiles128(xo + m * 2 * T * 128 + ks * 2048),
-                                     rows16(bo + ks * 256, 128, T / 8 * 128), kIdescX,
-                                     (s - s0) % kDrain != 0 || ks > 0);
-                    mma_commit(eb + kD2Done);
-                    mma_commit(eb + kEmpty + (uint32_t)(it & 1) * 8);
+                            for (int m = 0; m < 2; ++m)
+                                mma_bf16(tmem + kD2 + m * CF::kN,
+                                         tiles128(xo + m * 2 * T * 128 + ks * 2048),
+                                         rows16(bo + ks * 256, 128, T / 8 * 128), kIdescX,
+                                         (it - i0) % kDrain != 0 || ks > 0);
+                        mma_commit(eb + kD2Done);
+                        mma_commit(eb + kEmpty + (uint32_t)(it & 1) * 8);
+                        ++it;
+                        idle = false;
+                    }
+                    rounds = idle ? rounds + 1 : 0;
+                    if (idle) __nanosleep(40);  // the scheduler's other warps compute
+                    if (rounds != 0 && rounds % 4096 == 0) {
+                        if (*abort) break;
+                        if (rounds == 4096) since = gtimer();
+                        if (gtimer() - since > kTimeoutNs) {
+                            *abort = 1;
+                            atomicOr(a.err, kErrWaitTimeout);
+                        }
+                    }
                 }
+                it = end;
             }
             __syncwarp();
         });
@@ -250,10 +290,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint32_t slot = (uint32_t)(it & 1) * 8;
                     if (!wait(kOut + slot, (uint32_t)(it >> 1))) continue;
                     if (slice * CH < a.d)  // else behind the last channel (Split)
-                        tma_store_3d(&map_dx, (int)slice * CH, (int)(s * T), 0, stage(it));
+                        tma_store_3d(&map_dx, (int)slice * CH, (int)(s * T), 0,
+                                     K8 ? sb + L::OO : stage(it));
                     asm volatile("cp.async.bulk.commit_group;" ::: "memory");
                     asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-                    mbar_arrive(eb + kEmpty + slot);
+                    mbar_arrive(eb + (K8 ? kOutFree : kEmpty + slot));
                 }
             });
             asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
@@ -308,14 +349,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                 started = true;
             }
 
-            // ---- scales: one a thread, a step ahead, shared through [block][token][copy]
+            // ---- scales: one a thread, loaded two steps ahead and passed on one step ahead
+            // through [block][token][copy].  Every warp reads a step's scales before it arrives
+            // at that step's kD1Free and writes the next one's behind its own read, so a phase
+            // of that barrier says both that they are there and that the other half is free.
             const int sct = tid >> 3, scj = tid >> 1 & 3, scb = tid & 1;
-            const bool sin = K8 && scb * 32 < width;
-            const uint8_t *sp = a.xs + ((s0 * T + sct) * 4 + scj) * a.nblk + ch0 / 32 + scb;
+            const int64_t slices = (a.d + CH - 1) / CH;
+            const uint8_t *sp = a.xs + (s0 * slices + slice) * (T * 8) + tid;
             auto load_scale = [&](int64_t s) -> uint32_t {
                 uint32_t v = 0;
-                if (sin && s * T + sct < a.n) v = __ldg(sp);
-                sp += T * 4 * a.nblk;
+                if (K8 && slice < slices && s * T + sct < a.n) v = __ldg(sp);
+                sp += slices * (T * 8);
                 return v;
             };
             auto keep_scale = [&](int64_t i, uint32_t v) {
@@ -358,14 +402,23 @@ __global__ void __launch_bounds__(kThreads, 1)
 
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             keep_scale(it, load_scale(s0));
+            uint32_t next_scale = s0 + 1 < s1 ? load_scale(s0 + 1) : 0;
             meet<2, 32 * (kComputeWarps + 1)>();
             for (int64_t s = s0; s < s1; ++s, ++it) {
                 const uint32_t st = stage(it), slot = (uint32_t)(it & 1) * 8;
-                uint32_t next_scale = 0;
-                if (K8 && s + 1 < s1) next_scale = load_scale(s + 1);
                 wait(kFull + slot, (uint32_t)(it >> 1));
                 wait(kD1Full, (uint32_t)it);
                 tc_fence_after();
+                float4 sc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (K8) {
+                    if (it > 0) wait(kD1Free, (uint32_t)it - 1);
+                    const uint4 u = lds128(sb + L::OS + (uint32_t)(it & 1) * (2 * T * 16) +
+                                           ((cg >> 2) * T + tl) * 16);
+                    sc = make_float4(__uint_as_float(u.x), __uint_as_float(u.y),
+                                     __uint_as_float(u.z), __uint_as_float(u.w));
+                    keep_scale(it + 1, next_scale);
+                    if (s + 2 < s1) next_scale = load_scale(s + 2);
+                }
                 // ---- du W of this token
                 uint64_t v[4][4], qq, ff;
                 const uint32_t cfa = st + L::OR + tl * CF::kPairBytes;
@@ -386,45 +439,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int p = 0; p < 4; ++p)
                             v[j][p] = fmul2(pack2(acc[j][2 * p], acc[j][2 * p + 1]), ff);
                 }
-                // ---- x, and its operand once the products before have been through it
+                // ---- the products before have to be through before their sums move, and before
+                // the next ones may go
                 if (it > 0) wait(kD2Done, (uint32_t)it - 1);
                 if (s > s0 && (s - s0) % kDrain == 0) {
                     tc_fence_after();
                     drain(s - s0 == kDrain, nullptr);
                     tc_fence_before();
                 }
-                if (K8) meet<1, 32 * kComputeWarps>();  // all scales of the step are there
-                float4 sc;
-                if (K8) {
-                    const uint4 u = lds128(sb + L::OS + (uint32_t)(it & 1) * (2 * T * 16) +
-                                           ((cg >> 2) * T + tl) * 16);
-                    sc = make_float4(__uint_as_float(u.x), __uint_as_float(u.y),
-                                     __uint_as_float(u.z), __uint_as_float(u.w));
-                }
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    uint64_t xv[4];
-                    if (K8) {
-                        const float f1 = j == 0 ? sc.x : j == 1 ? sc.y : j == 2 ? sc.z : sc.w;
-                        const uint64_t f2 = pack2(f1, f1);
-                        float f[8];
-                        e4m3x8_to_float(lds64(st + L::OX + j * T * 64 + row8), f);
-#pragma unroll
-                        for (int p = 0; p < 4; ++p)
-                            xv[p] = fmul2(pack2(f[2 * p], f[2 * p + 1]), f2);
-                        sts128(sb + L::OO + j * T * 128 + row,
-                               make_uint4(pack_pair(xv[0]), pack_pair(xv[1]), pack_pair(xv[2]),
-                                          pack_pair(xv[3])));
-                    } else {
-                        const uint4 u = lds128(st + L::OX + j * T * 128 + row);
-                        xv[0] = bf16x2_to_f32x2(u.x), xv[1] = bf16x2_to_f32x2(u.y);
-                        xv[2] = bf16x2_to_f32x2(u.z), xv[3] = bf16x2_to_f32x2(u.w);
-                    }
-#pragma unroll
-                    for (int p = 0; p < 4; ++p) ffma2(v[j][p], qq, xv[p]);
-                }
-                if (K8) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                arrive(kGate);
+                if (!K8) arrive(kGate);  // x is its own operand
                 // ---- the stream's gradient through comb, and y's through pre
                 auto add = [&](uint32_t coef, const uint4 &u) {
                     uint64_t c[4];
@@ -442,14 +465,42 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int k = 0; k < 4; ++k) add(cfa + k * 32, lds128(st + k * T * 128 + row));
                 }
                 add(cfa + CF::kPre * 8, lds128(st + L::OY + row));
+                // ---- x; widened codes go over the gradient's tile, which this lane has read
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    uint64_t xv[4];
+                    if (K8) {
+                        const float f1 = j == 0 ? sc.x : j == 1 ? sc.y : j == 2 ? sc.z : sc.w;
+                        const uint64_t f2 = pack2(f1, f1);
+                        float f[8];
+                        e4m3x8_to_float(lds64(st + L::OX + j * T * 64 + row8), f);
+#pragma unroll
+                        for (int p = 0; p < 4; ++p)
+                            xv[p] = fmul2(pack2(f[2 * p], f[2 * p + 1]), f2);
+                        sts128(st + j * T * 128 + row,
+                               make_uint4(pack_pair(xv[0]), pack_pair(xv[1]), pack_pair(xv[2]),
+                                          pack_pair(xv[3])));
+                    } else {
+                        const uint4 u = lds128(st + L::OX + j * T * 128 + row);
+                        xv[0] = bf16x2_to_f32x2(u.x), xv[1] = bf16x2_to_f32x2(u.y);
+                        xv[2] = bf16x2_to_f32x2(u.z), xv[3] = bf16x2_to_f32x2(u.w);
+                    }
+#pragma unroll
+                    for (int p = 0; p < 4; ++p) ffma2(v[j][p], qq, xv[p]);
+                }
+                if (K8) {
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    arrive(kGate);
+                    if (it > 0) wait(kOutFree, (uint32_t)it - 1);
+                }
+                const uint32_t out = K8 ? sb + L::OO : st;
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    sts128(st + j * T * 128 + row,
+                    sts128(out + j * T * 128 + row,
                            make_uint4(pack_pair(v[j][0]), pack_pair(v[j][1]), pack_pair(v[j][2]),
                                       pack_pair(v[j][3])));
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 arrive(kOut + slot);
-                keep_scale(it + 1, next_scale);
             }
             wait(kD2Done, (uint32_t)it - 1);
             tc_fence_after();
@@ -502,8 +553,8 @@ cudaError_t launch(const PreBackward &p, const MainArgs &m, const DeviceInfo &di
         return cudaErrorInvalidValue;
     Args a;
     a.split = m.split;
-    a.n = p.n, a.d = p.d, a.nblk = kept_blocks(p.d);
-    a.xs = p.x.scales, a.w = p.w, a.rec = m.rec, a.dwp = m.dwp, a.err = di.err_word;
+    a.n = p.n, a.d = p.d;
+    a.xs = m.scales, a.w = p.w, a.rec = m.rec, a.dwp = m.dwp, a.err = di.err_word;
     a.has_g = p.dstream != nullptr;
     return launch_overlapped(k_dx_dw_tma<K8>, dim3((unsigned)m.split.blocks()), dim3(kThreads),
                              (size_t)L::SMEM, s, g, x, y, dx, a);
