@@ -47,12 +47,14 @@ struct Cfg {
     using CF = Coef<HC>;
     static constexpr int T = HC == 4 ? 32 : 16, CH = HC == 4 ? 128 : 64, FT = HC * CH;
     static constexpr int MIX = CF::kMix, KS = CF::kK / 16;
-    // a warp: 16 tokens, 16 channels, 4 copies; a lane of it 2 tokens, 4 channels
-    static constexpr int MT = T / 16, GROUPS = CH / 16, JQ = HC / 4, WARPS = MT * GROUPS * JQ;
+    // a warp: 16 tokens, 16 channels, NJ copies; a lane of it 2 tokens, 4 channels.  16 warps
+    // (at hc = 8 with 4 copies there would be 8, and each step took twice as long)
+    static constexpr int NJ = HC == 4 ? 4 : 2;
+    static constexpr int MT = T / 16, GROUPS = CH / 16, JQ = HC / NJ, WARPS = MT * GROUPS * JQ;
     static constexpr int THREADS = 32 * WARPS, MTILES = FT / 128;
-    static constexpr int PW = MTILES * 4 / WARPS;  // tiles of dW whose lanes a warp reads
+    static_assert(WARPS == 4 * MTILES, "a warp reads 32 lanes of one tile of dW");
     static constexpr int SUMS = MTILES * CF::kN;   // TMEM columns of the drained sums
-    static_assert(SUMS + MTILES / PW * CF::kMix <= 512, "TMEM");
+    static constexpr int SUMT = (512 - SUMS) / CF::kMix;  // tiles that find room there
     // Row pitches: a token's row is moved on by as many bytes as the lanes of one token read at
     // once, so that the lanes of neighbouring tokens meet in no bank.
     static constexpr int GP = HC * CH * 2 + 32, YP = CH * 2 + 32, XP = HC * CH + 16;
@@ -344,53 +346,57 @@ __global__ void __launch_bounds__(Cfg<HC, K8>::THREADS, 1) k_dx_dw(Args a) {
 
         // The tensor core rounds its running sums toward zero, which over many steps adds up to
         // more than binary32's own rounding.  So every kDrain steps the sums move on: into TMEM
-        // columns of their own, or (a warp's second tile at HC = 8) registers, added there with
-        // rounding to nearest; the products then start anew.  `out` takes the result instead.
-        float more[C::PW > 1 ? C::MIX : 1];
-        auto drain = [&](bool first, float *out) {
+        // columns of their own or, where those are taken (two of the tiles at HC = 8), to the
+        // place of the run's result, added there with rounding to nearest; the products then
+        // start anew.
+        float *const result = a.dwp + ((team + band) * a.split.wide + place) * C::MIX * C::FT;
+        auto drain = [&](bool first, bool last) {
+            const int m = warp >> 2;
+            const bool inside = m < C::SUMT;
+            const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);
+            const uint32_t ta = lanes + m * CF::kN, ts = lanes + C::SUMS + m * C::MIX;
+            float *of = result + m * 128 + (warp & 3) * 32 + lane;
+#pragma unroll 1
+            for (int c = 0; c < C::MIX; c += 8, of += 8 * C::FT) {
+                float v[8], u[8], w[8], sum[8];
+                tmem_ld8(ta + c, v);
+                if (CF::kProducts == 1) {
+                    tmem_ld8(ta + C::MIX + c, u);
+                    tmem_ld8(ta + 2 * C::MIX + c, w);
+                }
+                if (!first) {
+                    if (inside) {
+                        tmem_ld8(ts + c, sum);
+                    } else {
 #pragma unroll
-            for (int q = 0; q < C::PW; ++q) {
-                const int m = (warp >> 2) + q * (C::WARPS / 4);
-                const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);
-                const uint32_t ta = lanes + m * CF::kN, ts = lanes + C::SUMS + m * C::MIX;
-#pragma unroll
-                for (int c = 0; c < C::MIX; c += 8) {
-                    float v[8], u[8], w[8], sum[8];
-                    tmem_ld8(ta + c, v);
-                    if (CF::kProducts == 1) {
-                        tmem_ld8(ta + C::MIX + c, u);
-                        tmem_ld8(ta + 2 * C::MIX + c, w);
+                        for (int e = 0; e < 8; ++e) sum[e] = of[e * C::FT];
                     }
-                    if (!first && q == 0) tmem_ld8(ts + c, sum);
-                    tmem_ld_wait();
-                    arrived<8>(v);
-                    if (CF::kProducts == 1) {
-                        arrived<8>(u);
-                        arrived<8>(w);
+                }
+                tmem_ld_wait();
+                arrived<8>(v);
+                if (CF::kProducts == 1) {
+                    arrived<8>(u);
+                    arrived<8>(w);
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) v[e] += u[e] + w[e];
-                    }
-                    if (!first && q == 0) arrived<8>(sum);
+                    for (int e = 0; e < 8; ++e) v[e] += u[e] + w[e];
+                }
+                if (!first) {
+                    arrived<8>(sum);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        if (q > 0) sum[e] = more[c + e];
-                        if (!first) v[e] += sum[e];
-                        if (q > 0) more[c + e] = v[e];
-                    }
-                    if (out != nullptr) {
+                    for (int e = 0; e < 8; ++e) v[e] += sum[e];
+                }
+                if (last || !inside) {
 #pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            out[(int64_t)(c + e) * C::FT + m * 128 + (warp & 3) * 32 + lane] = v[e];
-                    } else if (q == 0) {
-                        tmem_st8(ts + c, v);
-                    }
+                    for (int e = 0; e < 8; ++e) of[e * C::FT] = v[e];
+                } else {
+                    tmem_st8(ts + c, v);
                 }
             }
             tmem_st_wait();
         };
 
         uint8_t *dxp =
-            a.dx + ((s0 * C::T + mt * 16 + tg) * F + jq * 4 * a.d + ch0 + (cl < width ? cl : 0)) * 2;
+            a.dx + ((s0 * C::T + mt * 16 + tg) * F + jq * C::NJ * a.d + ch0 + (cl < width ? cl : 0)) * 2;
         load(s0, 0);
         keep_scale(s0, load_scale(s0));
         for (int64_t s = s0; s < s1; ++s) {
@@ -404,7 +410,7 @@ __global__ void __launch_bounds__(Cfg<HC, K8>::THREADS, 1) k_dx_dw(Args a) {
                 products_done();  // of step s - 1, whose x is loaded over
                 if (full) {
                     tc_fence_after();
-                    drain(rel == kDrain, nullptr);
+                    drain(rel == kDrain, false);
                     tc_fence_before();
                     __syncthreads();
                 }
@@ -422,7 +428,7 @@ __global__ void __launch_bounds__(Cfg<HC, K8>::THREADS, 1) k_dx_dw(Args a) {
 
             // ---- du W
             const uint32_t st = sb + (uint32_t)(s & 1) * C::STAGE;
-            float acc[4][2][4];
+            float acc[C::NJ][2][4];
             uint32_t af[C::KS][4];
 #pragma unroll
             for (int ks = 0; ks < C::KS; ++ks) {
@@ -433,12 +439,12 @@ __global__ void __launch_bounds__(Cfg<HC, K8>::THREADS, 1) k_dx_dw(Args a) {
                              : "r"(ad));
             }
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
+            for (int j = 0; j < C::NJ; ++j)
 #pragma unroll
                 for (int p = 0; p < 2; ++p) {
                     const uint32_t wa =
                         sb + C::OW +
-                        ((((jq * 4 + j) * C::GROUPS + grp) * 2 + p) * 32 + lane) * C::WREG * 4;
+                        ((((jq * C::NJ + j) * C::GROUPS + grp) * 2 + p) * 32 + lane) * C::WREG * 4;
                     if (C::KS == 2) {
                         const uint4 b = lds128(wa);
                         mma_f16<true>(acc[j][p], af[0], b.x, b.y);
@@ -459,22 +465,22 @@ __global__ void __launch_bounds__(Cfg<HC, K8>::THREADS, 1) k_dx_dw(Args a) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int t = mt * 16 + h * 8 + tg;
-                const uint32_t cfa = st + C::SC + t * C::CP + jq * 32;
-                uint64_t v[4][2], qq, ff;
+                const uint32_t cfa = st + C::SC + t * C::CP + jq * C::NJ * 8;
+                uint64_t v[C::NJ][2], qq, ff;
                 lds_pairs(st + C::SC + t * C::CP + CF::kQ * 8, qq, ff);
                 ff = fmul2(ff, wdown2);
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
+                for (int j = 0; j < C::NJ; ++j)
 #pragma unroll
                     for (int p = 0; p < 2; ++p)
                         v[j][p] = fmul2(pack2(acc[j][p][2 * h], acc[j][p][2 * h + 1]), ff);
                 auto add = [&](uint32_t coef, const uint2 &u) {  // v_j += coef_j u
-                    uint64_t c[4];
-                    lds_pairs(coef, c[0], c[1]);
-                    lds_pairs(coef + 16, c[2], c[3]);
+                    uint64_t c[C::NJ];
+#pragma unroll
+                    for (int j = 0; j < C::NJ; j += 2) lds_pairs(coef + j * 8, c[j], c[j + 1]);
                     const uint64_t lo = bf16x2_to_f32x2(u.x), hi = bf16x2_to_f32x2(u.y);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
+                    for (int j = 0; j < C::NJ; ++j) {
                         ffma2(v[j][0], c[j], lo);
                         ffma2(v[j][1], c[j], hi);
                     }
@@ -489,15 +495,16 @@ __global__ void __launch_bounds__(Cfg<HC, K8>::THREADS, 1) k_dx_dw(Args a) {
                 if (K8 && h == 0) products_done();
                 const uint32_t in = cl < width && (s * C::T + t < a.n);
                 uint8_t *p = dxp + h * 16 * F;
-                uint64_t sc[4];
+                uint64_t sc[C::NJ];
                 if (K8) {
-                    const uint32_t sa = st + C::SS + ((t * (C::CH / 32) + cl / 32) * HC + jq * 4) * 8;
-                    lds_pairs(sa, sc[0], sc[1]);
-                    lds_pairs(sa + 16, sc[2], sc[3]);
+                    const uint32_t sa =
+                        st + C::SS + ((t * (C::CH / 32) + cl / 32) * HC + jq * C::NJ) * 8;
+#pragma unroll
+                    for (int j = 0; j < C::NJ; j += 2) lds_pairs(sa + j * 8, sc[j], sc[j + 1]);
                 }
 #pragma unroll
-                for (int j = 0; j < 4; ++j, p += a.d * 2) {
-                    const int jj = jq * 4 + j;
+                for (int j = 0; j < C::NJ; ++j, p += a.d * 2) {
+                    const int jj = jq * C::NJ + j;
                     const uint32_t oa = (jj * (C::CH / 8) + grp * 2 + (tl >> 1)) * C::OT + t / 8 * 128 +
                                         t % 8 * 16 + (tl & 1) * 8;
                     uint64_t xv[2];
@@ -520,7 +527,7 @@ __global__ void __launch_bounds__(Cfg<HC, K8>::THREADS, 1) k_dx_dw(Args a) {
             if (s + 1 < s1) keep_scale(s + 1, next_scale);
             if (K8 && full) {  // the products up to step s - 1 are done
                 tc_fence_after();
-                drain(rel == kDrain, nullptr);
+                drain(rel == kDrain, false);
             }
         }
         if (K8) {  // the last step's products
@@ -535,7 +542,7 @@ __global__ void __launch_bounds__(Cfg<HC, K8>::THREADS, 1) k_dx_dw(Args a) {
         }
         products_done();
         tc_fence_after();
-        drain(s1 - s0 <= kDrain, a.dwp + ((team + band) * a.split.wide + place) * C::MIX * C::FT);
+        drain(s1 - s0 <= kDrain, true);
         tc_fence_before();
         __syncthreads();  // before W, the operands and the sums are written anew
         tc_fence_after();
