@@ -356,8 +356,15 @@ KEPT_BLOCK = 32  # channels that share a scale byte (hcmix.h, hc_checkpoint)
 _BF16, _F32, _F8, _U8 = torch.bfloat16, torch.float32, torch.float8_e4m3fn, torch.uint8
 
 
-def _sized(t, name, count, dtype, dev):
-    _need(t, name, dtype, dev)
+def _on(t, name, dtype, index):
+    """_need on device `index`, in fewer steps."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != index or \
+            not t.is_contiguous():
+        _need(t, name, dtype, torch.device("cuda", index))
+
+
+def _sized(t, name, count, dtype, index):
+    _on(t, name, dtype, index)
     if t.numel() != count:
         raise ValueError("%s must hold %d values, got %d" % (name, count, t.numel()))
     return t.data_ptr()
@@ -372,36 +379,36 @@ def _made(t, name, shape, dtype, dev, stream):
         if stream is not None:
             t.record_stream(stream)
         return t
-    _need(t, name, dtype, dev)
+    _on(t, name, dtype, dev.index)
     if t.shape != shape:
-        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+        raise ValueError("%s must have shape %s, got %s" % (name, shape, tuple(t.shape)))
     return t
 
 
-def _kept(t, name, shape, dev):
+def _kept(t, name, shape, index):
     """A kept tensor of `shape`, bf16 or (codes, scales): the pointers to its
     data and to its scales (None)."""
     if isinstance(t, torch.Tensor):
-        _need(t, name, _BF16, dev)
+        _on(t, name, _BF16, index)
         if t.shape != shape:
-            raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+            raise ValueError("%s must have shape %s, got %s" % (name, shape, tuple(t.shape)))
         return t.data_ptr(), None
     if not isinstance(t, (tuple, list)) or len(t) != 2:
         raise TypeError("%s must be a bf16 tensor or (codes, scales)" % name)
     codes, scales = t
-    _need(codes, name + " codes", _F8, dev)
-    _need(scales, name + " scales", _U8, dev)
+    _on(codes, name + " codes", _F8, index)
+    _on(scales, name + " scales", _U8, index)
     if codes.shape != shape:
-        raise ValueError("%s codes must have shape %s, got %s" % (name, tuple(shape),
-                                                                  tuple(codes.shape)))
-    if scales.shape != shape[:-1] + ((shape[-1] + KEPT_BLOCK - 1) // KEPT_BLOCK,):
-        raise ValueError("%s scales must have shape %s, got %s" % (
-            name, tuple(shape[:-1]) + (-(-shape[-1] // KEPT_BLOCK),), tuple(scales.shape)))
+        raise ValueError("%s codes must have shape %s, got %s" % (name, shape, tuple(codes.shape)))
+    want = shape[:-1] + ((shape[-1] + KEPT_BLOCK - 1) // KEPT_BLOCK,)
+    if scales.shape != want:
+        raise ValueError("%s scales must have shape %s, got %s" % (name, want,
+                                                                   tuple(scales.shape)))
     return codes.data_ptr(), scales.data_ptr()
 
 
 def _rows_of(t):
-    shape = t.shape
+    shape = tuple(t.shape)
     if len(shape) < 1:
         raise ValueError("a row of channels at least is needed")
     d = shape[-1]
@@ -412,7 +419,7 @@ def _rows_of(t):
 
 
 def _tokens_of(t):
-    shape = t.shape
+    shape = tuple(t.shape)
     if len(shape) < 2:
         raise ValueError("a stream must be [..., hc, d]")
     n = 1
@@ -456,7 +463,7 @@ def hc_restore(codes, scales, x=None, stream=None):
     _need(codes, "codes", _F8)
     dev = codes.device
     shape, n, d = _rows_of(codes)
-    cp, sp = _kept((codes, scales), "x", shape, dev)
+    cp, sp = _kept((codes, scales), "x", shape, dev.index)
     x = _made(x, "x", shape, _BF16, dev, stream)
     _run("hc_restore", dev, stream, n, d, cp, sp, x.data_ptr())
     return x
@@ -467,8 +474,8 @@ def hc_pre_restore(codes, scales, pre, y=None, stream=None):
     _need(codes, "codes", _F8)
     dev = codes.device
     shape, n, hc, d = _tokens_of(codes)
-    cp, sp = _kept((codes, scales), "x", shape, dev)
-    pp = _sized(pre, "pre", n * hc, _F32, dev)
+    cp, sp = _kept((codes, scales), "x", shape, dev.index)
+    pp = _sized(pre, "pre", n * hc, _F32, dev.index)
     y = _made(y, "y", shape[:-2] + (d,), _BF16, dev, stream)
     _run("hc_pre_restore", dev, stream, n, hc, d, cp, sp, pp, y.data_ptr())
     return y
@@ -480,9 +487,9 @@ def hc_post_checkpoint(out, residual, post, comb, y=None, codes=None, scales=Non
     _need(residual, "residual", _BF16)
     dev = residual.device
     shape, n, hc, d = _tokens_of(residual)
-    op = _sized(out, "out", n * d, _BF16, dev)
-    pp = _sized(post, "post", n * hc, _F32, dev)
-    cb = _sized(comb, "comb", n * hc * hc, _F32, dev)
+    op = _sized(out, "out", n * d, _BF16, dev.index)
+    pp = _sized(post, "post", n * hc, _F32, dev.index)
+    cb = _sized(comb, "comb", n * hc * hc, _F32, dev.index)
     y = _made(y, "y", shape, _BF16, dev, stream)
     codes = _made(codes, "codes", shape, _F8, dev, stream)
     scales = _made(scales, "scales", shape[:-1] + ((d + KEPT_BLOCK - 1) // KEPT_BLOCK,), _U8, dev,
@@ -501,10 +508,10 @@ def hc_post_backward(dy, out, residual, post, comb, want_dresidual: bool = False
     dev = dy.device
     shape, n, hc, d = _tokens_of(dy)
     lead = shape[:-2]
-    op, osp = _kept(out, "out", lead + (d,), dev)
-    rp, rsp = _kept(residual, "residual", shape, dev)
-    pp = _sized(post, "post", n * hc, _F32, dev)
-    cb = _sized(comb, "comb", n * hc * hc, _F32, dev)
+    op, osp = _kept(out, "out", lead + (d,), dev.index)
+    rp, rsp = _kept(residual, "residual", shape, dev.index)
+    pp = _sized(post, "post", n * hc, _F32, dev.index)
+    cb = _sized(comb, "comb", n * hc * hc, _F32, dev.index)
     dout = _made(dout, "dout", lead + (d,), _BF16, dev, stream)
     dpost = _made(dpost, "dpost", lead + (hc,), _F32, dev, stream)
     dcomb = _made(dcomb, "dcomb", lead + (hc, hc), _F32, dev, stream)
@@ -536,18 +543,17 @@ def hc_mixes_pre_backward(dy, x, mixes, w_mix, hc_scale, hc_base, dpost, dcomb, 
     if not isinstance(data, torch.Tensor):
         raise TypeError("x must be a bf16 tensor or (codes, scales)")
     shape, n, hc, d = _tokens_of(data)
-    xp, xsp = _kept(x, "x", shape, dev)
+    xp, xsp = _kept(x, "x", shape, dev.index)
     mix, F = (2 + hc) * hc, hc * d
     if dy.shape != shape[:-2] + (d,):
-        raise ValueError("dy must have shape %s, got %s" % (tuple(shape[:-2]) + (d,),
-                                                            tuple(dy.shape)))
-    mp = _sized(mixes, "mixes", n * mix, _F32, dev)
-    wp = _sized(w_mix, "w_mix", mix * F, _F32, dev)
-    sp = _sized(hc_scale, "hc_scale", 3, _F32, dev)
-    bp = _sized(hc_base, "hc_base", mix, _F32, dev)
-    pp = _sized(dpost, "dpost", n * hc, _F32, dev)
-    cp = _sized(dcomb, "dcomb", n * hc * hc, _F32, dev)
-    gp = None if dstream is None else _sized(dstream, "dstream", n * F, _BF16, dev)
+        raise ValueError("dy must have shape %s, got %s" % (shape[:-2] + (d,), tuple(dy.shape)))
+    mp = _sized(mixes, "mixes", n * mix, _F32, dev.index)
+    wp = _sized(w_mix, "w_mix", mix * F, _F32, dev.index)
+    sp = _sized(hc_scale, "hc_scale", 3, _F32, dev.index)
+    bp = _sized(hc_base, "hc_base", mix, _F32, dev.index)
+    pp = _sized(dpost, "dpost", n * hc, _F32, dev.index)
+    cp = _sized(dcomb, "dcomb", n * hc * hc, _F32, dev.index)
+    gp = None if dstream is None else _sized(dstream, "dstream", n * F, _BF16, dev.index)
     dx = _made(dx, "dx", shape, _BF16, dev, stream)
     dw_mix = _made(dw_mix, "dw_mix", (mix, F), _F32, dev, stream)
     dscale = _made(dscale, "dscale", (3,), _F32, dev, stream)

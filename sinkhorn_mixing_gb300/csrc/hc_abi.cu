@@ -20,7 +20,6 @@ __device__ unsigned int g_err_word;
 
 namespace {
 std::atomic<uint64_t> g_launches{0};
-constexpr int kMaxDevices = 64;
 std::mutex g_mu;
 DeviceInfo g_info[kMaxDevices];
 bool g_have[kMaxDevices];
@@ -40,6 +39,15 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
             fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
     });
     return fn;
+}
+
+cudaError_t allow_smem(SmemState &state, const void *kernel, int bytes, const DeviceInfo &di) {
+    if (di.ctx != 0 && state.ctx[di.device].load(std::memory_order_acquire) == di.ctx)
+        return cudaSuccess;
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) state.ctx[di.device].store(di.ctx, std::memory_order_release);
+    return e;
 }
 
 bool overlap_launches() {

@@ -6,8 +6,11 @@
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
+#include <atomic>
 
 namespace hc {
+
+constexpr int kMaxDevices = 64;
 
 struct DeviceInfo {
     int device;
@@ -44,6 +47,13 @@ ForcedPath forced_path();
 // overlaps is the launch and scheduling of one kernel with the tail of the
 // other.  HCMIX_PDL=0 in the environment turns it off (read at each call).
 bool overlap_launches();
+
+// cudaFuncAttributeMaxDynamicSharedMemorySize of a kernel, set once per device
+// and context.  `state` belongs to the kernel (a static, zero at first).
+struct SmemState {
+    std::atomic<unsigned long long> ctx[kMaxDevices];
+};
+cudaError_t allow_smem(SmemState &state, const void *kernel, int bytes, const DeviceInfo &di);
 
 // The driver's cuTensorMapEncodeTiled, or nullptr when it is unavailable.
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();

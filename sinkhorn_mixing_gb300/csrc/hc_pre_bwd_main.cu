@@ -557,8 +557,9 @@ __global__ void __launch_bounds__(Cfg<HC, K8>::THREADS, 1) k_dx_dw(Args a) {
 template <int HC, bool K8>
 cudaError_t launch(const PreBackward &p, const MainArgs &m, const DeviceInfo &di, cudaStream_t s) {
     using C = Cfg<HC, K8>;
-    const cudaError_t e = cudaFuncSetAttribute(
-        k_dx_dw<HC, K8>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    static SmemState state;
+    const cudaError_t e =
+        allow_smem(state, reinterpret_cast<const void *>(k_dx_dw<HC, K8>), C::SMEM, di);
     if (e != cudaSuccess) return e;
     Args a;
     a.split = m.split;

@@ -536,8 +536,9 @@ bool stream_map(CUtensorMap *map, const void *p, bool bytes, int64_t n, int64_t 
 template <bool K8>
 cudaError_t launch(const PreBackward &p, const MainArgs &m, const DeviceInfo &di, cudaStream_t s) {
     using L = Lay<K8>;
-    const cudaError_t e = cudaFuncSetAttribute(
-        k_dx_dw_tma<K8>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM);
+    static SmemState state;
+    const cudaError_t e =
+        allow_smem(state, reinterpret_cast<const void *>(k_dx_dw_tma<K8>), L::SMEM, di);
     if (e != cudaSuccess) return e;
     CUtensorMap g, x, y, dx;
     const cuuint64_t dim[2] = {(cuuint64_t)p.d, (cuuint64_t)p.n};
@@ -564,8 +565,10 @@ cudaError_t launch(const PreBackward &p, const MainArgs &m, const DeviceInfo &di
 
 Split split_dx_dw_tma(int64_t n, int64_t d, int64_t most) { return Split::of(n, d, CH, T, most); }
 
+// Two steps of tokens at least: below, the other kernel is as fast (8 tokens of
+// 4 x 64: both are done before the host is) and needs no tensor maps.
 bool dx_dw_tma_takes(const PreBackward &p) {
-    return p.hc == 4 && p.d >= CH && p.n < (int64_t(1) << 31) && forced_path() != kPathGeneral &&
+    return p.hc == 4 && p.d >= CH && p.n >= 2 * T && p.n < (int64_t(1) << 31) && forced_path() != kPathGeneral &&
            (p.x.scales == nullptr || p.d % 16 == 0) && tensor_map_encoder() != nullptr;
 }
 

@@ -290,7 +290,8 @@ def test_mixes_pre_backward(hc, copies, n, d, k8):
 
 
 @pytest.mark.parametrize("n,d", [(2, 64), (63, 80), (64, 96), (65, 128), (700, 144), (1100, 192),
-                                 (3000, 5120)])
+                                 (3000, 5120), (128, 64), (129, 80), (190, 96), (193, 1040),
+                                 (1025, 264)])
 @pytest.mark.parametrize("k8", [True, False])
 def test_mixes_pre_backward_streamed(hc, monkeypatch, n, d, k8):
     # shapes that the TMA kernel takes, and the general path on the same inputs
