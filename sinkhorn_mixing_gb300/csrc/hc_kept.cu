@@ -60,7 +60,7 @@ cudaError_t by_pieces(int64_t rows, int64_t d, Fn f) {
 // GB): 674 us, 6.03 TB/s; with 8 channels a lane 780 us.  A row's last lane may
 // have 8.
 template <int U>
-__global__ void __launch_bounds__(256) k_checkpoint(Slots sl, int64_t nblk,
+__global__ void __launch_bounds__(256, 5) k_checkpoint(Slots sl, int64_t nblk,
                                                     const uint4 *__restrict__ x,
                                                     uint2 *__restrict__ codes,
                                                     uint8_t *__restrict__ scales) {
@@ -132,7 +132,7 @@ __global__ void __launch_bounds__(256) k_restore(Slots sl, int64_t nblk, Kept k,
 // --------------------------------------------------------- k_pre_restore
 // y = sum_j pre_j x_j of kept copies, the copies in the order of hc_pre.
 template <int HC, int U>
-__global__ void __launch_bounds__(256) k_pre_restore(Slots sl, int64_t nblk, Kept k,
+__global__ void __launch_bounds__(256, HC == 4 ? 4 : 6) k_pre_restore(Slots sl, int64_t nblk, Kept k,
                                                      const float *__restrict__ pre,
                                                      uint4 *__restrict__ y) {
     griddep_wait_then_release();
@@ -244,6 +244,10 @@ __global__ void __launch_bounds__(256, HC == 4 ? 3 : 2) k_post_checkpoint(Slots 
     }
 }
 
+// As many blocks as are resident at once (each kernel's launch bounds): they
+// share the slots evenly, where more blocks would leave a last partial wave
+// (k_checkpoint 674 -> 643 us, k_post_checkpoint of 4,096 tokens 90 -> 85 us;
+// k_restore was 2 us faster with 8 than with its 5).
 dim3 stream_grid(const Slots &sl, int u, int sms, int blocks_per_sm) {
     const int64_t per_block = 256 * u;
     const int64_t want = (sl.count + per_block - 1) / per_block;
@@ -262,7 +266,7 @@ cudaError_t launch_checkpoint(int64_t rows, int64_t d, const uint16_t *x, uint8_
     const int64_t nblk = kept_blocks(d);
     return by_pieces(rows, d, [&](int64_t r0, int64_t nr) {
         const Slots sl = make_slots(nr, d, 2);
-        return launch_overlapped(k_checkpoint<2>, stream_grid(sl, 2, di.sms, 8), dim3(256), 0, s,
+        return launch_overlapped(k_checkpoint<2>, stream_grid(sl, 2, di.sms, 5), dim3(256), 0, s,
                                  sl, nblk, reinterpret_cast<const uint4 *>(x + r0 * d),
                                  reinterpret_cast<uint2 *>(codes + r0 * d), scales + r0 * nblk);
     });
@@ -285,9 +289,9 @@ cudaError_t launch_pre_restore(int64_t n, int hc, int64_t d, const Kept &k, cons
         const Slots sl = make_slots(nt, d);
         uint4 *yv = reinterpret_cast<uint4 *>(y + t0 * d);
         const Kept kt = rows_from(k, t0 * hc, d);
-        return hc == 4 ? launch_overlapped(k_pre_restore<4, 2>, stream_grid(sl, 2, di.sms, 8),
+        return hc == 4 ? launch_overlapped(k_pre_restore<4, 2>, stream_grid(sl, 2, di.sms, 4),
                                            dim3(256), 0, s, sl, nblk, kt, pre + t0 * hc, yv)
-                       : launch_overlapped(k_pre_restore<8, 1>, stream_grid(sl, 1, di.sms, 8),
+                       : launch_overlapped(k_pre_restore<8, 1>, stream_grid(sl, 1, di.sms, 6),
                                            dim3(256), 0, s, sl, nblk, kt, pre + t0 * hc, yv);
     });
 }
@@ -299,7 +303,7 @@ cudaError_t launch_post_checkpoint(int64_t n, int hc, int64_t d, const uint16_t 
     const int64_t nblk = kept_blocks(d);
     return by_pieces(n, d, [&](int64_t t0, int64_t nt) {
         const Slots sl = make_slots(nt, d);
-        const dim3 grid = stream_grid(sl, 1, di.sms, 8);
+        const dim3 grid = stream_grid(sl, 1, di.sms, hc == 4 ? 3 : 2);
         const int64_t row = t0 * hc;
         const uint4 *ov = reinterpret_cast<const uint4 *>(out + t0 * d);
         const uint4 *rv = reinterpret_cast<const uint4 *>(res + row * d);

@@ -45,11 +45,11 @@ struct Record {
         if (tiled) {
             tile = rec + t / kTileTokens * CF::kTileBytes;
             r = (int)(t % kTileTokens);
-            coef = tile + r * CF::kPairBytes;
-            tile += kTileTokens * CF::kPairBytes + r % 8 * 16;
+            coef = tile + r * CF::kCoefBytes;
+            tile += kTileTokens * CF::kCoefBytes + r % 8 * 16;
         } else {
             coef = rec + t * CF::kBytes;
-            tile = coef + CF::kPairBytes;
+            tile = coef + CF::kCoefBytes;
             r = -1;
         }
     }
@@ -224,10 +224,10 @@ __global__ void __launch_bounds__(256 + 32 * mix_warps<HC>(), 3)
         __syncwarp();
         const bool pad = slot < tpb && !valid && grp * tpb + slot < npad;
         const Record<HC> to(rec, pad ? grp * tpb + slot : t, tiled != 0);
-        float2 *ct = reinterpret_cast<float2 *>(to.coef);
+        float *ct = reinterpret_cast<float *>(to.coef);
         if (valid) {
 #pragma unroll
-            for (int k = 0; k < HC; ++k) ct[k * HC + j] = make_float2(C[k], C[k]);
+            for (int k = 0; k < HC; ++k) ct[k * HC + j] = C[k];
         }
         // backward through the steps
         for (int i = steps - 1; i >= 0; --i) {
@@ -299,11 +299,11 @@ __global__ void __launch_bounds__(256 + 32 * mix_warps<HC>(), 3)
         const int ex = min(max((int)(__float_as_uint(top) >> 23), 14), 253);
         const float up = __uint_as_float((uint32_t)(267 - ex) << 23);
         if (valid) {
-            ct[CF::kPre + j] = make_float2(pre, pre);
+            ct[CF::kPre + j] = pre;
             if (j < 2) {
                 const float v = j == 0 ? -dot_m * r2 / features
                                        : __uint_as_float((uint32_t)(ex - 13) << 23);
-                ct[CF::kQ + j] = make_float2(v, v);
+                ct[CF::kQ + j] = v;
             }
             auto put = [&](int i, float v) {
                 to.put16(i, __half_as_ushort(__float2half_rn(v * up)));
@@ -325,7 +325,7 @@ __global__ void __launch_bounds__(256 + 32 * mix_warps<HC>(), 3)
             for (int k = 0; k < HC; ++k) db2[k] += G[k];
             ds0 = fmaf(dz0, m0, ds0), ds1 = fmaf(dz1, m1, ds1), ds2 += c2;
         } else if (pad) {
-            for (int i = j; i < CF::kPairBytes / 8; i += HC) ct[i] = make_float2(0.0f, 0.0f);
+            for (int i = j; i < CF::kCoefBytes / 4; i += HC) ct[i] = 0.0f;
             for (int i = j; i < CF::kK; i += HC) to.put16(i, 0);
             for (int i = j; i < CF::kParts; i += HC) to.put3(i, 0);
         }

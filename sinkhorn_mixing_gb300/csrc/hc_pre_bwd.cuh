@@ -28,8 +28,9 @@ __device__ __forceinline__ void arrived(float v[N]) {
 #pragma unroll
     for (int i = 0; i < N; ++i) asm volatile("" : "+f"(v[i]));
 }
-__device__ __forceinline__ void lds_pairs(uint32_t a, uint64_t &x, uint64_t &y) {
-    asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(x), "=l"(y) : "r"(a));
+// a binary32 pattern in both halves of a pair
+__device__ __forceinline__ uint64_t twice(uint32_t v) {
+    return pack2(__uint_as_float(v), __uint_as_float(v));
 }
 __device__ __forceinline__ uint32_t pack_pair(uint64_t v) {
     float lo, hi;

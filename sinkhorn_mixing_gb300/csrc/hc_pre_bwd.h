@@ -7,8 +7,8 @@
 namespace hc {
 
 // What the first kernel leaves per token for the second, one record of bytes:
-//   coefficients, each twice in a row (two-wide FMAs take a pair): comb
-//     transposed [k][j] (comb_jk of one k lie together), pre [HC], q, f
+//   coefficients, binary32: comb transposed [k][j] (comb_jk of one k lie
+//     together), pre [HC], q, f, padding to a pitch whose rows meet in no bank
 //   du16 [kK] fp16: du times a power of two 1/f of the token's own that puts
 //     its largest magnitude in [2^13, 2^14), zeros behind (2+HC) HC
 //   du3 [kParts] bf16: du = hi + mid + lo, three bf16 numbers (24 bits).
@@ -18,18 +18,19 @@ constexpr int kTileTokens = 64;
 template <int HC>
 struct Coef {
     static constexpr int kMix = (2 + HC) * HC;
-    static constexpr int kPre = HC * HC, kQ = kPre + HC, kF = kQ + 1;  // in pairs
+    static constexpr int kPre = HC * HC, kQ = kPre + HC, kF = kQ + 1;  // in floats
     static constexpr int kK = (kMix + 15) / 16 * 16;
     static constexpr int kN = 80;                        // N of one product
     static constexpr int kProducts = HC == 4 ? 1 : 3;
     static constexpr int kParts = kN * kProducts;
-    static constexpr int kPairBytes = (kF + 1) * 8, kKBytes = kK * 2, kPartBytes = kParts * 2;
-    static constexpr int kBytes = kPairBytes + kKBytes + kPartBytes;
+    static constexpr int kCoefBytes = HC == 4 ? 112 : 304, kKBytes = kK * 2, kPartBytes = kParts * 2;
+    static constexpr int kBytes = kCoefBytes + kKBytes + kPartBytes;
     // For the TMA kernel the records of kTileTokens tokens lie as its shared memory has them:
     // their coefficients, then du16 twice and du3 in blocks of 8 x 16 bytes (Tiled).
-    static constexpr int kTileBytes = kTileTokens * (kPairBytes + 2 * kKBytes + kPartBytes);
-    static_assert(kPairBytes % 16 == 0 && kKBytes % 16 == 0 && kPartBytes % 16 == 0,
+    static constexpr int kTileBytes = kTileTokens * (kCoefBytes + 2 * kKBytes + kPartBytes);
+    static_assert(kCoefBytes % 16 == 0 && kKBytes % 16 == 0 && kPartBytes % 16 == 0,
                   "16-byte pieces");
+    static_assert((kF + 1) * 4 <= kCoefBytes, "coefficients fit");
     static_assert(HC == 4 ? 3 * kMix <= kN : kMix == kN, "three parts fit");
 };
 

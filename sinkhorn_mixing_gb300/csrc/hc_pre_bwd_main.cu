@@ -58,22 +58,26 @@ struct Cfg {
     // Row pitches: a token's row is moved on by as many bytes as the lanes of one token read at
     // once, so that the lanes of neighbouring tokens meet in no bank.
     static constexpr int GP = HC * CH * 2 + 32, YP = CH * 2 + 32, XP = HC * CH + 16;
-    static constexpr int CP = CF::kPairBytes, AP = CF::kKBytes + 16;
+    static constexpr int CP = CF::kCoefBytes, AP = CF::kKBytes + 16;
     // x as the M operand: 8 channels x 8 tokens in 128 bytes (channels along 16 bytes), the
     // blocks of a channel group's tokens in a row
     static constexpr int OT = T / 8 * 128, OBYTES = FT / 8 * OT;
     static constexpr int BT = T / 8 * 128, BBYTES = CF::kParts / 8 * BT;
     // stage
     static constexpr int SG = 0, SY = SG + T * GP, SX = SY + T * YP;
-    static constexpr int SS = SX + (K8 ? T * XP : OBYTES);  // scales, each twice
+    static constexpr int SS = SX + (K8 ? T * XP : OBYTES);  // scales
     static constexpr int SCALES = T * HC * CH / 32;
-    static constexpr int SC = SS + (K8 ? SCALES * 8 : 0), SA = SC + T * CP;
+    static constexpr int SC = SS + (K8 ? SCALES * 4 : 0), SA = SC + T * CP;
     static constexpr int STAGE = (SA + T * AP + 127) / 128 * 128;
-    // the block's memory
+    // the block's memory: two stages, a longer ring for du3, which products still under way read
+    // (three stages, which would fit at HC = 8 in 8 bits, took longer: 4,096 tokens of 8 x 5120
+    // 607 us against 525)
     static constexpr int BRING = K8 ? 3 : 2;
     static constexpr int OB = 2 * STAGE, OO = OB + BRING * BBYTES;  // du3 ring; x operand (K8)
     static constexpr int OW = OO + (K8 ? OBYTES : 0), WREG = 2 * KS;
     static constexpr int WBYTES = FT / 8 * 32 * WREG * 4;
+    static constexpr int WV = MIX * FT / 4 / THREADS;               // float4 of W a thread
+    static_assert(WV * 4 * THREADS == MIX * FT, "W splits over the threads");
     static constexpr int OE = OW + WBYTES;                          // barrier, flags, maxima
     static constexpr int SMEM = OE + 256;
     static constexpr uint32_t IDESC = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 15) | (1u << 16) |
@@ -101,6 +105,17 @@ __device__ __forceinline__ uint32_t lds32(uint32_t a) {
 }
 __device__ __forceinline__ void sts64(uint32_t a, uint32_t x, uint32_t y) {
     asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(a), "r"(x), "r"(y) : "memory");
+}
+// N floats, each twice
+template <int N>
+__device__ __forceinline__ void lds_twice(uint32_t a, uint64_t (&v)[N]) {
+    if (N == 4) {
+        const uint4 u = lds128(a);
+        v[0] = twice(u.x), v[1] = twice(u.y), v[N - 2] = twice(u.z), v[N - 1] = twice(u.w);
+    } else {
+        const uint2 u = lds64(a);
+        v[0] = twice(u.x), v[1] = twice(u.y);
+    }
 }
 // c = a b (first) or c += a b
 template <bool FIRST>
@@ -163,6 +178,10 @@ __global__ void __launch_bounds__(Cfg<HC, K8>::THREADS, 1) k_dx_dw(Args a) {
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    if (CF::kK > C::MIX)  // the rows of W behind the mix numbers stay zero
+        for (int q = tid; q < C::WBYTES / 16; q += C::THREADS)
+            sts128(sb + C::OW + q * 16, make_uint4(0, 0, 0, 0));
+    __syncthreads();
 
     // lane's place: tokens mt*16 + lane/4 (+ 8), channels cl .. cl+3 of the slice, copies jq*4 ..
     const int mt = warp % C::MT, grp = warp / C::MT % C::GROUPS, jq = warp / (C::MT * C::GROUPS);
@@ -189,10 +208,17 @@ __global__ void __launch_bounds__(Cfg<HC, K8>::THREADS, 1) k_dx_dw(Args a) {
         // ---- the slice of W, in fp16 times a power of two that brings its largest magnitude
         // to [2^13, 2^14), laid out as the products' B fragments
         float top = 0.0f;
-        for (int q = tid; q < C::MIX * C::FT; q += C::THREADS) {
-            const int i = q / C::FT, m = q % C::FT, c = m % C::CH;
-            if (c < width)
-                top = fmaxf(top, fabsf(__ldg(a.w + (int64_t)i * F + m / C::CH * a.d + ch0 + c)));
+        float4 wv[C::WV];  // all of it in flight at once
+#pragma unroll
+        for (int r = 0; r < C::WV; ++r) {
+            const int q = (r * C::THREADS + tid) * 4, i = q / C::FT, f = q % C::FT;
+            wv[r] = f % C::CH < width
+                        ? __ldg(reinterpret_cast<const float4 *>(a.w + (int64_t)i * F +
+                                                                 f / C::CH * a.d + ch0 + f % C::CH))
+                        : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            top = fmaxf(fmaxf(fmaxf(fabsf(wv[r].x), fabsf(wv[r].y)),
+                              fmaxf(fabsf(wv[r].z), fabsf(wv[r].w))),
+                        top);
         }
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1)
@@ -206,18 +232,20 @@ __global__ void __launch_bounds__(Cfg<HC, K8>::THREADS, 1) k_dx_dw(Args a) {
         const int ex = min(max((int)(__float_as_uint(top) >> 23), 14), 253);
         const float wup = __uint_as_float((uint32_t)(267 - ex) << 23);
         const float wdown = __uint_as_float((uint32_t)(ex - 13) << 23);
-        const uint64_t wdown2 = pack2(wdown, wdown);
-        for (int q = tid; q < CF::kK * C::FT; q += C::THREADS) {
-            const int i = q / C::FT, m = q % C::FT, j = m / C::CH, c = m % C::CH;
-            float v = 0.0f;
-            if (i < C::MIX && c < width) v = __ldg(a.w + (int64_t)i * F + j * a.d + ch0 + c);
-            // channel 4 t + 2 p + b of its group of 16 is row n = 2 t + b of product p
-            const int g = (c >> 2 & 3) * 2 + (c & 1), p = c >> 1 & 1;
+#pragma unroll
+        for (int r = 0; r < C::WV; ++r) {
+            const int q = (r * C::THREADS + tid) * 4, i = q / C::FT, f = q % C::FT;
+            const float w4[4] = {wv[r].x, wv[r].y, wv[r].z, wv[r].w};
             const int k = i & 15, reg = (i >> 4) * 2 + (k >> 3);
-            const int nt = (j * C::GROUPS + (c >> 4)) * 2 + p, ln = g * 4 + (k & 7) / 2;
-            reinterpret_cast<__half *>(
-                smem + C::OW)[((nt * 32 + ln) * C::WREG + reg) * 2 + (k & 1)] =
-                __float2half_rn(v * wup);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                // channel 4 t + 2 p + b of its group of 16 is row n = 2 t + b of product p
+                const int c = f % C::CH + e, g = (c >> 2 & 3) * 2 + (e & 1), p = e >> 1;
+                const int nt = (f / C::CH * C::GROUPS + (c >> 4)) * 2 + p, ln = g * 4 + (k & 7) / 2;
+                reinterpret_cast<__half *>(
+                    smem + C::OW)[((nt * 32 + ln) * C::WREG + reg) * 2 + (k & 1)] =
+                    __float2half_rn(w4[e] * wup);
+            }
         }
         if (!started) {
             griddep_wait_then_release();
@@ -229,7 +257,7 @@ __global__ void __launch_bounds__(Cfg<HC, K8>::THREADS, 1) k_dx_dw(Args a) {
         // past the slice's end read 0 bytes at column 0.
         constexpr int GT = C::THREADS / (C::FT / 8), YT = C::THREADS / (C::CH / 8);
         constexpr int XV = C::FT / 16, XT = C::THREADS / XV;
-        constexpr int RV = CF::kBytes / 16, R1 = CF::kPairBytes / 16, R2 = R1 + CF::kKBytes / 16;
+        constexpr int RV = CF::kBytes / 16, R1 = CF::kCoefBytes / 16, R2 = R1 + CF::kKBytes / 16;
         constexpr int RN = (C::T * RV + C::THREADS - 1) / C::THREADS;
         const int gt = tid / (C::FT / 8), gv = tid % (C::FT / 8);
         const int gk = gv / (C::CH / 8), gc = gv % (C::CH / 8) * 8;
@@ -258,7 +286,7 @@ __global__ void __launch_bounds__(Cfg<HC, K8>::THREADS, 1) k_dx_dw(Args a) {
         // `whole`: all C::T tokens exist, else the first `left`
         auto load_rows = [&](int64_t s, int64_t rel, auto whole, int left) {
             constexpr bool W = decltype(whole)::value;
-            const uint32_t st = sb + (uint32_t)(s & 1) * C::STAGE;
+            const uint32_t st = sb + (uint32_t)(rel & 1) * C::STAGE;
             const uint32_t bt =
                 sb + C::OB + (uint32_t)(rel % C::BRING) * C::BBYTES - C::STAGE;
             if (a.g != nullptr) {
@@ -321,15 +349,15 @@ __global__ void __launch_bounds__(Cfg<HC, K8>::THREADS, 1) k_dx_dw(Args a) {
             sp += C::T * HC * a.nblk;
             return v;
         };
-        auto keep_scale = [&](int64_t s, uint32_t v) {
-            const uint32_t f = __float_as_uint(kept_scale(v));
+        auto keep_scale = [&](int64_t rel, uint32_t v) {
             if (K8 && tid < C::SCALES)
-                sts64(sb + (uint32_t)(s & 1) * C::STAGE + C::SS + tid * 8, f, f);
+                reinterpret_cast<float *>(smem + (rel & 1) * C::STAGE + C::SS)[tid] =
+                    kept_scale(v);
         };
         // dW += du^T x of the step `rel` of this run: one thread issues
-        auto issue = [&](int64_t s, int64_t rel) {
+        auto issue = [&](int64_t rel) {
             const uint32_t xo =
-                K8 ? sb + C::OO : sb + (uint32_t)(s & 1) * C::STAGE + C::SX;
+                K8 ? sb + C::OO : sb + (uint32_t)(rel & 1) * C::STAGE + C::SX;
             const uint32_t bo = sb + C::OB + (uint32_t)(rel % C::BRING) * C::BBYTES;
 #pragma unroll
             for (int ks = 0; ks < C::T / 16; ++ks)
@@ -398,7 +426,7 @@ __global__ void __launch_bounds__(Cfg<HC, K8>::THREADS, 1) k_dx_dw(Args a) {
         uint8_t *dxp =
             a.dx + ((s0 * C::T + mt * 16 + tg) * F + jq * C::NJ * a.d + ch0 + (cl < width ? cl : 0)) * 2;
         load(s0, 0);
-        keep_scale(s0, load_scale(s0));
+        keep_scale(0, load_scale(s0));
         for (int64_t s = s0; s < s1; ++s) {
             const int64_t rel = s - s0;
             const bool full = rel > 0 && rel % kDrain == 0;
@@ -417,17 +445,17 @@ __global__ void __launch_bounds__(Cfg<HC, K8>::THREADS, 1) k_dx_dw(Args a) {
             }
             if (tid == 0 && (!K8 || rel > 0)) {
                 tc_fence_after();
-                issue(K8 ? s - 1 : s, K8 ? rel - 1 : rel);
+                issue(K8 ? rel - 1 : rel);
             }
             if (!K8 || rel > 0) ++commits;
             uint32_t next_scale = 0;
-            if (s + 1 < s1) {
+            if (s + 1 < s1) {  // into the stage that step s - 1 has left
                 load(s + 1, rel + 1);
                 next_scale = load_scale(s + 1);
             }
 
             // ---- du W
-            const uint32_t st = sb + (uint32_t)(s & 1) * C::STAGE;
+            const uint32_t st = sb + (uint32_t)(rel & 1) * C::STAGE;
             float acc[C::NJ][2][4];
             uint32_t af[C::KS][4];
 #pragma unroll
@@ -465,10 +493,13 @@ __global__ void __launch_bounds__(Cfg<HC, K8>::THREADS, 1) k_dx_dw(Args a) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int t = mt * 16 + h * 8 + tg;
-                const uint32_t cfa = st + C::SC + t * C::CP + jq * C::NJ * 8;
+                const uint32_t cfa = st + C::SC + t * C::CP + jq * C::NJ * 4;
                 uint64_t v[C::NJ][2], qq, ff;
-                lds_pairs(st + C::SC + t * C::CP + CF::kQ * 8, qq, ff);
-                ff = fmul2(ff, wdown2);
+                {
+                    const uint2 u = lds64(st + C::SC + t * C::CP + CF::kQ * 4);
+                    const float q = __uint_as_float(u.x), f = __uint_as_float(u.y) * wdown;
+                    qq = pack2(q, q), ff = pack2(f, f);
+                }
 #pragma unroll
                 for (int j = 0; j < C::NJ; ++j)
 #pragma unroll
@@ -476,8 +507,7 @@ __global__ void __launch_bounds__(Cfg<HC, K8>::THREADS, 1) k_dx_dw(Args a) {
                         v[j][p] = fmul2(pack2(acc[j][p][2 * h], acc[j][p][2 * h + 1]), ff);
                 auto add = [&](uint32_t coef, const uint2 &u) {  // v_j += coef_j u
                     uint64_t c[C::NJ];
-#pragma unroll
-                    for (int j = 0; j < C::NJ; j += 2) lds_pairs(coef + j * 8, c[j], c[j + 1]);
+                    lds_twice(coef, c);
                     const uint64_t lo = bf16x2_to_f32x2(u.x), hi = bf16x2_to_f32x2(u.y);
 #pragma unroll
                     for (int j = 0; j < C::NJ; ++j) {
@@ -488,19 +518,16 @@ __global__ void __launch_bounds__(Cfg<HC, K8>::THREADS, 1) k_dx_dw(Args a) {
                 if (a.g != nullptr) {
 #pragma unroll
                     for (int k = 0; k < HC; ++k)
-                        add(cfa + k * HC * 8, lds64(st + C::SG + t * C::GP + (k * C::CH + cl) * 2));
+                        add(cfa + k * HC * 4, lds64(st + C::SG + t * C::GP + (k * C::CH + cl) * 2));
                 }
-                add(cfa + CF::kPre * 8, lds64(st + C::SY + t * C::YP + cl * 2));
+                add(cfa + CF::kPre * 4, lds64(st + C::SY + t * C::YP + cl * 2));
                 // x, last: its operand is free once the products of step s - 1 are done
                 if (K8 && h == 0) products_done();
                 const uint32_t in = cl < width && (s * C::T + t < a.n);
                 uint8_t *p = dxp + h * 16 * F;
                 uint64_t sc[C::NJ];
                 if (K8) {
-                    const uint32_t sa =
-                        st + C::SS + ((t * (C::CH / 32) + cl / 32) * HC + jq * C::NJ) * 8;
-#pragma unroll
-                    for (int j = 0; j < C::NJ; j += 2) lds_pairs(sa + j * 8, sc[j], sc[j + 1]);
+                    lds_twice(st + C::SS + ((t * (C::CH / 32) + cl / 32) * HC + jq * C::NJ) * 4, sc);
                 }
 #pragma unroll
                 for (int j = 0; j < C::NJ; ++j, p += a.d * 2) {
@@ -524,7 +551,7 @@ __global__ void __launch_bounds__(Cfg<HC, K8>::THREADS, 1) k_dx_dw(Args a) {
                 }
             }
             dxp += C::T * F * 2;
-            if (s + 1 < s1) keep_scale(s + 1, next_scale);
+            if (s + 1 < s1) keep_scale(rel + 1, next_scale);
             if (K8 && full) {  // the products up to step s - 1 are done
                 tc_fence_after();
                 drain(rel == kDrain, false);
@@ -536,7 +563,7 @@ __global__ void __launch_bounds__(Cfg<HC, K8>::THREADS, 1) k_dx_dw(Args a) {
             __syncthreads();
             if (tid == 0) {
                 tc_fence_after();
-                issue(s1 - 1, s1 - 1 - s0);
+                issue(s1 - 1 - s0);
             }
             ++commits;
         }

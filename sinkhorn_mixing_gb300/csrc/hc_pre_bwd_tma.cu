@@ -179,6 +179,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    for (int q = tid; q < FT * 64 / 16; q += kThreads)  // W's rows behind the mix numbers: zeros
+        sts128(sb + L::OW + q * 16, make_uint4(0, 0, 0, 0));
+    __syncthreads();
     // wait_bar reads the timer, which takes long, so the waits of a healthy run end before it
     auto wait = [&](uint32_t bar, uint32_t parity) {
 #pragma unroll 1
@@ -233,7 +236,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         test(kFull + (uint32_t)(next & 1) * 8, (uint32_t)(next >> 1)) &&
                         (next == 0 || test(kD1Free, (uint32_t)(next - 1)))) {
                         tc_fence_after();
-                        const uint32_t ao = stage(next) + L::OR + T * CF::kPairBytes;
+                        const uint32_t ao = stage(next) + L::OR + T * CF::kCoefBytes;
 #pragma unroll
                         for (int ks = 0; ks < CF::kK / 16; ++ks)
                             mma_bf16(tmem, rows16(ao + ks * 256, 128, 512),
@@ -246,7 +249,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tc_fence_after();
                         const uint32_t xo = stage(it) + (K8 ? 0 : L::OX);
                         const uint32_t bo =
-                            stage(it) + L::OR + T * CF::kPairBytes + 2 * T * CF::kKBytes;
+                            stage(it) + L::OR + T * CF::kCoefBytes + 2 * T * CF::kKBytes;
 #pragma unroll
                         for (int ks = 0; ks < T / 16; ++ks)
 #pragma unroll
@@ -318,11 +321,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int width = (int)min((int64_t)CH, a.d - ch0);
             // ---- the slice of W in fp16, its largest magnitude brought to [2^13, 2^14): 8 x 8
             // blocks [feature group][mix group][feature][mix]
+            constexpr int kW = MIX * FT / 4 / (32 * kComputeWarps);
             float top = 0.0f;
-            for (int q = tid; q < MIX * FT; q += 32 * kComputeWarps) {
-                const int i = q / FT, m = q % FT, c = m % CH;
-                if (c < width)
-                    top = fmaxf(top, fabsf(__ldg(a.w + (int64_t)i * F + m / CH * a.d + ch0 + c)));
+            float4 wv[kW];  // all of it in flight at once
+#pragma unroll
+            for (int r = 0; r < kW; ++r) {
+                const int q = (r * 32 * kComputeWarps + tid) * 4, i = q / FT, f = q % FT;
+                wv[r] = f % CH < width
+                            ? __ldg(reinterpret_cast<const float4 *>(
+                                  a.w + (int64_t)i * F + f / CH * a.d + ch0 + f % CH))
+                            : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                top = fmaxf(fmaxf(fmaxf(fabsf(wv[r].x), fabsf(wv[r].y)),
+                                  fmaxf(fabsf(wv[r].z), fabsf(wv[r].w))),
+                            top);
             }
 #pragma unroll
             for (int off = 16; off > 0; off >>= 1)
@@ -336,13 +347,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int ex = min(max((int)(__float_as_uint(top) >> 23), 14), 253);
             const float wup = __uint_as_float((uint32_t)(267 - ex) << 23);
             const float wdown = __uint_as_float((uint32_t)(ex - 13) << 23);
-            const uint64_t wdown2 = pack2(wdown, wdown);
-            for (int q = tid; q < CF::kK * FT; q += 32 * kComputeWarps) {
-                const int i = q / FT, m = q % FT, c = m % CH;
-                float v = 0.0f;
-                if (i < MIX && c < width) v = __ldg(a.w + (int64_t)i * F + m / CH * a.d + ch0 + c);
-                *reinterpret_cast<__half *>(smem + L::OW + m / 8 * 512 + i / 8 * 128 + m % 8 * 16 +
-                                            i % 8 * 2) = __float2half_rn(v * wup);
+#pragma unroll
+            for (int r = 0; r < kW; ++r) {
+                const int q = (r * 32 * kComputeWarps + tid) * 4, i = q / FT, f = q % FT;
+                const float w4[4] = {wv[r].x, wv[r].y, wv[r].z, wv[r].w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    *reinterpret_cast<__half *>(smem + L::OW + (f + e) / 8 * 512 + i / 8 * 128 +
+                                                (f + e) % 8 * 16 + i % 8 * 2) =
+                        __float2half_rn(w4[e] * wup);
             }
             if (!started) {
                 griddep_wait_then_release();
@@ -421,13 +434,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 // ---- du W of this token
                 uint64_t v[4][4], qq, ff;
-                const uint32_t cfa = st + L::OR + tl * CF::kPairBytes;
+                const uint32_t cfa = st + L::OR + tl * CF::kCoefBytes;
                 {
                     float acc[4][8];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) tmem_ld8(lanes + j * CH + cg * 8, acc[j]);
-                    lds_pairs(cfa + CF::kQ * 8, qq, ff);
-                    ff = fmul2(ff, wdown2);
+                    const uint2 u = lds64(cfa + CF::kQ * 4);
+                    const float q = __uint_as_float(u.x), f = __uint_as_float(u.y) * wdown;
+                    qq = pack2(q, q), ff = pack2(f, f);
                     tmem_ld_wait();
 #pragma unroll
                     for (int j = 0; j < 4; ++j) arrived<8>(acc[j]);
@@ -450,9 +464,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!K8) arrive(kGate);  // x is its own operand
                 // ---- the stream's gradient through comb, and y's through pre
                 auto add = [&](uint32_t coef, const uint4 &u) {
-                    uint64_t c[4];
-                    lds_pairs(coef, c[0], c[1]);
-                    lds_pairs(coef + 16, c[2], c[3]);
+                    const uint4 w = lds128(coef);
+                    const uint64_t c[4] = {twice(w.x), twice(w.y), twice(w.z), twice(w.w)};
                     const uint64_t b[4] = {bf16x2_to_f32x2(u.x), bf16x2_to_f32x2(u.y),
                                            bf16x2_to_f32x2(u.z), bf16x2_to_f32x2(u.w)};
 #pragma unroll
@@ -462,9 +475,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 };
                 if (a.has_g) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) add(cfa + k * 32, lds128(st + k * T * 128 + row));
+                    for (int k = 0; k < 4; ++k) add(cfa + k * 16, lds128(st + k * T * 128 + row));
                 }
-                add(cfa + CF::kPre * 8, lds128(st + L::OY + row));
+                add(cfa + CF::kPre * 4, lds128(st + L::OY + row));
                 // ---- x; widened codes go over the gradient's tile, which this lane has read
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
