@@ -45,8 +45,8 @@ struct Record {
         if (tiled) {
             tile = rec + t / kTileTokens * CF::kTileBytes;
             r = (int)(t % kTileTokens);
-            coef = tile + r * CF::kCoefBytes;
-            tile += kTileTokens * CF::kCoefBytes + r % 8 * 16;
+            coef = tile + r * CF::kTileCoefBytes;
+            tile += kTileTokens * CF::kTileCoefBytes + r % 8 * 16;
         } else {
             coef = rec + t * CF::kBytes;
             tile = coef + CF::kCoefBytes;
@@ -59,15 +59,16 @@ struct Record {
             return;
         }
         uint8_t *p = tile + (r / 8 * (CF::kK / 8) + i / 8) * 128 + i % 8 * 2;
-        *reinterpret_cast<uint16_t *>(p) = v;
-        *reinterpret_cast<uint16_t *>(p + kTileTokens * CF::kKBytes) = v;
+#pragma unroll
+        for (int i = 0; i < CF::kTileRepeats; ++i)
+            *reinterpret_cast<uint16_t *>(p + i * kTileTokens * CF::kKBytes) = v;
     }
     __device__ __forceinline__ void put3(int i, uint16_t v) const {
         if (r < 0) {
             reinterpret_cast<uint16_t *>(tile + CF::kKBytes)[i] = v;
             return;
         }
-        *reinterpret_cast<uint16_t *>(tile + 2 * kTileTokens * CF::kKBytes +
+        *reinterpret_cast<uint16_t *>(tile + CF::kTileRepeats * kTileTokens * CF::kKBytes +
                                       (i / 8 * (kTileTokens / 8) + r / 8) * 128 + i % 8 * 2) = v;
     }
 };
@@ -325,7 +326,7 @@ __global__ void __launch_bounds__(256 + 32 * mix_warps<HC>(), 3)
             for (int k = 0; k < HC; ++k) db2[k] += G[k];
             ds0 = fmaf(dz0, m0, ds0), ds1 = fmaf(dz1, m1, ds1), ds2 += c2;
         } else if (pad) {
-            for (int i = j; i < CF::kCoefBytes / 4; i += HC) ct[i] = 0.0f;
+            for (int i = j; i <= CF::kF; i += HC) ct[i] = 0.0f;
             for (int i = j; i < CF::kK; i += HC) to.put16(i, 0);
             for (int i = j; i < CF::kParts; i += HC) to.put3(i, 0);
         }

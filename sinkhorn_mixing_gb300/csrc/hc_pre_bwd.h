@@ -13,7 +13,7 @@ namespace hc {
 //     its largest magnitude in [2^13, 2^14), zeros behind (2+HC) HC
 //   du3 [kParts] bf16: du = hi + mid + lo, three bf16 numbers (24 bits).
 //     HC = 4: [hi | mid | lo | zeros] of 24 each, in 80; HC = 8: 3 x 80.
-constexpr int kTileTokens = 64;
+constexpr int kTileTokens = 32;
 
 template <int HC>
 struct Coef {
@@ -26,8 +26,10 @@ struct Coef {
     static constexpr int kCoefBytes = HC == 4 ? 112 : 304, kKBytes = kK * 2, kPartBytes = kParts * 2;
     static constexpr int kBytes = kCoefBytes + kKBytes + kPartBytes;
     // For the TMA kernel the records of kTileTokens tokens lie as its shared memory has them:
-    // their coefficients, then du16 twice and du3 in blocks of 8 x 16 bytes (Tiled).
-    static constexpr int kTileBytes = kTileTokens * (kCoefBytes + 2 * kKBytes + kPartBytes);
+    // their coefficients, then du16, over and over to 128 rows, and du3 in blocks of 8 x 16 bytes.
+    static constexpr int kTileCoefBytes = 96, kTileRepeats = 128 / kTileTokens;
+    static constexpr int kTileBytes =
+        kTileTokens * (kTileCoefBytes + kTileRepeats * kKBytes + kPartBytes);
     static_assert(kCoefBytes % 16 == 0 && kKBytes % 16 == 0 && kPartBytes % 16 == 0,
                   "16-byte pieces");
     static_assert((kF + 1) * 4 <= kCoefBytes, "coefficients fit");

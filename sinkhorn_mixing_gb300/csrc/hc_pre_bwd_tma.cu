@@ -3,11 +3,11 @@
 // shapes).
 //
 // A block owns 64 channels of all four copies (256 features) and walks over
-// tokens in steps of 64 (Split).  Both products run on tcgen05:
-//   du W    [64 tokens, 256 features], K = 24: one product a step into TMEM,
-//     fp16 operands times powers of two (as in hc_pre_bwd_main.cu).  The 64
-//     tokens stand in the 128 rows twice, so that all four warps of a quadrant
-//     group find them in the lanes they can read.
+// tokens in steps of 32 (Split).  Both products run on tcgen05:
+//   du W    [32 tokens, 256 features], K = 24: one product a step into TMEM,
+//     fp16 operands times powers of two (as in hc_pre_bwd_main.cu).  The 32
+//     tokens stand in the 128 rows four times, so that every warp finds them in
+//     the lanes it can read.
 //   du^T x  [256 features, 24], K = tokens: sums over the steps in TMEM, x as
 //     kept in bf16 (codes are widened into an operand tile on the way), du in
 //     three bf16 parts.
@@ -15,9 +15,13 @@
 // serve 8 channels of 4 copies.  dx leaves by a TMA store, from the stage's
 // gradient tile; of codes, that tile takes the widened x instead and dx has a
 // tile of its own, so that the stage is free once the products are done.
-// Roles: warps 0-15 compute, warp 16 loads (one thread), warp 17 issues the
-// products, warp 18 stores.  Two stages; every wait has a limit, and after one
-// ran out all roles run through without acting, so that all barriers are met.
+// Roles: warps 0-7 compute the even steps and warps 8-15 the odd ones, so that
+// one group's arithmetic runs under the other's waits; warp 16 loads (one
+// thread), warp 17 issues the products, warp 18 stores.  Four stages; every wait
+// has a limit, and after one ran out all roles run through without acting, so
+// that all barriers are met.
+// (With steps of 64 tokens, two stages and all 16 warps on each step 65,536 tokens
+// of 4 x 5120 in 8 bits took 1,994 us in all, this way 1,828.)
 #include <cuda_fp16.h>
 
 #include "hc_pre_bwd.cuh"
@@ -30,25 +34,32 @@ using namespace ptx;
 using CF = Coef<4>;
 
 constexpr int T = kTileTokens, CH = 64, FT = 4 * CH, MIX = 24;
-constexpr int kComputeWarps = 16, kThreads = 32 * (kComputeWarps + 3);
-constexpr int kDrain = 8;  // steps between moves of dW's running sums (32 products each)
+constexpr int kGroupWarps = 8, kComputeWarps = 2 * kGroupWarps;
+constexpr int kThreads = 32 * (kComputeWarps + 3);
+constexpr int kStages = 4;
+// Steps between moves of dW's running sums (32 products each).  Even: the moves of a run are
+// all one group's.
+constexpr int kDrain = 16;
 
 template <bool K8>
 struct Lay {
     static constexpr int X = T * FT * (K8 ? 1 : 2), OX = T * FT * 2, OY = OX + X;
-    static constexpr int OR = OY + T * CH * 2, STAGE = OR + CF::kTileBytes;
-    static constexpr int OO = 2 * STAGE;                       // dx on its way out (K8)
+    static constexpr int OR = OY + T * CH * 2;
+    static constexpr int STAGE = OR + CF::kTileBytes;
+    static constexpr int OO = kStages * STAGE;                 // dx on its way out (K8)
     static constexpr int OW = OO + (K8 ? T * FT * 2 : 0);      // W, 32 halves a feature
-    static constexpr int OS = OW + FT * 64;                    // scales [2][2 blocks][T][4]
-    static constexpr int OE = OS + (K8 ? 2 * 2 * T * 16 : 0);  // barriers, flags, maxima
-    static constexpr int SMEM = OE + 256;
+    static constexpr int OS = OW + FT * 64;                    // scales [group][2][2 blocks][T][4]
+    static constexpr int OE = OS + (K8 ? 2 * 2 * 2 * T * 16 : 0);  // barriers, flags, maxima
+    static constexpr int SMEM = OE + 512;
     static_assert(STAGE % 1024 == 0 && OW % 1024 == 0, "swizzled tiles");
     static_assert(SMEM <= 232448, "shared memory");
 };
 
-enum Bar { kFull = 0, kEmpty = 16, kD1Full = 32, kD1Free = 40, kGate = 48, kD2Done = 56, kOut = 64 };
-constexpr int kOutFree = 168;
-constexpr int kAbort = 80, kTmem = 84, kCalm = 88, kMaxima = 96;
+// Barriers: one a stage, and below those one for even and one for odd steps, as a wait
+// names a phase by its parity and each group sees every second step.
+enum Bar { kFull = 0, kEmpty = 32, kOut = 64, kD1Full = 96, kD1Free = 112, kGate = 128,
+           kD2Done = 144, kOutFree = 160 };
+constexpr int kAbort = 176, kTmem = 180, kCalm = 184, kMaxima = 192;
 constexpr int kD2 = 256, kSums = kD2 + 2 * CF::kN;  // TMEM columns; du W has 0..255
 static_assert(kSums + 2 * MIX <= 512, "TMEM");
 
@@ -150,16 +161,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     float *maxima = reinterpret_cast<float *>(smem + L::OE + kMaxima);  // per warp
 
     if (tid == 0) {
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < kStages; ++i) {
             mbar_init(eb + kFull + 8 * i, 1);
             mbar_init(eb + kEmpty + 8 * i, K8 ? 1 : 2);  // products; and the store
-            mbar_init(eb + kOut + 8 * i, kComputeWarps);
+            mbar_init(eb + kOut + 8 * i, kGroupWarps);
         }
-        mbar_init(eb + kD1Full, 1);
-        mbar_init(eb + kD1Free, kComputeWarps);
-        mbar_init(eb + kGate, kComputeWarps);
-        mbar_init(eb + kD2Done, 1);
-        mbar_init(eb + kOutFree, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(eb + kD1Full + 8 * i, 1);
+            mbar_init(eb + kD1Free + 8 * i, kGroupWarps);
+            mbar_init(eb + kGate + 8 * i, kGroupWarps);
+            mbar_init(eb + kD2Done + 8 * i, 1);
+            mbar_init(eb + kOutFree + 8 * i, 1);
+        }
         *abort = 0;
         *calm = 0;
         if ((sb & 1023u) != 0) {  // swizzled tiles need it
@@ -189,9 +202,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (mbar_try(eb + bar, parity & 1)) return true;
         return wait_bar<false>(eb + bar, parity & 1, abort, a.err);
     };
-    auto test = [&](uint32_t bar, uint32_t parity) { return mbar_test(eb + bar, parity & 1); };
-    auto stage = [&](int64_t it) { return sb + (uint32_t)(it & 1) * L::STAGE; };
-    int64_t it = 0;  // steps of this block so far: stage it & 1, its use it >> 1
+    // step i's barrier of a stage (its use i / kStages), and of its parity (i / 2)
+    auto at_stage = [](Bar b, int64_t i) { return (uint32_t)b + (uint32_t)(i % kStages) * 8; };
+    auto at_parity = [](Bar b, int64_t i) { return (uint32_t)b + (uint32_t)(i & 1) * 8; };
+    auto wait_stage = [&](Bar b, int64_t i) {
+        return wait(at_stage(b, i), (uint32_t)(i / kStages));
+    };
+    auto wait_parity = [&](Bar b, int64_t i) { return wait(at_parity(b, i), (uint32_t)(i >> 1)); };
+    auto stage = [&](int64_t i) { return sb + (uint32_t)(i % kStages) * L::STAGE; };
+    int64_t it = 0;  // steps of this block so far
 
     if (warp == kComputeWarps) {
         // ------------------------------------------------------- loads
@@ -200,10 +219,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             asm volatile("fence.proxy.async;" ::: "memory");  // records were plain stores
             over_runs(a.split, [&](int64_t slice, int64_t, int64_t s0, int64_t s1) {
                 for (int64_t s = s0; s < s1; ++s, ++it) {
-                    const uint32_t slot = (uint32_t)(it & 1) * 8;
-                    if (it >= 2 && !wait(kEmpty + slot, (uint32_t)(it >> 1) - 1)) continue;
+                    if (it >= kStages && !wait_stage(kEmpty, it - kStages)) continue;
                     if (*abort) continue;
-                    const uint32_t st = stage(it), bar = eb + kFull + slot;
+                    const uint32_t st = stage(it), bar = eb + at_stage(kFull, it);
                     mbar_expect_tx(bar, L::X + T * CH * 2 + CF::kTileBytes +
                                             (a.has_g ? T * FT * 2 : 0));
                     const int c = (int)slice * CH, t = (int)(s * T);
@@ -214,8 +232,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             });
             if (*abort)  // what was loaded has to land before this block ends
-                for (int64_t i = it > 2 ? it - 2 : 0; i < it; ++i)
-                    wait_bar<false>(eb + kFull + (uint32_t)(i & 1) * 8, (uint32_t)(i >> 1) & 1, calm,
+                for (int64_t i = it > kStages ? it - kStages : 0; i < it; ++i)
+                    wait_bar<false>(eb + at_stage(kFull, i), (uint32_t)(i / kStages) & 1, calm,
                                     a.err, 1000000);
         }
     } else if (warp == kComputeWarps + 1) {
@@ -232,24 +250,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint32_t rounds = 0;
                 while (it < end) {
                     bool idle = true;
-                    if (next < end && next <= it + 1 &&
-                        test(kFull + (uint32_t)(next & 1) * 8, (uint32_t)(next >> 1)) &&
-                        (next == 0 || test(kD1Free, (uint32_t)(next - 1)))) {
+                    if (next < end &&
+                        mbar_test(eb + at_stage(kFull, next), (uint32_t)(next / kStages) & 1) &&
+                        (next == 0 || mbar_test(eb + at_parity(kD1Free, next - 1),
+                                                (uint32_t)((next - 1) >> 1) & 1))) {
                         tc_fence_after();
-                        const uint32_t ao = stage(next) + L::OR + T * CF::kCoefBytes;
+                        const uint32_t ao = stage(next) + L::OR + T * CF::kTileCoefBytes;
 #pragma unroll
                         for (int ks = 0; ks < CF::kK / 16; ++ks)
                             mma_bf16(tmem, rows16(ao + ks * 256, 128, 512),
                                      rows16(sb + L::OW + ks * 256, 128, 512), kIdescW, ks > 0);
-                        mma_commit(eb + kD1Full);
+                        mma_commit(eb + at_parity(kD1Full, next));
                         ++next;
                         idle = false;
                     }
-                    if (it < next && test(kGate, (uint32_t)it)) {
+                    if (it < next &&
+                        mbar_test(eb + at_parity(kGate, it), (uint32_t)(it >> 1) & 1)) {
                         tc_fence_after();
                         const uint32_t xo = stage(it) + (K8 ? 0 : L::OX);
                         const uint32_t bo =
-                            stage(it) + L::OR + T * CF::kCoefBytes + 2 * T * CF::kKBytes;
+                            stage(it) + L::OR + T * CF::kTileCoefBytes + 128 * CF::kKBytes;
 #pragma unroll
                         for (int ks = 0; ks < T / 16; ++ks)
 #pragma unroll
@@ -258,8 +278,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                                          tiles128(xo + m * 2 * T * 128 + ks * 2048),
                                          rows16(bo + ks * 256, 128, T / 8 * 128), kIdescX,
                                          (it - i0) % kDrain != 0 || ks > 0);
-                        mma_commit(eb + kD2Done);
-                        mma_commit(eb + kEmpty + (uint32_t)(it & 1) * 8);
+                        mma_commit(eb + at_parity(kD2Done, it));
+                        mma_commit(eb + at_stage(kEmpty, it));
                         ++it;
                         idle = false;
                     }
@@ -278,9 +298,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             __syncwarp();
         });
-        if (lane == 0 && *abort) {  // products in flight read shared memory
-            mma_commit(eb + kD1Full);
-            mma_commit(eb + kD2Done);
+        if (lane == 0 && *abort) {  // products in flight read shared memory: let them end
             const uint64_t t0 = gtimer();
             while (gtimer() - t0 < 1000000) {
             }
@@ -290,22 +308,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) {
             over_runs(a.split, [&](int64_t slice, int64_t, int64_t s0, int64_t s1) {
                 for (int64_t s = s0; s < s1; ++s, ++it) {
-                    const uint32_t slot = (uint32_t)(it & 1) * 8;
-                    if (!wait(kOut + slot, (uint32_t)(it >> 1))) continue;
+                    if (!wait_stage(kOut, it)) continue;
                     if (slice * CH < a.d)  // else behind the last channel (Split)
                         tma_store_3d(&map_dx, (int)slice * CH, (int)(s * T), 0,
                                      K8 ? sb + L::OO : stage(it));
                     asm volatile("cp.async.bulk.commit_group;" ::: "memory");
                     asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-                    mbar_arrive(eb + (K8 ? kOutFree : kEmpty + slot));
+                    mbar_arrive(eb + (K8 ? at_parity(kOutFree, it) : at_stage(kEmpty, it)));
                 }
             });
             asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
         }
     } else {
         // ----------------------------------------------------- compute
-        // lane's token of the step, and the warp's 8 channels
-        const int tl = (warp & 1) * 32 + lane, cg = (warp >> 2) * 2 + (warp >> 1 & 1);
+        // lane's token of the step is `lane`; the warp's group and 8 channels
+        const int group = warp / kGroupWarps, tl = lane, cg = (warp >> 2 & 1) * 4 + (warp & 3);
+        const int gt = tid % (32 * kGroupWarps);
         const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);
         const uint32_t row = (uint32_t)tl * 128 + (uint32_t)((cg ^ (tl & 7)) << 4);
         const uint32_t row8 =
@@ -362,31 +380,36 @@ __global__ void __launch_bounds__(kThreads, 1)
                 started = true;
             }
 
-            // ---- scales: one a thread, loaded two steps ahead and passed on one step ahead
+            // ---- this group's steps of the run
+            const int64_t run = it, end = it + (s1 - s0);
+            const int64_t own = run + ((run ^ group) & 1);
+            // Scales: one a thread, loaded two of the group's steps ahead and passed on one ahead
             // through [block][token][copy].  Every warp reads a step's scales before it arrives
             // at that step's kD1Free and writes the next one's behind its own read, so a phase
             // of that barrier says both that they are there and that the other half is free.
-            const int sct = tid >> 3, scj = tid >> 1 & 3, scb = tid & 1;
+            const int sct = gt >> 3, scj = gt >> 1 & 3, scb = gt & 1;
             const int64_t slices = (a.d + CH - 1) / CH;
-            const uint8_t *sp = a.xs + (s0 * slices + slice) * (T * 8) + tid;
-            auto load_scale = [&](int64_t s) -> uint32_t {
+            const uint8_t *sp = a.xs + ((s0 + (own - run)) * slices + slice) * (T * 8) + gt;
+            auto load_scale = [&](int64_t i) -> uint32_t {
                 uint32_t v = 0;
-                if (K8 && slice < slices && s * T + sct < a.n) v = __ldg(sp);
-                sp += slices * (T * 8);
+                if (K8 && i < end && slice < slices && (s0 + (i - run)) * T + sct < a.n)
+                    v = __ldg(sp);
+                sp += 2 * slices * (T * 8);
                 return v;
             };
+            const uint32_t sbuf = L::OS + group * (2 * 2 * T * 16);
             auto keep_scale = [&](int64_t i, uint32_t v) {
                 if (K8)
-                    *reinterpret_cast<float *>(smem + L::OS + (i & 1) * (2 * T * 16) +
+                    *reinterpret_cast<float *>(smem + sbuf + (i >> 1 & 1) * (2 * T * 16) +
                                                (scb * T + sct) * 16 + scj * 4) = kept_scale(v);
             };
             // dW's sums so far move on (see hc_pre_bwd_main.cu); `out`: the run's result.  A
-            // warp reads 32 lanes of one tile, 16 or 8 of the 24 mix numbers.
+            // group's warps read 32 lanes of one of the two tiles each.
             auto drain = [&](bool first, float *out) {
-                const int m = warp >> 2 & 1, c0 = warp >> 3 ? 16 : 0, c1 = warp >> 3 ? 24 : 16;
+                const int m = warp >> 2 & 1;
                 const uint32_t ta = lanes + kD2 + m * CF::kN, ts = lanes + kSums + m * MIX;
 #pragma unroll 1
-                for (int c = c0; c < c1; c += 8) {
+                for (int c = 0; c < MIX; c += 8) {
                     float v[8], u[8], w[8], sum[8];
                     tmem_ld8(ta + c, v);
                     tmem_ld8(ta + MIX + c, u);
@@ -414,27 +437,27 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
 
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            keep_scale(it, load_scale(s0));
-            uint32_t next_scale = s0 + 1 < s1 ? load_scale(s0 + 1) : 0;
+            keep_scale(own, load_scale(own));
+            uint32_t next_scale = load_scale(own + 2);
             meet<2, 32 * (kComputeWarps + 1)>();
-            for (int64_t s = s0; s < s1; ++s, ++it) {
-                const uint32_t st = stage(it), slot = (uint32_t)(it & 1) * 8;
-                wait(kFull + slot, (uint32_t)(it >> 1));
-                wait(kD1Full, (uint32_t)it);
+            for (int64_t i = own; i < end; i += 2) {
+                const uint32_t st = stage(i);
+                wait_stage(kFull, i);
+                wait_parity(kD1Full, i);
                 tc_fence_after();
                 float4 sc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                 if (K8) {
-                    if (it > 0) wait(kD1Free, (uint32_t)it - 1);
-                    const uint4 u = lds128(sb + L::OS + (uint32_t)(it & 1) * (2 * T * 16) +
+                    if (i >= 2) wait_parity(kD1Free, i - 2);
+                    const uint4 u = lds128(sb + sbuf + (uint32_t)(i >> 1 & 1) * (2 * T * 16) +
                                            ((cg >> 2) * T + tl) * 16);
                     sc = make_float4(__uint_as_float(u.x), __uint_as_float(u.y),
                                      __uint_as_float(u.z), __uint_as_float(u.w));
-                    keep_scale(it + 1, next_scale);
-                    if (s + 2 < s1) next_scale = load_scale(s + 2);
+                    keep_scale(i + 2, next_scale);
+                    next_scale = load_scale(i + 4);
                 }
                 // ---- du W of this token
                 uint64_t v[4][4], qq, ff;
-                const uint32_t cfa = st + L::OR + tl * CF::kCoefBytes;
+                const uint32_t cfa = st + L::OR + tl * CF::kTileCoefBytes;
                 {
                     float acc[4][8];
 #pragma unroll
@@ -446,22 +469,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) arrived<8>(acc[j]);
                     tc_fence_before();
-                    arrive(kD1Free);
+                    arrive(at_parity(kD1Free, i));
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
 #pragma unroll
                         for (int p = 0; p < 4; ++p)
                             v[j][p] = fmul2(pack2(acc[j][2 * p], acc[j][2 * p + 1]), ff);
                 }
-                // ---- the products before have to be through before their sums move, and before
-                // the next ones may go
-                if (it > 0) wait(kD2Done, (uint32_t)it - 1);
-                if (s > s0 && (s - s0) % kDrain == 0) {
-                    tc_fence_after();
-                    drain(s - s0 == kDrain, nullptr);
-                    tc_fence_before();
-                }
-                if (!K8) arrive(kGate);  // x is its own operand
                 // ---- the stream's gradient through comb, and y's through pre
                 auto add = [&](uint32_t coef, const uint4 &u) {
                     const uint4 w = lds128(coef);
@@ -501,11 +515,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int p = 0; p < 4; ++p) ffma2(v[j][p], qq, xv[p]);
                 }
-                if (K8) {
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                    arrive(kGate);
-                    if (it > 0) wait(kOutFree, (uint32_t)it - 1);
+                // ---- du^T x may go, once the step before is through it (the other group's, which
+                // is half a step ahead) and its sums have moved on where it is time
+                if (K8) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                if (i > 0) wait_parity(kD2Done, i - 1);
+                if (i > run && (i - run) % kDrain == 0) {
+                    tc_fence_after();
+                    drain(i - run == kDrain, nullptr);
+                    tc_fence_before();
                 }
+                arrive(at_parity(kGate, i));
+                if (K8 && i > 0) wait_parity(kOutFree, i - 1);
                 const uint32_t out = K8 ? sb + L::OO : st;
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
@@ -513,12 +533,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                            make_uint4(pack_pair(v[j][0]), pack_pair(v[j][1]), pack_pair(v[j][2]),
                                       pack_pair(v[j][3])));
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                arrive(kOut + slot);
+                arrive(at_stage(kOut, i));
             }
-            wait(kD2Done, (uint32_t)it - 1);
-            tc_fence_after();
-            drain(s1 - s0 <= kDrain, a.dwp + partial * MIX * FT);
-            tc_fence_before();
+            it = end;
+            if ((run & 1) == group) {
+                wait_parity(kD2Done, end - 1);
+                tc_fence_after();
+                drain(s1 - s0 <= kDrain, a.dwp + partial * MIX * FT);
+                tc_fence_before();
+            }
             meet<1, 32 * kComputeWarps>();  // before maxima and W are written anew
         });
     }
@@ -578,10 +601,10 @@ cudaError_t launch(const PreBackward &p, const MainArgs &m, const DeviceInfo &di
 
 Split split_dx_dw_tma(int64_t n, int64_t d, int64_t most) { return Split::of(n, d, CH, T, most); }
 
-// Two steps of tokens at least: below, the other kernel is as fast (8 tokens of
+// Four steps of tokens at least: below, the other kernel is as fast (8 tokens of
 // 4 x 64: both are done before the host is) and needs no tensor maps.
 bool dx_dw_tma_takes(const PreBackward &p) {
-    return p.hc == 4 && p.d >= CH && p.n >= 2 * T && p.n < (int64_t(1) << 31) && forced_path() != kPathGeneral &&
+    return p.hc == 4 && p.d >= CH && p.n >= 4 * T && p.n < (int64_t(1) << 31) && forced_path() != kPathGeneral &&
            (p.x.scales == nullptr || p.d % 16 == 0) && tensor_map_encoder() != nullptr;
 }
 
