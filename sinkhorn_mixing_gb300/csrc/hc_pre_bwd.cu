@@ -23,6 +23,8 @@ constexpr int kMaxBlocks = 160 * 3;  // of k_mix_backward: rows of partial sums
 
 template <int HC>
 __host__ __device__ constexpr int mix_warps() { return 8 * HC / 32; }
+template <int HC>
+__host__ __device__ constexpr int mix_blocks() { return HC == 4 ? 3 : 2; }  // on an SM
 
 // -------------------------------------------------------- k_mix_backward
 // Warps 0-7 sum <dy, x_j> and sum x^2 of up to 8 tokens at a time (2^lg lanes
@@ -74,7 +76,7 @@ struct Record {
 };
 
 template <int HC, bool K8>
-__global__ void __launch_bounds__(256 + 32 * mix_warps<HC>(), 3)
+__global__ void __launch_bounds__(256 + 32 * mix_warps<HC>(), mix_blocks<HC>())
     k_mix_backward(int64_t n, int64_t npad, int64_t nv, int64_t nblk, int lg, int iters, float eps,
                    float norm_eps, float features, const uint4 *__restrict__ dy, Kept x,
                    const float *__restrict__ mixes, const float *__restrict__ scale,
@@ -436,11 +438,11 @@ cudaError_t launch(const PreBackward &p, const DeviceInfo &di, cudaStream_t s) {
     m.dwp = reinterpret_cast<float *>(p.ws + at.dw);
     float *mp = reinterpret_cast<float *>(p.ws + at.mix);
     int lg = 5;
-    while (lg < 8 && (1 << lg) < nv && (p.n >> (8 - lg)) < (int64_t)di.sms * 3) ++lg;
+    while (lg < 8 && (2 << lg) <= nv && (p.n >> (8 - lg)) < (int64_t)di.sms * mix_blocks<HC>()) ++lg;
     const bool tiled = dx_dw_tma_takes(p);
     const int64_t npad = tiled ? (p.n + kTileTokens - 1) / kTileTokens * kTileTokens : p.n;
     const int64_t groups = (npad + (256 >> lg) - 1) / (256 >> lg);
-    const int64_t cap = di.sms * 3 < kMaxBlocks ? di.sms * 3 : kMaxBlocks;
+    const int64_t most = di.sms * mix_blocks<HC>(), cap = most < kMaxBlocks ? most : kMaxBlocks;
     const int blocks = (int)(groups < cap ? groups : cap);
     const size_t smem = (size_t)MW * (2 * p.iters - 1) * 32 * 4;
     if (smem > 48 * 1024) {
