@@ -125,7 +125,6 @@ struct KeptVec {  // 8 channels as loaded
                                          int64_t vec) {
         v = __ldcs(static_cast<const uint4 *>(k.data) + row * nv + vec);
     }
-    __device__ __forceinline__ void zero() { v = make_uint4(0, 0, 0, 0); }
     __device__ __forceinline__ void values(float f[8]) const { unpack8(v, f); }
     // the channels in pairs and unscaled; returns their scale
     __device__ __forceinline__ float pairs(uint64_t f[4]) const {
@@ -144,7 +143,6 @@ struct KeptVec<true> {
         c = __ldcs(static_cast<const uint2 *>(k.data) + row * nv + vec);
         b = __ldg(k.scales + row * nblk + (vec >> 2));
     }
-    __device__ __forceinline__ void zero() { c = make_uint2(0, 0), b = 0; }
     __device__ __forceinline__ void values(float f[8]) const {
         const float s = kept_scale(b);
         e4m3x8_to_float(c, f);

@@ -38,21 +38,76 @@ struct Scatter<N, 0> {
     static __device__ __forceinline__ void run(float *, int, int &, int &) {}
 };
 
+// W channels of a bf16 row, and of a kept one.
+template <int W>
+struct Vec;
+template <>
+struct Vec<8> {
+    using T = uint4;
+    static __device__ __forceinline__ void unpack(const T &v, float f[8]) { unpack8(v, f); }
+    static __device__ __forceinline__ T pack(const float f[8]) { return pack8(f); }
+};
+template <>
+struct Vec<4> {
+    using T = uint2;
+    static __device__ __forceinline__ void unpack(const T &v, float f[4]) {
+        f[0] = bf16lo(v.x), f[1] = bf16hi(v.x), f[2] = bf16lo(v.y), f[3] = bf16hi(v.y);
+    }
+    static __device__ __forceinline__ T pack(const float f[4]) {
+        return make_uint2(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]));
+    }
+};
+template <bool K8, int W>
+struct KeptPart {
+    typename Vec<W>::T v;
+    __device__ __forceinline__ void load(const Kept &k, int64_t row, int64_t nv, int64_t, int64_t i) {
+        v = __ldcs(static_cast<const typename Vec<W>::T *>(k.data) + row * nv + i);
+    }
+    __device__ __forceinline__ void values(float f[W]) const { Vec<W>::unpack(v, f); }
+};
+template <>
+struct KeptPart<true, 8> : KeptVec<true> {};
+template <>
+struct KeptPart<true, 4> {
+    uint32_t c, b;
+    __device__ __forceinline__ void load(const Kept &k, int64_t row, int64_t nv, int64_t nblk,
+                                         int64_t i) {
+        c = __ldcs(static_cast<const uint32_t *>(k.data) + row * nv + i);
+        b = __ldg(k.scales + row * nblk + (i >> 3));
+    }
+    __device__ __forceinline__ void values(float f[4]) const {
+        const float s = kept_scale(b);
+        e4m3x4_to_float(c, f);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) f[e] *= s;
+    }
+};
+
+constexpr __host__ __device__ int part_width(int hc, bool dres) { return hc == 8 && dres ? 4 : 8; }
+
 // 2^lg lanes share a token (32 at least): one warp, or several whose sums
-// meet in shared memory; 256 threads hold 256 >> lg tokens.
+// meet in shared memory; 256 threads hold 256 >> lg tokens.  A lane takes W
+// channels at a time: 8, but 4 at hc = 8 where dres is wanted too, with which and
+// the 72 sums the registers go no further (4,096 tokens of 8 x 5120 in bf16: 252
+// us, with 8 channels 327; without dres 144 us, with 4 channels 150).
 //
 // The FMAs are two wide over neighbouring k (fma.rn.f32x2): the running sums
 // of k and k+1 are one 64-bit register, so the packing costs no register and
 // no instruction, and comb's and post's pairs are loaded as they lie.
 template <int HC, bool R8, bool O8, bool DRES>
 __global__ void __launch_bounds__(256, HC == 4 ? 2 : 1)
-    k_post_backward(int64_t n, int64_t nv, int64_t nblk, int lg, const uint4 *g, Kept out,
+    k_post_backward(int64_t n, int64_t d, int64_t nblk, int lg, const uint16_t *g0, Kept out,
                     Kept res, const float *__restrict__ post, const float *__restrict__ comb,
-                    uint4 *__restrict__ dout, float *__restrict__ dpost,
-                    float *__restrict__ dcomb, uint4 *dres) {
-    constexpr int KP = HC / 2, NS = HC * (HC + 1);
+                    uint16_t *__restrict__ dout0, float *__restrict__ dpost,
+                    float *__restrict__ dcomb, uint16_t *dres0) {
+    constexpr int KP = HC / 2, NS = HC * (HC + 1), W = part_width(HC, DRES);
+    using V = Vec<W>;
     __shared__ float red[8][NS];
     griddep_wait_then_release();
+    const auto *g = reinterpret_cast<const typename V::T *>(g0);
+    auto *dout = reinterpret_cast<typename V::T *>(dout0);
+    auto *dres = reinterpret_cast<typename V::T *>(dres0);
+    const int64_t nv = d / W;
     const int lanes = 1 << lg, slot = threadIdx.x >> lg, l = threadIdx.x & (lanes - 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int tpb = 256 >> lg;
@@ -64,40 +119,42 @@ __global__ void __launch_bounds__(256, HC == 4 ? 2 : 1)
 #pragma unroll
             for (int p = 0; p < KP; ++p) acc[j][p] = 0;
         if (t < n) {
-            uint64_t pk[KP];
-#pragma unroll
-            for (int p = 0; p < KP; ++p)
-                pk[p] = __ldg(reinterpret_cast<const uint64_t *>(post + t * HC) + p);
             for (int64_t v = l; v < nv; v += lanes) {
-                uint4 gv[HC];
-                KeptVec<R8> rv[HC];
-                KeptVec<O8> ov;
+                typename V::T gv[HC];
+                KeptPart<R8, W> rv[HC];
+                KeptPart<O8, W> ov;
 #pragma unroll
-                for (int k = 0; k < HC; ++k) gv[k] = ld_stream(g + (t * HC + k) * nv + v);
+                for (int k = 0; k < HC; ++k) gv[k] = __ldcs(g + (t * HC + k) * nv + v);
 #pragma unroll
                 for (int j = 0; j < HC; ++j) rv[j].load(res, t * HC + j, nv, nblk, v);
                 ov.load(out, t, nv, nblk, v);
-                uint64_t gp[KP][8];
+                uint64_t gp[KP][W];
 #pragma unroll
                 for (int p = 0; p < KP; ++p) {
-                    float a[8], b[8];
-                    unpack8(gv[2 * p], a);
-                    unpack8(gv[2 * p + 1], b);
+                    float a[W], b[W];
+                    V::unpack(gv[2 * p], a);
+                    V::unpack(gv[2 * p + 1], b);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) gp[p][e] = pack2(a[e], b[e]);
+                    for (int e = 0; e < W; ++e) gp[p][e] = pack2(a[e], b[e]);
                 }
-                float f[8], s[8];
+                float f[W], s[W];
+                {
+                    uint64_t pk[KP];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    uint64_t d = fmul2(pk[0], gp[0][e]);
+                    for (int p = 0; p < KP; ++p)
+                        pk[p] = __ldg(reinterpret_cast<const uint64_t *>(post + t * HC) + p);
 #pragma unroll
-                    for (int p = 1; p < KP; ++p) ffma2(d, pk[p], gp[p][e]);
-                    s[e] = sum2(d);
+                    for (int e = 0; e < W; ++e) {
+                        uint64_t sum = fmul2(pk[0], gp[0][e]);
+#pragma unroll
+                        for (int p = 1; p < KP; ++p) ffma2(sum, pk[p], gp[p][e]);
+                        s[e] = sum2(sum);
+                    }
+                    __stcs(dout + t * nv + v, V::pack(s));
                 }
-                st_stream(dout + t * nv + v, pack8(s));
                 ov.values(f);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
+                for (int e = 0; e < W; ++e) {
                     const uint64_t fe = pack2(f[e], f[e]);
 #pragma unroll
                     for (int p = 0; p < KP; ++p) ffma2(acc[HC][p], fe, gp[p][e]);
@@ -106,7 +163,7 @@ __global__ void __launch_bounds__(256, HC == 4 ? 2 : 1)
                 for (int j = 0; j < HC; ++j) {
                     rv[j].values(f);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
+                    for (int e = 0; e < W; ++e) {
                         const uint64_t fe = pack2(f[e], f[e]);
 #pragma unroll
                         for (int p = 0; p < KP; ++p) ffma2(acc[j][p], fe, gp[p][e]);
@@ -118,13 +175,13 @@ __global__ void __launch_bounds__(256, HC == 4 ? 2 : 1)
                             c[p] = __ldg(
                                 reinterpret_cast<const uint64_t *>(comb + (t * HC + j) * HC) + p);
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            uint64_t d = fmul2(c[0], gp[0][e]);
+                        for (int e = 0; e < W; ++e) {
+                            uint64_t sum = fmul2(c[0], gp[0][e]);
 #pragma unroll
-                            for (int p = 1; p < KP; ++p) ffma2(d, c[p], gp[p][e]);
-                            s[e] = sum2(d);
+                            for (int p = 1; p < KP; ++p) ffma2(sum, c[p], gp[p][e]);
+                            s[e] = sum2(sum);
                         }
-                        st_stream(dres + (t * HC + j) * nv + v, pack8(s));
+                        __stcs(dres + (t * HC + j) * nv + v, V::pack(s));
                     }
                 }
             }
@@ -156,10 +213,10 @@ __global__ void __launch_bounds__(256, HC == 4 ? 2 : 1)
 }
 
 template <int HC, bool R8, bool O8>
-cudaError_t launch(int64_t n, int64_t d, const uint4 *g, const Kept &out, const Kept &res,
-                   const float *post, const float *comb, uint4 *dout, float *dpost, float *dcomb,
-                   uint4 *dres, const DeviceInfo &di, cudaStream_t s) {
-    const int64_t nv = d / 8;
+cudaError_t launch(int64_t n, int64_t d, const uint16_t *g, const Kept &out, const Kept &res,
+                   const float *post, const float *comb, uint16_t *dout, float *dpost,
+                   float *dcomb, uint16_t *dres, const DeviceInfo &di, cudaStream_t s) {
+    const int64_t nv = d / part_width(HC, dres != nullptr);
     // a warp per token where the tokens fill the GPU, else more of them, so
     // long as each lane keeps a vector of its own
     int lg = 5;
@@ -168,7 +225,7 @@ cudaError_t launch(int64_t n, int64_t d, const uint4 *g, const Kept &out, const 
     const dim3 grid((unsigned)(want < cap ? want : cap));
     auto *kernel = dres != nullptr ? &k_post_backward<HC, R8, O8, true>
                                    : &k_post_backward<HC, R8, O8, false>;
-    return launch_overlapped(kernel, grid, dim3(256), 0, s, n, nv, kept_blocks(d), lg, g, out, res,
+    return launch_overlapped(kernel, grid, dim3(256), 0, s, n, d, kept_blocks(d), lg, g, out, res,
                              post, comb, dout, dpost, dcomb, dres);
 }
 
@@ -183,9 +240,7 @@ cudaError_t launch_post_backward(int64_t n, int hc, int64_t d, const uint16_t *g
                              : (o8 ? &launch<4, false, true> : &launch<4, false, false>))
                        : (r8 ? (o8 ? &launch<8, true, true> : &launch<8, true, false>)
                              : (o8 ? &launch<8, false, true> : &launch<8, false, false>));
-    return fn(n, d, reinterpret_cast<const uint4 *>(g), out, res, post, comb,
-              reinterpret_cast<uint4 *>(dout), dpost, dcomb, reinterpret_cast<uint4 *>(dres), di,
-              s);
+    return fn(n, d, g, out, res, post, comb, dout, dpost, dcomb, dres, di, s);
 }
 
 }  // namespace hc

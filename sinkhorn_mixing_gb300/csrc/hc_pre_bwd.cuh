@@ -37,6 +37,12 @@ __device__ __forceinline__ uint32_t pack_pair(uint64_t v) {
     unpack2(v, lo, hi);
     return pack_bf16x2(lo, hi);
 }
+// Shared-memory matrix descriptor without swizzle: blocks of 8 x 16 bytes, `k`
+// bytes to the next block along K, `mn` along M or N.
+__device__ __forceinline__ uint64_t rows16(uint32_t saddr, uint32_t k, uint32_t mn) {
+    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(k >> 4) << 16) |
+           ((uint64_t)(mn >> 4) << 32) | ((uint64_t)1 << 46);
+}
 
 }  // namespace ptx
 }  // namespace hc

@@ -142,14 +142,6 @@ __device__ __forceinline__ void stg64_if(uint8_t *p, uint32_t x, uint32_t y, uin
         "r"(x), "r"(y), "r"(in)
         : "memory");
 }
-// Shared-memory matrix descriptor without swizzle, the M or N axis along the
-// 16-byte rows of 8 x 8 blocks: `mn` bytes to the next 8 of that axis, `k` to
-// the next 8 of K.
-__device__ __forceinline__ uint64_t mn_desc(uint32_t saddr, uint32_t k, uint32_t mn) {
-    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(k >> 4) << 16) |
-           ((uint64_t)(mn >> 4) << 32) | ((uint64_t)1 << 46);
-}
-
 template <int HC, bool K8>
 __global__ void __launch_bounds__(Cfg<HC, K8>::THREADS, 1) k_dx_dw(Args a) {
     using C = Cfg<HC, K8>;
@@ -366,8 +358,8 @@ __global__ void __launch_bounds__(Cfg<HC, K8>::THREADS, 1) k_dx_dw(Args a) {
 #pragma unroll
                     for (int p = 0; p < CF::kProducts; ++p)
                         mma_bf16(tmem + m * CF::kN,
-                                 mn_desc(xo + m * 16 * C::OT + ks * 256, 128, C::OT),
-                                 mn_desc(bo + p * (CF::kN / 8) * C::BT + ks * 256, 128, C::BT),
+                                 rows16(xo + m * 16 * C::OT + ks * 256, 128, C::OT),
+                                 rows16(bo + p * (CF::kN / 8) * C::BT + ks * 256, 128, C::BT),
                                  C::IDESC, rel % kDrain != 0 || ks > 0 || p > 0);
             mma_commit(bar);
         };

@@ -118,14 +118,8 @@ __device__ __forceinline__ void meet() {
     asm volatile("bar.sync %0, %1;" ::"n"(ID), "n"(N) : "memory");
 }
 
-// Matrix descriptors.  rows16: blocks of 8 x 16 bytes without swizzle, `k` bytes
-// to the next block along K, `mn` along M or N.  tiles128: rows of 128 bytes
-// (64 features) with 128-byte swizzle, rows along K; 64 tokens to the next 64
-// features.
-__device__ __forceinline__ uint64_t rows16(uint32_t saddr, uint32_t k, uint32_t mn) {
-    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(k >> 4) << 16) |
-           ((uint64_t)(mn >> 4) << 32) | ((uint64_t)1 << 46);
-}
+// Matrix descriptor of rows of 128 bytes (64 features) with 128-byte swizzle, rows
+// along K; T tokens to the next 64 features.
 __device__ __forceinline__ uint64_t tiles128(uint32_t saddr) {
     return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(T * 128 >> 4) << 16) |
            ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
