@@ -180,65 +180,82 @@ __global__ void __launch_bounds__(256, HC == 4 ? 4 : 6) k_pre_restore(Slots sl, 
 // every copy of a vector before it stores any of them.  Coefficients are
 // loaded per vector, row by row of comb: they hit the first-level cache, and
 // only the accumulators stay in registers.
-template <int HC>
-__global__ void __launch_bounds__(256, HC == 4 ? 3 : 2) k_post_checkpoint(Slots sl, int64_t nblk,
-                                                         const uint4 *__restrict__ out,
-                                                         const uint4 *res,
-                                                         const float *__restrict__ post,
-                                                         const float *__restrict__ comb, uint4 *y,
-                                                         uint2 *__restrict__ codes,
-                                                         uint8_t *__restrict__ scales) {
+template <int HC, int U>
+__global__ void __launch_bounds__(256, 2) k_post_checkpoint(Slots sl, int64_t nblk,
+                                                            const uint4 *__restrict__ out,
+                                                            const uint4 *res,
+                                                            const float *__restrict__ post,
+                                                            const float *__restrict__ comb,
+                                                            uint4 *y, uint2 *__restrict__ codes,
+                                                            uint8_t *__restrict__ scales) {
     griddep_wait_then_release();
     const uint32_t lane = threadIdx.x & 31;
-    const uint32_t step = gridDim.x * 256u;
-    for (uint32_t i0 = blockIdx.x * 256u + (threadIdx.x & ~31u); i0 < sl.count; i0 += step) {
-        int64_t t;
-        uint32_t v;
-        sl.at(i0 + lane, t, v);
-        const bool in = i0 + lane < sl.count && v < sl.nv;
-        uint4 o = make_uint4(0, 0, 0, 0), r[HC];
-        if (in) {
-            o = ld_stream(out + t * sl.nv + v);
-        } else {
-            t = 0, v = 0;  // a row that exists, for the coefficients
+    const uint32_t step = gridDim.x * 256u * U;
+    for (uint32_t i0 = (blockIdx.x * 256u + (threadIdx.x & ~31u)) * U; i0 < sl.count; i0 += step) {
+        int64_t t[U];
+        uint32_t v[U];
+        bool in[U];
+        uint4 o[U], r[U][HC];
+#pragma unroll
+        for (int a = 0; a < U; ++a) {
+            sl.at(i0 + 32 * a + lane, t[a], v[a]);
+            in[a] = i0 + 32 * a + lane < sl.count && v[a] < sl.nv;
+            if (!in[a]) t[a] = 0, v[a] = 0;  // a row that exists, for the coefficients
+            o[a] = in[a] ? ld_stream(out + t[a] * sl.nv + v[a]) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int j = 0; j < HC; ++j)
+                r[a][j] = in[a] ? ld_stream(res + (t[a] * HC + j) * sl.nv + v[a])
+                                : make_uint4(0, 0, 0, 0);
         }
 #pragma unroll
-        for (int j = 0; j < HC; ++j)
-            r[j] = in ? ld_stream(res + (t * HC + j) * sl.nv + v) : make_uint4(0, 0, 0, 0);
-        float acc[HC][8], f[8];
-        unpack8(o, f);
-        auto load_row = [&](const float *p, float c[HC]) {
+        for (int a = 0; a < U; ++a) {
+            // two copies wide: acc[p][e] is channel e of copies 2p and 2p+1, and the
+            // coefficients' pairs are loaded as they lie
+            uint64_t acc[HC / 2][8], c[HC / 2];
+            float f[8];
+            unpack8(o[a], f);
+            auto load_row = [&](const float *p) {
 #pragma unroll
-            for (int q = 0; q < HC / 4; ++q) {
-                const float4 w = __ldg(reinterpret_cast<const float4 *>(p) + q);
-                c[4 * q] = w.x, c[4 * q + 1] = w.y, c[4 * q + 2] = w.z, c[4 * q + 3] = w.w;
+                for (int q = 0; q < HC / 4; ++q) {
+                    const ulonglong2 w = __ldg(reinterpret_cast<const ulonglong2 *>(p) + q);
+                    c[2 * q] = w.x, c[2 * q + 1] = w.y;
+                }
+            };
+            load_row(post + t[a] * HC);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const uint64_t fe = pack2(f[e], f[e]);
+#pragma unroll
+                for (int p = 0; p < HC / 2; ++p) acc[p][e] = fmul2(c[p], fe);
             }
-        };
-        float c[HC];
-        load_row(post + t * HC, c);
 #pragma unroll
-        for (int k = 0; k < HC; ++k)
+            for (int j = 0; j < HC; ++j) {
+                unpack8(r[a][j], f);
+                load_row(comb + (t[a] * HC + j) * HC);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) acc[k][e] = c[k] * f[e];
+                for (int e = 0; e < 8; ++e) {
+                    const uint64_t fe = pack2(f[e], f[e]);
 #pragma unroll
-        for (int j = 0; j < HC; ++j) {
-            unpack8(r[j], f);
-            load_row(comb + (t * HC + j) * HC, c);
+                    for (int p = 0; p < HC / 2; ++p) ffma2(acc[p][e], c[p], fe);
+                }
+            }
 #pragma unroll
-            for (int k = 0; k < HC; ++k)
+            for (int k = 0; k < HC; ++k) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) acc[k][e] = fmaf(c[k], f[e], acc[k][e]);
-        }
-#pragma unroll
-        for (int k = 0; k < HC; ++k) {
-            const uint4 p = pack8(acc[k]);
-            uint32_t byte;
-            const uint2 c8 = kept_quantise(p, byte);
-            if (in) {
-                const int64_t row = t * HC + k;
-                st_stream(y + row * sl.nv + v, p);
-                __stcs(codes + row * sl.nv + v, c8);
-                if ((lane & 3) == 0) scales[row * nblk + (v >> 2)] = (uint8_t)byte;
+                for (int e = 0; e < 8; ++e) {
+                    float lo, hi;
+                    unpack2(acc[k / 2][e], lo, hi);
+                    f[e] = k % 2 ? hi : lo;
+                }
+                const uint4 p = pack8(f);
+                uint32_t byte;
+                const uint2 c8 = kept_quantise(p, byte);
+                if (in[a]) {
+                    const int64_t row = t[a] * HC + k;
+                    st_stream(y + row * sl.nv + v[a], p);
+                    __stcs(codes + row * sl.nv + v[a], c8);
+                    if ((lane & 3) == 0) scales[row * nblk + (v[a] >> 2)] = (uint8_t)byte;
+                }
             }
         }
     }
@@ -303,13 +320,13 @@ cudaError_t launch_post_checkpoint(int64_t n, int hc, int64_t d, const uint16_t 
     const int64_t nblk = kept_blocks(d);
     return by_pieces(n, d, [&](int64_t t0, int64_t nt) {
         const Slots sl = make_slots(nt, d);
-        const dim3 grid = stream_grid(sl, 1, di.sms, hc == 4 ? 3 : 2);
+        const dim3 grid = stream_grid(sl, hc == 4 ? 2 : 1, di.sms, 2);
         const int64_t row = t0 * hc;
         const uint4 *ov = reinterpret_cast<const uint4 *>(out + t0 * d);
         const uint4 *rv = reinterpret_cast<const uint4 *>(res + row * d);
         uint4 *yv = reinterpret_cast<uint4 *>(y + row * d);
         uint2 *cv = reinterpret_cast<uint2 *>(codes + row * d);
-        auto *kernel = hc == 4 ? &k_post_checkpoint<4> : &k_post_checkpoint<8>;
+        auto *kernel = hc == 4 ? &k_post_checkpoint<4, 2> : &k_post_checkpoint<8, 1>;
         return launch_overlapped(kernel, grid, dim3(256), 0, s, sl, nblk, ov, rv, post + row,
                                  comb + row * hc, yv, cv, scales + row * nblk);
     });
