@@ -28,8 +28,9 @@
  *     layouts stated per function.
  *   - Arguments are validated on the host before anything is enqueued; a
  *     call that returns an error has launched nothing.  n == 0 is a valid
- *     no-op (gradients that sum over tokens are then set to zero).  Supported: hc in {4, 8}; d > 0 with d % 8 == 0; every pointer
- *     16-byte aligned; iters >= 1; eps >= 0; norm_eps >= 0.
+ *     no-op (gradients that sum over tokens are then set to zero).  Supported:
+ *     hc in {4, 8}; d > 0 with d % 8 == 0; every pointer 16-byte aligned (but
+ *     scale bytes of kept streams); iters >= 1; eps >= 0; norm_eps >= 0.
  *   - Outputs must not overlap inputs or each other, except that hc_post may
  *     write y over residual exactly (y == residual), and where an entry point
  *     states another such pair.
@@ -317,7 +318,8 @@ hc_status hc_mixes_pre_noalloc(int64_t n, int hc, int64_t d, int iters, float ep
  * nearest even; magnitudes that would round to 2^128, which bf16 lacks, become
  * the code 240 below it.  NaN and the infinities become the code 0x7F (NaN) and
  * leave the block's other channels as they would be without them.  Bytes from
- * elsewhere are taken as they are in 1..254; 0 reads as a scale of 0.
+ * elsewhere are taken as they are in 1..254; 0 reads as a scale of 0.  scales
+ * pointers need no alignment.
  *
  * hc_checkpoint      x [rows, d] bf16 (in) -> codes, scales (out)
  * hc_restore         codes, scales (in) -> x [rows, d] bf16 (out); exact: every

@@ -23,6 +23,9 @@ hc_status check_tokens(int64_t n, int hc, int64_t d) {
     return st != HC_OK ? st : check_rows(n * hc, d);
 }
 
+// scale bytes are read and written one by one: any address will do
+hc_status scales_ok(const uint8_t *p) { return p == nullptr ? HC_ERR_INVALID_ARG : HC_OK; }
+
 uint64_t scale_bytes(uint64_t rows, int64_t d) { return rows * (uint64_t)hc::kept_blocks(d); }
 
 // A kept tensor's two ranges: bf16 rows (no scales), or codes and scales.
@@ -42,7 +45,7 @@ hc_status hc_checkpoint(int64_t rows, int64_t d, const uint16_t *x, uint8_t *cod
     hc_status st = check_rows(rows, d);
     if (st != HC_OK) return st;
     if (rows == 0) return HC_OK;
-    if ((st = ptrs_ok({x, codes, scales})) != HC_OK) return st;
+    if ((st = ptrs_ok({x, codes})) != HC_OK || (st = scales_ok(scales)) != HC_OK) return st;
     const uint64_t el = (uint64_t)rows * d;
     if (!disjoint({rng(codes, el), rng(scales, scale_bytes(rows, d))}, {rng(x, el * 2)}))
         return HC_ERR_INVALID_ARG;
@@ -57,7 +60,7 @@ hc_status hc_restore(int64_t rows, int64_t d, const uint8_t *codes, const uint8_
     hc_status st = check_rows(rows, d);
     if (st != HC_OK) return st;
     if (rows == 0) return HC_OK;
-    if ((st = ptrs_ok({codes, scales, x})) != HC_OK) return st;
+    if ((st = ptrs_ok({codes, x})) != HC_OK || (st = scales_ok(scales)) != HC_OK) return st;
     const uint64_t el = (uint64_t)rows * d;
     if (!disjoint({rng(x, el * 2)}, {rng(codes, el), rng(scales, scale_bytes(rows, d))}))
         return HC_ERR_INVALID_ARG;
@@ -73,7 +76,7 @@ hc_status hc_pre_restore(int64_t n, int hc, int64_t d, const uint8_t *codes,
     hc_status st = check_tokens(n, hc, d);
     if (st != HC_OK) return st;
     if (n == 0) return HC_OK;
-    if ((st = ptrs_ok({codes, scales, pre, y})) != HC_OK) return st;
+    if ((st = ptrs_ok({codes, pre, y})) != HC_OK || (st = scales_ok(scales)) != HC_OK) return st;
     const uint64_t rows = (uint64_t)n * hc;
     if (!disjoint({rng(y, (uint64_t)n * d * 2)},
                   {rng(codes, rows * d), rng(scales, scale_bytes(rows, d)), rng(pre, rows * 4)}))
@@ -90,7 +93,9 @@ hc_status hc_post_checkpoint(int64_t n, int hc, int64_t d, const uint16_t *out,
     hc_status st = check_tokens(n, hc, d);
     if (st != HC_OK) return st;
     if (n == 0) return HC_OK;
-    if ((st = ptrs_ok({out, residual, post, comb, y, codes, scales})) != HC_OK) return st;
+    if ((st = ptrs_ok({out, residual, post, comb, y, codes})) != HC_OK ||
+        (st = scales_ok(scales)) != HC_OK)
+        return st;
     const uint64_t rows = (uint64_t)n * hc, el = rows * d;
     const Range ry = rng(y, el * 2), rr = rng(residual, el * 2), rc = rng(codes, el),
                 rs = rng(scales, scale_bytes(rows, d));
@@ -116,7 +121,7 @@ hc_status hc_post_backward(int64_t n, int hc, int64_t d, const uint16_t *dy, con
     if (st != HC_OK) return st;
     if (n == 0) return HC_OK;
     if ((st = ptrs_ok({dy, out, residual, post, comb, dout, dpost, dcomb})) != HC_OK) return st;
-    if (!al16(out_scales) || !al16(residual_scales) || !al16(dresidual)) return HC_ERR_MISALIGNED;
+    if (!al16(dresidual)) return HC_ERR_MISALIGNED;
     const uint64_t rows = (uint64_t)n * hc;
     const Range rg = rng(dy, rows * d * 2);
     const Range rres = dresidual ? rng(dresidual, rows * d * 2) : Range{0, 0};
@@ -168,7 +173,7 @@ hc_status hc_mixes_pre_backward(int64_t n, int hc, int64_t d, int iters, float e
     if ((st = ptrs_ok({dy, x, mixes, w_mix, hc_scale, hc_base, dpost, dcomb, dx, dw_mix, dscale,
                        dbase})) != HC_OK)
         return st;
-    if (!al16(x_scales) || !al16(dstream)) return HC_ERR_MISALIGNED;
+    if (!al16(dstream)) return HC_ERR_MISALIGNED;
     if (workspace == nullptr || workspace_bytes < hc::pre_backward_bytes(n, hc, d))
         return HC_ERR_INVALID_ARG;
     if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return HC_ERR_MISALIGNED;

@@ -68,7 +68,13 @@ def test_rows(L):
         assert call(fn, CK, (4, 1 << 25)) == UNSUPPORTED
         assert fn(0, 64, None, None, None, None) == OK
         assert call(fn, CK, (4, 64), codes=NULL) == INVALID
-        assert call(fn, CK, (4, 64), scales=fake(2, 8)) == MISALIGNED
+    for fn, order in ((L.hc_checkpoint, CK), (L.hc_restore, ("codes", "scales", "x"))):
+        for k in ("x", "codes"):
+            assert call(fn, order, (4, 64), **{k: fake(9, 8)}) == MISALIGNED
+        for k in order:
+            assert call(fn, order, (4, 64), **{k: NULL}) == INVALID
+        if _no_gpu():
+            assert call(fn, order, (4, 64), scales=fake(9, 3)) == CUDA   # any address
     # outputs on inputs and on each other
     assert call(L.hc_checkpoint, CK, (4, 64), codes=fake(0, 256)) == INVALID
     assert call(L.hc_checkpoint, CK, (4, 64), scales=fake(1, 240)) == INVALID
@@ -97,8 +103,7 @@ def test_post_backward(L):
     for k in ("dy", "out", "res", "post", "comb", "dout", "dpost", "dcomb"):
         assert call(L.hc_post_backward, PB, (4, 4, 64), **{k: NULL}) == INVALID
         assert call(L.hc_post_backward, PB, (4, 4, 64), **{k: fake(30, 8)}) == MISALIGNED
-    for k in ("osc", "rsc", "dres"):
-        assert call(L.hc_post_backward, PB, (4, 4, 64), **{k: fake(30, 8)}) == MISALIGNED
+    assert call(L.hc_post_backward, PB, (4, 4, 64), dres=fake(30, 8)) == MISALIGNED
     assert call(L.hc_post_backward, PB, (4, 4, 64), dout=fake(0, 512)) == INVALID
     assert call(L.hc_post_backward, PB, (4, 4, 64), dres=fake(0, 16)) == INVALID
     assert call(L.hc_post_backward, PB, (4, 4, 64), dres=fake(3)) == INVALID
@@ -125,8 +130,7 @@ def test_mixes_pre_backward(L):
     for k in ("dy", "x", "mixes", "w", "scale", "base", "dpost", "dcomb", "dx", "dw", "dsc", "db"):
         assert mb(L, **{k: NULL}) == INVALID
         assert mb(L, **{k: fake(30, 4)}) == MISALIGNED
-    for k in ("xsc", "ds"):
-        assert mb(L, **{k: fake(30, 4)}) == MISALIGNED
+    assert mb(L, ds=fake(30, 4)) == MISALIGNED
     assert mb(L, ws=NULL) == INVALID
     assert mb(L, wsb=need - 1) == INVALID
     assert mb(L, ws=fake(40, 16)) == MISALIGNED

@@ -93,6 +93,28 @@ def test_checkpoint_shapes_and_empty(hc):
     assert c.shape == (0, 4, 64) and hc.hc_restore(c, s).shape == (0, 4, 64)
 
 
+def test_scales_at_any_address(hc):
+    # a batch cut by tokens: 12 scale bytes a token, so the cut's scales are not aligned
+    g = gen(4)
+    x = bf16((40, 4, 72), g).cuda()
+    codes, scales = hc.hc_checkpoint(x)
+    cut = (codes[1:].contiguous(), scales[1:])
+    assert scales[1:].data_ptr() % 16 == 12
+    assert torch.equal(hc.hc_restore(*cut), hc.hc_restore(codes, scales)[1:])
+    pre = torch.rand(40, 4, generator=g).cuda()
+    assert torch.equal(hc.hc_pre_restore(*cut, pre[1:].contiguous()),
+                       hc.hc_pre_restore(codes, scales, pre)[1:])
+    out = torch.full((500,), 7, dtype=torch.uint8, device="cuda")
+    _, s2 = hc.hc_checkpoint(x, scales=out[5:485].view(40, 4, 3))
+    assert torch.equal(s2, scales) and bool((out[:5] == 7).all()) and bool((out[485:] == 7).all())
+    c = pre_case(hc, 40, 4, 72, True)
+    d = dict(c, x=(c["x"][0], torch.cat([c["x"][1].view(-1)[:1], c["x"][1].view(-1)])[1:]
+                   .view(40, 4, 3)))
+    assert d["x"][1].data_ptr() % 16 == 1
+    for a, b in zip(run_pre(hc, d), run_pre(hc, c)):
+        assert torch.equal(a, b)
+
+
 def test_checkpoint_long_tensor(hc):
     # more than 2^31 channels: the last rows are where 32-bit offsets would fail
     n, d = 110_000, 20480
