@@ -57,7 +57,7 @@ cudaError_t by_pieces(int64_t rows, int64_t d, Fn f) {
 // ---------------------------------------------------------- k_checkpoint
 // A lane takes 16 channels where the other kernels take 8: two lanes a block,
 // one shuffle, and 16 bytes of codes a store.  65,536 tokens of 4 x 5120 (4.07
-// GB): 674 us, 6.03 TB/s; with 8 channels a lane 780 us.  A row's last lane may
+// GB): 647 us, 6.3 TB/s; with 8 channels a lane 780 us.  A row's last lane may
 // have 8.
 template <int U>
 __global__ void __launch_bounds__(256, 5) k_checkpoint(Slots sl, int64_t nblk,
@@ -102,6 +102,7 @@ __global__ void __launch_bounds__(256, 5) k_checkpoint(Slots sl, int64_t nblk,
 }
 
 // ------------------------------------------------------------- k_restore
+// 16,384 tokens of 4 x 5120 (1.02 GB): 160 us, 6.35 TB/s.
 template <int U>
 __global__ void __launch_bounds__(256) k_restore(Slots sl, int64_t nblk, Kept k,
                                                  uint4 *__restrict__ x) {
@@ -130,7 +131,8 @@ __global__ void __launch_bounds__(256) k_restore(Slots sl, int64_t nblk, Kept k,
 }
 
 // --------------------------------------------------------- k_pre_restore
-// y = sum_j pre_j x_j of kept copies, the copies in the order of hc_pre.
+// y = sum_j pre_j x_j of kept copies, the copies in the order of hc_pre.  16,384
+// tokens of 4 x 5120 (514 MB): 81 us, 6.35 TB/s.
 template <int HC, int U>
 __global__ void __launch_bounds__(256, HC == 4 ? 4 : 6) k_pre_restore(Slots sl, int64_t nblk, Kept k,
                                                      const float *__restrict__ pre,
@@ -179,7 +181,9 @@ __global__ void __launch_bounds__(256, HC == 4 ? 4 : 6) k_pre_restore(Slots sl, 
 // order, so y is hc_post's bit for bit.  residual may equal y: a lane loads
 // every copy of a vector before it stores any of them.  Coefficients are
 // loaded per vector, row by row of comb: they hit the first-level cache, and
-// only the accumulators stay in registers.
+// only the accumulators stay in registers.  16,384 tokens of 4 x 5120 (1.86 GB):
+// 300 us, 6.2 TB/s (one vector in flight and one-wide FMAs: 335 us); 4,096 of
+// 8 x 5120 (886 MB): 186 us, 4.8 TB/s, 16 warps an SM.
 template <int HC, int U>
 __global__ void __launch_bounds__(256, 2) k_post_checkpoint(Slots sl, int64_t nblk,
                                                             const uint4 *__restrict__ out,
@@ -263,8 +267,7 @@ __global__ void __launch_bounds__(256, 2) k_post_checkpoint(Slots sl, int64_t nb
 
 // As many blocks as are resident at once (each kernel's launch bounds): they
 // share the slots evenly, where more blocks would leave a last partial wave
-// (k_checkpoint 674 -> 643 us, k_post_checkpoint of 4,096 tokens 90 -> 85 us;
-// k_restore was 2 us faster with 8 than with its 5).
+// (k_checkpoint 674 -> 643 us; k_restore was 2 us faster with 8 than with its 5).
 dim3 stream_grid(const Slots &sl, int u, int sms, int blocks_per_sm) {
     const int64_t per_block = 256 * u;
     const int64_t want = (sl.count + per_block - 1) / per_block;

@@ -6,7 +6,9 @@
 //   dres_j    = sum_k comb_jk G_k                 (a vector, when wanted)
 // One pass: each of G, out and r is read once (out and r in bf16 or as kept in
 // 8 bits), HC * (HC + 1) running sums stay in registers until the token's end.
-// It is an HBM stream with 2 + HC (+ HC) FMAs per stream element.
+// It is an HBM stream with 2 + HC (+ HC) FMAs per stream element: 16,384 tokens of
+// 4 x 5120, out and r in 8 bits (1.27 GB), 217 us, 5.85 TB/s; 4,096 of 8 x 5120 in
+// bf16 (755 MB) 140 us, 5.4 TB/s.
 #include "hc_kept.cuh"
 
 namespace hc {
@@ -89,7 +91,7 @@ constexpr __host__ __device__ int part_width(int hc, bool dres) { return hc == 8
 // meet in shared memory; 256 threads hold 256 >> lg tokens.  A lane takes W
 // channels at a time: 8, but 4 at hc = 8 where dres is wanted too, with which and
 // the 72 sums the registers go no further (4,096 tokens of 8 x 5120 in bf16: 252
-// us, with 8 channels 327; without dres 144 us, with 4 channels 150).
+// us, with 8 channels 327; without dres 140 us, with 4 channels 150).
 //
 // The FMAs are two wide over neighbouring k (fma.rn.f32x2): the running sums
 // of k and k+1 are one 64-bit register, so the packing costs no register and
