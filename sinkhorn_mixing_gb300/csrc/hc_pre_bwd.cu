@@ -449,9 +449,12 @@ cudaError_t launch(const PreBackward &p, const DeviceInfo &di, cudaStream_t s) {
     const int blocks = (int)(groups < cap ? groups : cap);
     const size_t smem = (size_t)MW * (2 * p.iters - 1) * 32 * 4;
     if (smem > 48 * 1024) {
-        const cudaError_t e =
-            cudaFuncSetAttribute(k_mix_backward<HC, K8>,
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        // the limit is the most that any call asks for, not this call's: one with fewer
+        // steps on another thread must not lower it before this launch
+        static SmemState state;
+        const int limit = MW * (2 * kBackwardMaxIters - 1) * 32 * 4;
+        const cudaError_t e = allow_smem(
+            state, reinterpret_cast<const void *>(k_mix_backward<HC, K8>), limit, di);
         if (e != cudaSuccess) return e;
     }
     cudaError_t e = launch_overlapped(

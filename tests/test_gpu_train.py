@@ -1,5 +1,6 @@
 """The training operators against their 64-bit forms (GPU)."""
 import ctypes
+import threading
 
 import numpy as np
 import pytest
@@ -422,6 +423,34 @@ def test_same_bits_every_time(hc):
         for _ in range(3):
             for a, b in zip(run_pre(hc, c), first):
                 assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("k8", [True, False])
+def test_two_threads_with_different_steps(hc, k8):
+    # the steps set the coefficients kernel's shared memory: 131 KB and 77 KB here
+    c = pre_case(hc, 9, 8, 64, k8)
+    steps = (256, 150)
+    want = [run_pre(hc, c, iters=i) for i in steps]
+    torch.cuda.synchronize()
+    failed = []
+
+    def calls(which):
+        try:
+            s = torch.cuda.Stream()
+            with torch.cuda.stream(s):
+                for _ in range(300):
+                    got = run_pre(hc, c, iters=steps[which])
+                s.synchronize()
+                assert all(torch.equal(a, b) for a, b in zip(got, want[which]))
+        except Exception as e:
+            failed.append(e)
+
+    threads = [threading.Thread(target=calls, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed, failed
 
 
 def test_on_another_stream_and_in_a_graph(hc):
