@@ -371,13 +371,16 @@ def _sized(t, name, count, dtype, index):
 
 
 def _made(t, name, shape, dtype, dev, stream):
-    """An output: the caller's, checked, or a new one.  A tensor made here for a
-    stream other than the current one is not handed out again by the allocator
-    before that stream is done with it."""
+    """An output: the caller's, checked, or a new one.  One made for another stream
+    is that stream's own memory, so that nothing the current stream has still to do
+    can touch it, and it is not handed out again before the current stream, which
+    may read it, is done with it either."""
     if t is None:
-        t = torch.empty(shape, dtype=dtype, device=dev)
-        if stream is not None:
-            t.record_stream(stream)
+        if stream is None:
+            return torch.empty(shape, dtype=dtype, device=dev)
+        with torch.cuda.stream(stream):
+            t = torch.empty(shape, dtype=dtype, device=dev)
+        t.record_stream(torch.cuda.current_stream(dev))
         return t
     _on(t, name, dtype, dev.index)
     if t.shape != shape:

@@ -453,6 +453,33 @@ def test_two_threads_with_different_steps(hc, k8):
     assert not failed, failed
 
 
+def test_outputs_for_another_stream(hc):
+    # a tensor freed while the current stream has still to read it is not an output of another
+    # stream's call: same size, so that the allocator would hand the block out at once
+    codes, scales = hc.hc_checkpoint(torch.full((4096, 256), 3.0, dtype=torch.bfloat16,
+                                                device="cuda"))
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    block = torch.full((4096, 256), 5.0, dtype=torch.bfloat16, device="cuda")
+    torch.cuda.synchronize()
+    at = block.data_ptr()
+    kept = torch.empty_like(block)
+    torch.cuda._sleep(50_000_000)
+    kept.copy_(block)
+    del block
+    got = hc.hc_restore(codes, scales, stream=s)
+    assert got.data_ptr() != at
+    # and the other way round: read on the current stream, freed, made again for s
+    s.synchronize()
+    torch.cuda._sleep(50_000_000)
+    again = got.clone()
+    at = got.data_ptr()
+    del got
+    assert hc.hc_restore(codes, scales, stream=s).data_ptr() != at
+    torch.cuda.synchronize()
+    assert bool((kept == 5.0).all()) and bool((again == 3.0).all())
+
+
 def test_on_another_stream_and_in_a_graph(hc):
     c = pre_case(hc, 300, 4, 512, True)
     p = post_case(hc, 300, 4, 512, True, True)
