@@ -362,7 +362,7 @@ __global__ void __launch_bounds__(256 + 32 * mix_warps<HC>(), mix_blocks<HC>())
 // ----------------------------------------------------------------- k_sum
 // dW from the partial sums of the teams that worked on a band, four features a
 // thread; behind those blocks, one warp per column of k_mix_backward's partial
-// sums.  It adds 9 us to a call at hc = 4 and d = 5120, 17 us at hc = 8.
+// sums.  It adds 9 us to a call at hc = 4 and d = 5120, 21 us at hc = 8.
 template <int HC>
 __global__ void __launch_bounds__(256) k_sum(Split sp, int64_t d, int per_slice,
                                              const float *__restrict__ dwp,

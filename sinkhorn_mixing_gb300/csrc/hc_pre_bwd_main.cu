@@ -16,7 +16,7 @@
 // of W in shared memory, and walks over tokens in steps (Split); each step's
 // tiles come through a two-stage ring of 16-byte asynchronous copies, the next
 // step's loads running under this one's arithmetic.  4,096 tokens of 8 x 5120 in 8
-// bits (0.9 GB): 431 us, bound by a step's latency (41% of the issue slots, 58% of
+// bits (0.9 GB): 412 us, bound by a step's latency (41% of the issue slots, 58% of
 // the LSU's wavefronts).
 #include <cuda_fp16.h>
 #include <type_traits>
@@ -442,11 +442,13 @@ __global__ void __launch_bounds__(Cfg<HC, K8>::THREADS, 1) k_dx_dw(Args a) {
                 issue(K8 ? rel - 1 : rel);
             }
             if (!K8 || rel > 0) ++commits;
+            // The next step's loads go into the stage that step s - 1 has left.  Two of each
+            // scheduler's four warps issue theirs before du W and two behind it, so that the
+            // loads and the products of a step run beside each other (4,096 tokens of 8 x 5120
+            // in 8 bits 498 -> 487 us, in bf16 537 -> 532; all behind it 540).  The condition is
+            // formed twice from `warp`: a register that held it would spill others (502).
             uint32_t next_scale = 0;
-            if (s + 1 < s1) {  // into the stage that step s - 1 has left
-                load(s + 1, rel + 1);
-                next_scale = load_scale(s + 1);
-            }
+            if (s + 1 < s1 && (warp & 4)) load(s + 1, rel + 1), next_scale = load_scale(s + 1);
 
             // ---- du W
             const uint32_t st = sb + (uint32_t)(rel & 1) * C::STAGE;
@@ -482,6 +484,8 @@ __global__ void __launch_bounds__(Cfg<HC, K8>::THREADS, 1) k_dx_dw(Args a) {
                         }
                     }
                 }
+
+            if (s + 1 < s1 && !(warp & 4)) load(s + 1, rel + 1), next_scale = load_scale(s + 1);
 
             // ---- the other terms, token by token, two channels wide
 #pragma unroll
