@@ -448,16 +448,14 @@ cudaError_t launch(const PreBackward &p, const DeviceInfo &di, cudaStream_t s) {
     const int64_t most = di.sms * mix_blocks<HC>(), cap = most < kMaxBlocks ? most : kMaxBlocks;
     const int blocks = (int)(groups < cap ? groups : cap);
     const size_t smem = (size_t)MW * (2 * p.iters - 1) * 32 * 4;
-    if (smem > 48 * 1024) {
-        // the limit is the most that any call asks for, not this call's: one with fewer
-        // steps on another thread must not lower it before this launch
-        static SmemState state;
-        const int limit = MW * (2 * kBackwardMaxIters - 1) * 32 * 4;
-        const cudaError_t e = allow_smem(
-            state, reinterpret_cast<const void *>(k_mix_backward<HC, K8>), limit, di);
-        if (e != cudaSuccess) return e;
-    }
-    cudaError_t e = launch_overlapped(
+    // Asked for whatever this call needs: what a launch may use without asking covers the
+    // kernel's static part too.  The limit is the most that any call asks for, not this call's:
+    // one with fewer steps on another thread must not lower it before this launch.
+    static SmemState state;
+    cudaError_t e = allow_smem(state, reinterpret_cast<const void *>(k_mix_backward<HC, K8>),
+                               MW * (2 * kBackwardMaxIters - 1) * 32 * 4, di);
+    if (e != cudaSuccess) return e;
+    e = launch_overlapped(
         k_mix_backward<HC, K8>, dim3(blocks), dim3(256 + 32 * MW), smem, s, p.n, npad, nv, nblk, lg,
         p.iters, p.eps, p.norm_eps, (float)F, reinterpret_cast<const uint4 *>(p.dy), p.x, p.mixes,
         p.scale, p.base, p.dpost, p.dcomb, m.rec, (int)tiled, tiled ? m.scales : nullptr, mp);
