@@ -175,7 +175,7 @@ hc_status hc_mixes(int64_t n, int hc, int64_t d, float norm_eps, const uint16_t 
         return HC_ERR_INVALID_ARG;
     hc::DeviceInfo di;
     cudaError_t e = hc::device_info(&di);
-    if (e != cudaSuccess) return HC_ERR_CUDA;
+    if (e != cudaSuccess) return cuda_failed();
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (hc::decode_supported(n, hc, d, di)) {
         return from_cuda(hc::launch_decode(n, hc, d, /*iters=*/1, /*eps=*/0.0f, norm_eps, x,
@@ -211,7 +211,7 @@ hc_status hc_split_sinkhorn(int64_t n, int hc, int iters, float eps, const float
                   {rng(mixes, n * mix * 4ull), rng(hc_scale, 12), rng(hc_base, mix * 4)}))
         return HC_ERR_INVALID_ARG;
     hc::DeviceInfo di;
-    if (hc::device_info(&di) != cudaSuccess) return HC_ERR_CUDA;
+    if (hc::device_info(&di) != cudaSuccess) return cuda_failed();
     return from_cuda(hc::launch_split_sinkhorn(n, hc, iters, eps, mixes, hc_scale, hc_base, pre,
                                                post, comb, di,
                                                reinterpret_cast<cudaStream_t>(stream)));
@@ -227,7 +227,7 @@ hc_status hc_pre(int64_t n, int hc, int64_t d, const uint16_t *x, const float *p
                   {rng(x, (uint64_t)n * hc * d * 2), rng(pre, (uint64_t)n * hc * 4)}))
         return HC_ERR_INVALID_ARG;
     hc::DeviceInfo di;
-    if (hc::device_info(&di) != cudaSuccess) return HC_ERR_CUDA;
+    if (hc::device_info(&di) != cudaSuccess) return cuda_failed();
     return from_cuda(
         hc::launch_pre(n, hc, d, x, pre, y, di, reinterpret_cast<cudaStream_t>(stream)));
 }
@@ -246,7 +246,7 @@ hc_status hc_post(int64_t n, int hc, int64_t d, const uint16_t *out, const uint1
                          rng(comb, (uint64_t)n * hc * hc * 4)}))
         return HC_ERR_INVALID_ARG;
     hc::DeviceInfo di;
-    if (hc::device_info(&di) != cudaSuccess) return HC_ERR_CUDA;
+    if (hc::device_info(&di) != cudaSuccess) return cuda_failed();
     return from_cuda(hc::launch_post(n, hc, d, out, residual, post, comb, y, di,
                                      reinterpret_cast<cudaStream_t>(stream)));
 }
@@ -301,7 +301,7 @@ hc_status mixes_pre_impl(int64_t n, int hc, int64_t d, int iters, float eps, flo
         if (ws_status != HC_OK && !(hc == 4 && d % 256 == 0 && d <= 5120)) return ws_status;
     }
     hc::DeviceInfo di;
-    if (hc::device_info(&di) != cudaSuccess) return HC_ERR_CUDA;
+    if (hc::device_info(&di) != cudaSuccess) return cuda_failed();
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (hc::decode_supported(n, hc, d, di)) {
         return from_cuda(hc::launch_decode(n, hc, d, iters, eps, norm_eps, x, w_mix, hc_scale,
@@ -405,7 +405,7 @@ hc_status hc_post_mixes_pre(int64_t n, int hc, int64_t d, const uint16_t *out,
                   {rres}))
         return HC_ERR_INVALID_ARG;
     hc::DeviceInfo di;
-    if (hc::device_info(&di) != cudaSuccess) return HC_ERR_CUDA;
+    if (hc::device_info(&di) != cudaSuccess) return cuda_failed();
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (hc::fused_supported(hc, d, di) && !hc::decode_supported(n, hc, d, di)) {
         // one launch: the ring streams the residual; the new stream goes to
@@ -439,7 +439,7 @@ hc_status hc_post_mixes_pre(int64_t n, int hc, int64_t d, const uint16_t *out,
             return HC_ERR_INVALID_ARG;
     }
     const cudaError_t e = hc::launch_post(n, hc, d, out, residual, post, comb, x_next, di, s);
-    if (e != cudaSuccess) return HC_ERR_CUDA;
+    if (e != cudaSuccess) return cuda_failed();
     return mixes_pre_impl(n, hc, d, iters, eps, norm_eps, x_next, w_mix, hc_scale, hc_base,
                           nullptr, 0.0f, mixes, pre_next, post_next, comb_next, y_next, workspace,
                           workspace_bytes, stream);
@@ -448,19 +448,19 @@ hc_status hc_post_mixes_pre(int64_t n, int hc, int64_t d, const uint16_t *out,
 hc_status hc_selftest_wait_timeout(uint64_t limit_ns, hc_stream_t stream) {
     if (limit_ns < 1 || limit_ns > 1000000000ull) return HC_ERR_INVALID_ARG;
     hc::DeviceInfo di;
-    if (hc::device_info(&di) != cudaSuccess) return HC_ERR_CUDA;
+    if (hc::device_info(&di) != cudaSuccess) return cuda_failed();
     return from_cuda(
         hc::launch_wait_timeout(limit_ns, di, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 hc_status hc_device_error(unsigned int *flags, int clear) {
-    if (cudaDeviceSynchronize() != cudaSuccess) return HC_ERR_CUDA;
+    if (cudaDeviceSynchronize() != cudaSuccess) return cuda_failed();
     unsigned int v = 0;
-    if (cudaMemcpyFromSymbol(&v, hc::g_err_word, sizeof v) != cudaSuccess) return HC_ERR_CUDA;
+    if (cudaMemcpyFromSymbol(&v, hc::g_err_word, sizeof v) != cudaSuccess) return cuda_failed();
     if (flags) *flags = v;
     if (clear) {
         const unsigned int z = 0;
-        if (cudaMemcpyToSymbol(hc::g_err_word, &z, sizeof z) != cudaSuccess) return HC_ERR_CUDA;
+        if (cudaMemcpyToSymbol(hc::g_err_word, &z, sizeof z) != cudaSuccess) return cuda_failed();
     }
     return HC_OK;
 }

@@ -50,7 +50,7 @@ hc_status hc_checkpoint(int64_t rows, int64_t d, const uint16_t *x, uint8_t *cod
     if (!disjoint({rng(codes, el), rng(scales, scale_bytes(rows, d))}, {rng(x, el * 2)}))
         return HC_ERR_INVALID_ARG;
     hc::DeviceInfo di;
-    if (hc::device_info(&di) != cudaSuccess) return HC_ERR_CUDA;
+    if (hc::device_info(&di) != cudaSuccess) return cuda_failed();
     return from_cuda(hc::launch_checkpoint(rows, d, x, codes, scales, di,
                                            reinterpret_cast<cudaStream_t>(stream)));
 }
@@ -65,7 +65,7 @@ hc_status hc_restore(int64_t rows, int64_t d, const uint8_t *codes, const uint8_
     if (!disjoint({rng(x, el * 2)}, {rng(codes, el), rng(scales, scale_bytes(rows, d))}))
         return HC_ERR_INVALID_ARG;
     hc::DeviceInfo di;
-    if (hc::device_info(&di) != cudaSuccess) return HC_ERR_CUDA;
+    if (hc::device_info(&di) != cudaSuccess) return cuda_failed();
     return from_cuda(hc::launch_restore(rows, d, hc::Kept{codes, scales}, x, di,
                                         reinterpret_cast<cudaStream_t>(stream)));
 }
@@ -82,7 +82,7 @@ hc_status hc_pre_restore(int64_t n, int hc, int64_t d, const uint8_t *codes,
                   {rng(codes, rows * d), rng(scales, scale_bytes(rows, d)), rng(pre, rows * 4)}))
         return HC_ERR_INVALID_ARG;
     hc::DeviceInfo di;
-    if (hc::device_info(&di) != cudaSuccess) return HC_ERR_CUDA;
+    if (hc::device_info(&di) != cudaSuccess) return cuda_failed();
     return from_cuda(hc::launch_pre_restore(n, hc, d, hc::Kept{codes, scales}, pre, y, di,
                                             reinterpret_cast<cudaStream_t>(stream)));
 }
@@ -106,7 +106,7 @@ hc_status hc_post_checkpoint(int64_t n, int hc, int64_t d, const uint16_t *out,
         !disjoint({rc, rs}, {rr}))
         return HC_ERR_INVALID_ARG;
     hc::DeviceInfo di;
-    if (hc::device_info(&di) != cudaSuccess) return HC_ERR_CUDA;
+    if (hc::device_info(&di) != cudaSuccess) return cuda_failed();
     return from_cuda(hc::launch_post_checkpoint(n, hc, d, out, residual, post, comb, y, codes,
                                                 scales, di,
                                                 reinterpret_cast<cudaStream_t>(stream)));
@@ -136,7 +136,7 @@ hc_status hc_post_backward(int64_t n, int hc, int64_t d, const uint16_t *dy, con
         !disjoint({rdo, rdp, rdc}, {rg}))
         return HC_ERR_INVALID_ARG;
     hc::DeviceInfo di;
-    if (hc::device_info(&di) != cudaSuccess) return HC_ERR_CUDA;
+    if (hc::device_info(&di) != cudaSuccess) return cuda_failed();
     return from_cuda(hc::launch_post_backward(
         n, hc, d, dy, hc::Kept{out, out_scales}, hc::Kept{residual, residual_scales}, post, comb,
         dout, dpost, dcomb, dresidual, di, reinterpret_cast<cudaStream_t>(stream)));
@@ -190,7 +190,7 @@ hc_status hc_mixes_pre_backward(int64_t n, int hc, int64_t d, int iters, float e
         !disjoint({rdw, rds, rdb, rws}, {rg}))
         return HC_ERR_INVALID_ARG;
     hc::DeviceInfo di;
-    if (hc::device_info(&di) != cudaSuccess) return HC_ERR_CUDA;
+    if (hc::device_info(&di) != cudaSuccess) return cuda_failed();
     hc::PreBackward p;
     p.n = n, p.d = d, p.hc = hc, p.iters = iters, p.eps = eps, p.norm_eps = norm_eps;
     p.dy = dy, p.x = hc::Kept{x, x_scales}, p.mixes = mixes, p.w = w_mix, p.scale = hc_scale;

@@ -62,7 +62,13 @@ inline bool disjoint(std::initializer_list<Range> outs, std::initializer_list<Ra
     return true;
 }
 
-inline hc_status from_cuda(cudaError_t e) { return e == cudaSuccess ? HC_OK : HC_ERR_CUDA; }
+// A CUDA call or launch has failed.  The runtime keeps its error until someone asks for it, and
+// the next call's launch does (launched()): it is taken away here, with the call it belongs to.
+inline hc_status cuda_failed() {
+    (void)cudaGetLastError();
+    return HC_ERR_CUDA;
+}
+inline hc_status from_cuda(cudaError_t e) { return e == cudaSuccess ? HC_OK : cuda_failed(); }
 
 }  // namespace check
 }  // namespace hc

@@ -19,6 +19,7 @@
 #include <mutex>
 
 #include "../../include/hcmix.h"
+#include "hc_check.h"
 #include "hc_internal.h"
 
 namespace hc {
@@ -101,9 +102,9 @@ extern "C" hc_status hc_mixes_pre_noalloc(int64_t n, int hc, int64_t d, int iter
             if (hc::overlap(outs[a], b)) return HC_ERR_INVALID_ARG;
     }
     hc::DeviceInfo di;
-    if (hc::device_info(&di) != cudaSuccess) return HC_ERR_CUDA;
+    if (hc::device_info(&di) != cudaSuccess) return hc::check::cuda_failed();
     float *scratch = nullptr;
-    if (hc::scratch_on_current_device(di, &scratch) != cudaSuccess) return HC_ERR_CUDA;
+    if (hc::scratch_on_current_device(di, &scratch) != cudaSuccess) return hc::check::cuda_failed();
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     // the projection hc_mixes_pre's general path uses (tensor cores where
     // they take the shape), with W converted inside the kernel: no scratch
@@ -113,5 +114,5 @@ extern "C" hc_status hc_mixes_pre_noalloc(int64_t n, int hc, int64_t d, int iter
         e = hc::launch_split_sinkhorn(n, hc, iters, eps, scratch, hc_scale, hc_base, pre, post,
                                       comb, di, s);
     if (e == cudaSuccess) e = hc::launch_pre(n, hc, d, x, pre, y, di, s);
-    return e == cudaSuccess ? HC_OK : HC_ERR_CUDA;
+    return hc::check::from_cuda(e);
 }
