@@ -114,7 +114,9 @@ __global__ void __launch_bounds__(256 + 32 * mix_warps<HC>(), mix_blocks<HC>())
                                             bf16x2_to_f32x2(yv.z), bf16x2_to_f32x2(yv.w)};
 #pragma unroll
                     for (int j = 0; j < HC; ++j) {
-                        // a vector lies in one block: its scale comes after its sums
+                        // A vector lies in one block: its scale comes after its sums (to the
+                        // squares twice, as its own square may be infinite, or 0, where theirs
+                        // times it is not)
                         uint64_t f[4];
                         const float sc = xv[j].pairs(f);
                         uint64_t dot = fmul2(f[0], y2[0]), sq = fmul2(f[0], f[0]);
@@ -124,7 +126,7 @@ __global__ void __launch_bounds__(256 + 32 * mix_warps<HC>(), mix_blocks<HC>())
                             ffma2(sq, f[e], f[e]);
                         }
                         acc[j] = K8 ? fmaf(sc, sum2(dot), acc[j]) : acc[j] + sum2(dot);
-                        acc[HC] = K8 ? fmaf(sc * sc, sum2(sq), acc[HC]) : acc[HC] + sum2(sq);
+                        acc[HC] = K8 ? fmaf(sc, sc * sum2(sq), acc[HC]) : acc[HC] + sum2(sq);
                     }
                 }
             }
