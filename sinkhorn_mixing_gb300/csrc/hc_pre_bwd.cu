@@ -318,8 +318,10 @@ __global__ void __launch_bounds__(256 + 32 * mix_warps<HC>(), mix_blocks<HC>())
 #pragma unroll
                 for (int p = 0; p < 3; ++p) {
                     const __nv_bfloat16 b = __float2bfloat16_rn(v);
+                    const float part = __bfloat162float(b);
                     to.put3(p * MIX + i, __bfloat16_as_ushort(b));
-                    v -= __bfloat162float(b);
+                    // nothing is left of an infinity (inf - inf would be NaN, and dW's sum too)
+                    v = fabsf(part) == INFINITY ? 0.0f : v - part;
                 }
             };
             put(j, du0);

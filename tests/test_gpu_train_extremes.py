@@ -46,3 +46,25 @@ def test_zeros_in_a_block_of_large_numbers(hc, copies, n, d):
     tol = UBF * dx.abs() + (ref.split_tolerance(20) + (16 + copies) * U32) * mag
     assert torch.all((got[0][3].cpu().double() - dx).abs() <= tol)
     assert bool((x[3, 1, 2] == 2.0 ** 100).all())
+
+
+@pytest.mark.parametrize("copies,n", [(4, 40), (4, 200), (8, 40)])
+@pytest.mark.parametrize("k8", [True, False])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_infinite_gradient_of_one_mix_number(hc, copies, n, k8, sign):
+    # du of one mix number is infinite: its row of dW is du x summed, infinite with x's sign (NaN
+    # where x is 0), and the other rows are as they were
+    c = t.pre_case(hc, n, copies, 96, k8)
+    plain = t.run_pre(hc, c)
+    c["dpost"][5, 2] = sign * float("inf")
+    got = t.run_pre(hc, c)
+    row = copies + 2
+    x = ref.values(c["x"])[5].flatten()
+    dw = got[1].cpu().double()
+    keep = [i for i in range(dw.shape[0]) if i != row]
+    assert torch.equal(got[1][keep], plain[1][keep])
+    assert torch.equal(dw[row][x != 0], sign * x[x != 0].sign() * float("inf"))
+    assert bool(torch.isnan(dw[row][x == 0]).all())
+    assert float(got[3][row]) == sign * float("inf")
+    tokens = [i for i in range(n) if i != 5]
+    assert torch.equal(got[0][tokens], plain[0][tokens])
