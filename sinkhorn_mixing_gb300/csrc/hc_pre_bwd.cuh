@@ -28,6 +28,13 @@ __device__ __forceinline__ void arrived(float v[N]) {
 #pragma unroll
     for (int i = 0; i < N; ++i) asm volatile("" : "+f"(v[i]));
 }
+// The calling thread's products still under way, after which a block may end: they read its shared
+// memory and write its TMEM.  `bar` (count 1) has had no arrival, so that the phase that is waited
+// for is this commit's whatever other barriers' waits gave up on.
+__device__ __forceinline__ void settle_products(uint32_t bar) {
+    mma_commit(bar);
+    settle_bar(bar, 0);
+}
 // a binary32 pattern in both halves of a pair
 __device__ __forceinline__ uint64_t twice(uint32_t v) {
     return pack2(__uint_as_float(v), __uint_as_float(v));

@@ -25,6 +25,7 @@
 // of 4 x 5120 in 8 bits took 1,994 us in all, this way 1,828.)
 #include <cuda_fp16.h>
 
+#include "hc_loads.h"
 #include "hc_pre_bwd.cuh"
 #include "hc_pre_bwd.h"
 
@@ -60,7 +61,7 @@ struct Lay {
 // names a phase by its parity and each group sees every second step.
 enum Bar { kFull = 0, kEmpty = 32, kOut = 64, kD1Full = 96, kD1Free = 112, kGate = 128,
            kD2Done = 144, kOutFree = 160 };
-constexpr int kAbort = 176, kTmem = 180, kCalm = 184, kMaxima = 192;
+constexpr int kAbort = 176, kTmem = 180, kLast = 184, kMaxima = 192;
 constexpr int kD2 = 256, kSums = kD2 + 2 * CF::kN;  // TMEM columns; du W has 0..255
 static_assert(kSums + 2 * MIX <= 512, "TMEM");
 
@@ -151,7 +152,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t sb = su32(smem), eb = sb + L::OE;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     volatile int *abort = reinterpret_cast<int *>(smem + L::OE + kAbort);
-    volatile int *calm = reinterpret_cast<int *>(smem + L::OE + kCalm);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::OE + kTmem);
     float *maxima = reinterpret_cast<float *>(smem + L::OE + kMaxima);  // per warp
 
@@ -168,8 +168,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(eb + kD2Done + 8 * i, 1);
             mbar_init(eb + kOutFree + 8 * i, 1);
         }
+        mbar_init(eb + kLast, 1);
         *abort = 0;
-        *calm = 0;
         if ((sb & 1023u) != 0) {  // swizzled tiles need it
             atomicOr(a.err, kErrSmemLayout);
             *abort = 1;
@@ -212,10 +212,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) {
             griddep_wait_then_release();
             asm volatile("fence.proxy.async;" ::: "memory");  // records were plain stores
+            RingLoads<kStages> loads;
             over_runs(a.split, [&](int64_t slice, int64_t, int64_t s0, int64_t s1) {
                 for (int64_t s = s0; s < s1; ++s, ++it) {
                     if (it >= kStages && !wait_stage(kEmpty, it - kStages)) continue;
                     if (*abort) continue;
+                    loads.issue();
                     const uint32_t st = stage(it), bar = eb + at_stage(kFull, it);
                     mbar_expect_tx(bar, L::X + T * CH * 2 + CF::kTileBytes +
                                             (a.has_g ? T * FT * 2 : 0));
@@ -226,10 +228,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tma_load_2d(st + L::OY, &map_y, c, t, bar);
                 }
             });
-            if (*abort)  // what was loaded has to land before this block ends
-                for (int64_t i = it > kStages ? it - kStages : 0; i < it; ++i)
-                    wait_bar<false>(eb + at_stage(kFull, i), (uint32_t)(i / kStages) & 1, calm,
-                                    a.err, 1000000);
+            // what was loaded has to land before this block ends, waited for by others or not
+            loads.in_flight([&](int stage, uint32_t parity) {
+                settle_bar(eb + kFull + 8 * stage, parity);
+            });
         }
     } else if (warp == kComputeWarps + 1) {
         // ---------------------------------------------------- products
@@ -293,17 +295,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             __syncwarp();
         });
-        if (lane == 0 && *abort) {  // products in flight read shared memory: let them end
-            const uint64_t t0 = gtimer();
-            while (gtimer() - t0 < 1000000) {
-            }
-        }
+        if (lane == 0) settle_products(eb + kLast);
     } else if (warp == kComputeWarps + 2) {
         // ------------------------------------------------------ stores
         if (lane == 0) {
             over_runs(a.split, [&](int64_t slice, int64_t, int64_t s0, int64_t s1) {
                 for (int64_t s = s0; s < s1; ++s, ++it) {
-                    if (!wait_stage(kOut, it)) continue;
+                    if (!wait_stage(kOut, it) || *abort) continue;
                     if (slice * CH < a.d)  // else behind the last channel (Split)
                         tma_store_3d(&map_dx, (int)slice * CH, (int)(s * T), 0,
                                      K8 ? sb + L::OO : stage(it));

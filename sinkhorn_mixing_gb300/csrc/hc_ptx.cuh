@@ -89,6 +89,17 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile
     }
 }
 
+// Waits for the phase of `bar` with the given parity for limit_ns at most, whether the block is
+// aborting or not: what is in flight at the end of a block that gave up still reads or writes its
+// shared memory or TMEM, which the next block gets.
+__device__ __forceinline__ void settle_bar(uint32_t bar, uint32_t parity,
+                                           uint64_t limit_ns = kTimeoutNs) {
+    if (mbar_try(bar, parity)) return;
+    const uint64_t t0 = gtimer();
+    while (!mbar_try(bar, parity) && gtimer() - t0 <= limit_ns) {
+    }
+}
+
 __device__ __forceinline__ uint32_t mapa(uint32_t addr, uint32_t rank) {
     uint32_t r;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
