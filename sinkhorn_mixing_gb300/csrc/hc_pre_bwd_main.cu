@@ -84,6 +84,7 @@ struct Cfg {
     static constexpr int SMEM = OE + 256;
     static constexpr uint32_t IDESC = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 15) | (1u << 16) |
                                       ((uint32_t)(CF::kN >> 3) << 17) | (8u << 24);
+    static_assert(WARPS % 2 == 0 && 16 + WARPS * 4 + 8 <= 256, "barriers, flags, maxima");
     static_assert(SMEM <= 232448, "shared memory");
     static_assert(SCALES <= THREADS, "a scale byte per thread");
 };
@@ -155,9 +156,11 @@ __global__ void __launch_bounds__(Cfg<HC, K8>::THREADS, 1) k_dx_dw(Args a) {
     volatile int *abort = reinterpret_cast<int *>(smem + C::OE + 8);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::OE + 12);
     float *maxima = reinterpret_cast<float *>(smem + C::OE + 16);  // per warp
+    const uint32_t last = sb + C::OE + 16 + C::WARPS * 4;  // barrier of the end, after a timeout
 
     if (tid == 0) {
         mbar_init(bar, 1);
+        mbar_init(last, 1);
         *abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -573,6 +576,7 @@ __global__ void __launch_bounds__(Cfg<HC, K8>::THREADS, 1) k_dx_dw(Args a) {
         tc_fence_after();
         step += s1 - s0;
     }
+    if (tid == 0 && *abort) settle_products(last);  // what a wait gave up on
     __syncthreads();
     if (warp == 0)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512)
