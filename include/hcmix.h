@@ -397,6 +397,17 @@ hc_status hc_post_backward(int64_t n, int hc, int64_t d, const uint16_t *dy, con
  *   not shared with another call in flight; its contents need not be kept.
  * iters <= 256 (else HC_ERR_UNSUPPORTED).  The sums run in a fixed order: the
  * same call gives the same bits.
+ * dx's sum over i has both factors, r dm_i and w_i, rounded to 11 significant
+ * bits: numbers more than 2^28 below the token's largest |r dm_i|, or below the
+ * largest |w| of the 64 or 128 channels (all copies) that a block works on,
+ * have fewer, and more than 2^38 below it they count as zero.  The sum itself
+ * and the other terms are binary32, and dx is rounded to bf16 once; where dx is
+ * that sum alone its error grows by a few per cent, and an element whose terms
+ * cancel may lose more of its own size.  dw_mix keeps 24 bits of r dm_i.
+ * Infinities: an infinite r dm_i makes its row of dw_mix infinite with x's sign
+ * (NaN where x is 0) and the token's dx infinite or NaN; other rows and tokens
+ * are as they were.  A token whose mean square is above binary32's range has
+ * r = 0 here.
  */
 size_t hc_mixes_pre_backward_bytes(int64_t n, int hc, int64_t d);
 hc_status hc_mixes_pre_backward(int64_t n, int hc, int64_t d, int iters, float eps, float norm_eps,

@@ -132,7 +132,7 @@ __global__ void __launch_bounds__(256) k_restore(Slots sl, int64_t nblk, Kept k,
 
 // --------------------------------------------------------- k_pre_restore
 // y = sum_j pre_j x_j of kept copies, the copies in the order of hc_pre.  16,384
-// tokens of 4 x 5120 (514 MB): 81 us, 6.35 TB/s.
+// tokens of 4 x 5120 (514 MB): 80 us, 6.4 TB/s; of 8 x 5120 (860 MB): 144 us, 6.0 TB/s.
 template <int HC, int U>
 __global__ void __launch_bounds__(256, HC == 4 ? 4 : 6) k_pre_restore(Slots sl, int64_t nblk, Kept k,
                                                      const float *__restrict__ pre,
@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(256, HC == 4 ? 4 : 6) k_pre_restore(Slots sl, 
 // loaded per vector, row by row of comb: they hit the first-level cache, and
 // only the accumulators stay in registers.  16,384 tokens of 4 x 5120 (1.86 GB):
 // 300 us, 6.2 TB/s (one vector in flight and one-wide FMAs: 335 us); 4,096 of
-// 8 x 5120 (886 MB): 186 us, 4.8 TB/s, 16 warps an SM.
+// 8 x 5120 (886 MB): 186 us, 4.8 TB/s (128 registers leave 16 warps an SM).
 template <int HC, int U>
 __global__ void __launch_bounds__(256, 2) k_post_checkpoint(Slots sl, int64_t nblk,
                                                             const uint4 *__restrict__ out,

@@ -7,8 +7,10 @@
 // One pass: each of G, out and r is read once (out and r in bf16 or as kept in
 // 8 bits), HC * (HC + 1) running sums stay in registers until the token's end.
 // It is an HBM stream with 2 + HC (+ HC) FMAs per stream element: 16,384 tokens of
-// 4 x 5120, out and r in 8 bits (1.27 GB), 217 us, 5.85 TB/s; 4,096 of 8 x 5120 in
-// bf16 (755 MB) 140 us, 5.4 TB/s.
+// 4 x 5120, out and r in 8 bits (1.27 GB), 217 us, 5.9 TB/s; in bf16 (1.68 GB) 256 us, 6.6
+// TB/s; with dres 323 and 396 us, 6.0 and 5.9 TB/s.  4,096 of 8 x 5120 in bf16 (757 MB) 139
+// us, 5.4 TB/s; in 8 bits (575 MB) 144 us, 4.0 TB/s; with dres 249 and 262 us, 4.4 and 3.5
+// TB/s, where the sums take 255 registers and one block is on an SM.
 #include "hc_kept.cuh"
 
 namespace hc {

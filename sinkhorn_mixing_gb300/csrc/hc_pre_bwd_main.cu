@@ -16,8 +16,8 @@
 // of W in shared memory, and walks over tokens in steps (Split); each step's
 // tiles come through a two-stage ring of 16-byte asynchronous copies, the next
 // step's loads running under this one's arithmetic.  4,096 tokens of 8 x 5120 in 8
-// bits (0.9 GB): 412 us, bound by a step's latency (41% of the issue slots, 58% of
-// the LSU's wavefronts).
+// bits (0.9 GB): 412 us; no unit is full (LSU wavefronts 67%, issue slots 44%, DRAM 33%,
+// tensor pipe 18%): all warps go through a step together, and nothing runs under its waits.
 #include <cuda_fp16.h>
 #include <type_traits>
 
@@ -73,7 +73,7 @@ struct Cfg {
     static constexpr int STAGE = (SA + T * AP + 127) / 128 * 128;
     // the block's memory: two stages, a longer ring for du3, which products still under way read
     // (three stages, which would fit at HC = 8 in 8 bits, took longer: 4,096 tokens of 8 x 5120
-    // 607 us against 525)
+    // 607 us against 525 for two in the same build)
     static constexpr int BRING = K8 ? 3 : 2;
     static constexpr int OB = 2 * STAGE, OO = OB + BRING * BBYTES;  // du3 ring; x operand (K8)
     static constexpr int OW = OO + (K8 ? OBYTES : 0), WREG = 2 * KS;

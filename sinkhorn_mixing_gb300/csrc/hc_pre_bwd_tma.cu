@@ -547,7 +547,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                      : "memory");
 }
 
-// [hc][n][d] view of a stream: boxes of 64 channels, 64 tokens, all copies.
+// [hc][n][d] view of a stream: boxes of 64 channels, T tokens, all copies.
 bool stream_map(CUtensorMap *map, const void *p, bool bytes, int64_t n, int64_t d) {
     const cuuint64_t es = bytes ? 1 : 2;
     const cuuint64_t dim[3] = {(cuuint64_t)d, (cuuint64_t)n, 4};
