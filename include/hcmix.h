@@ -13,6 +13,8 @@
  *                      next (same docstring)
  *   hc_checkpoint and the entry points after it: the stream kept in 8 bits for
  *                      the backward pass, and the gradients of the above
+ *   hc_norm, hc_embed  the norm of rows and the stream's first value, with their
+ *                      gradients
  *
  * Conventions shared by every entry point
  *   - Every tensor pointer is a DEVICE pointer owned by the caller.  The
@@ -29,8 +31,9 @@
  *   - Arguments are validated on the host before anything is enqueued; a
  *     call that returns an error has launched nothing.  n == 0 is a valid
  *     no-op (gradients that sum over tokens are then set to zero).  Supported:
- *     hc in {4, 8}; d > 0 with d % 8 == 0; every pointer 16-byte aligned (but
- *     scale bytes of kept streams); iters >= 1; eps >= 0; norm_eps >= 0.
+ *     hc in {4, 8} (hc_embed: {1, 4, 8}); d > 0 with d % 8 == 0; every pointer
+ *     16-byte aligned (but scale bytes of kept streams, and token ids); iters >= 1;
+ *     eps >= 0; norm_eps >= 0.
  *   - Outputs must not overlap inputs or each other, except that hc_post may
  *     write y over residual exactly (y == residual), and where an entry point
  *     states another such pair.
@@ -66,13 +69,21 @@ typedef enum hc_status {
     HC_OK = 0,
     HC_ERR_INVALID_ARG = 1,  /* null pointer, negative size, bad iters/eps,
                                 overlapping buffers, workspace too small */
-    HC_ERR_UNSUPPORTED = 2,  /* hc not in {4, 8}, sizes beyond int64 range, iters
-                                above an entry point's limit */
+    HC_ERR_UNSUPPORTED = 2,  /* hc not in {4, 8} (hc_embed: {1, 4, 8}), sizes beyond
+                                int64 range, iters or a count above an entry
+                                point's limit, an unknown type */
     HC_ERR_MISALIGNED = 3,   /* d % 8 != 0 or a pointer not 16-byte aligned */
     HC_ERR_CUDA = 4          /* a CUDA runtime call or launch failed */
 } hc_status;
 
 #define HCMIX_ABI_VERSION 1
+
+/* Types of the rows of hc_norm and of the tables of hc_embed. */
+typedef enum hc_dtype {
+    HC_BF16 = 0,
+    HC_F16 = 1,
+    HC_F32 = 2
+} hc_dtype;
 
 /* Static, NUL-terminated description of a status code.  Never NULL. */
 const char *hc_status_string(hc_status s);
@@ -417,6 +428,80 @@ hc_status hc_mixes_pre_backward(int64_t n, int hc, int64_t d, int iters, float e
                                 const uint16_t *dstream, uint16_t *dx, float *dw_mix,
                                 float *dscale, float *dbase, void *workspace,
                                 size_t workspace_bytes, hc_stream_t stream);
+
+/*
+ * hc_norm -- the norm of rows, as a sublayer reads its input: with mu the row's
+ * mean (center != 0: layer norm) or 0 (center == 0: RMS norm, the one that
+ * hc_mixes_pre_norm applies),
+ *   r_t = 1 / sqrt( mean_c (x_{t,c} - mu_t)^2 + eps )
+ *   y_{t,c} = (x_{t,c} - mu_t) * r_t * weight_c + bias_c
+ * in binary32, stored in x's type rounded to nearest even.
+ *   x [rows, d] (in), y [rows, d] (out): dtype is an hc_dtype; y == x (in place)
+ *   is allowed
+ *   weight, bias [d] float (in, each may be NULL: ones, zeros)
+ * A sublayer that is recomputed from a kept stream runs hc_pre_restore, then this.
+ * A row whose sum of squares is above binary32's range has r = 0; eps = 0 and a
+ * row whose squares are all 0 gives NaN, as the formula does.
+ */
+hc_status hc_norm(int64_t rows, int64_t d, int dtype, int center, float eps, const void *x,
+                  const float *weight, const float *bias, void *y, hc_stream_t stream);
+
+/*
+ * hc_norm_backward -- gradients of hc_norm from dy, the gradient of its y.  With
+ * h = (x - mu) r and g = dy * weight, per row:
+ *   dx = r (g - h mean_c(g h))              (center == 0)
+ *   dx = r (g - mean_c(g) - h mean_c(g h))  (center != 0)
+ *   dweight_c = sum_t dy_{t,c} h_{t,c};  dbias_c = sum_t dy_{t,c}
+ * mu and r are formed from x again; the forward call keeps nothing.
+ *   dy, x [rows, d] (in), dx [rows, d] (out): dtype; dx == dy is allowed
+ *   weight [d] float (in, may be NULL: ones)
+ *   dweight, dbias [d] float (out, each may be NULL): sums over this call's rows,
+ *   written and not added to; zeros for rows == 0
+ *   workspace: hc_norm_backward_bytes(rows, d) bytes, 256-byte aligned, not shared
+ *   with another call in flight; its contents need not be kept.
+ * The sums run in a fixed order: the same call gives the same bits.  With
+ * hc_mixes_pre_norm forward, x is hc_pre's y (hc_pre, hc_pre_restore) and dx is
+ * the dy of hc_mixes_pre_backward.
+ */
+size_t hc_norm_backward_bytes(int64_t rows, int64_t d);
+hc_status hc_norm_backward(int64_t rows, int64_t d, int dtype, int center, float eps,
+                           const void *dy, const void *x, const float *weight, void *dx,
+                           float *dweight, float *dbias, void *workspace, size_t workspace_bytes,
+                           hc_stream_t stream);
+
+/*
+ * hc_embed -- the first value of the stream: each token's row of a table, in every
+ * copy,
+ *   x_{t,j,c} = bf16( scale * table_{id_t,c} )  for j = 0 .. hc-1.
+ *   ids [n] int32 or int64 (id_bytes 4 or 8) (in); an id outside 0 .. vocab-1
+ *   (padding) names no row: its token's copies are zeros
+ *   table [vocab, d] (in), dtype an hc_dtype;  x [n, hc, d] bf16 (out)
+ * hc in {1, 4, 8} (1: a plain embedding); n <= 2^30, vocab <= 2^31 - 2 (else
+ * HC_ERR_UNSUPPORTED); scale finite.
+ */
+hc_status hc_embed(int64_t n, int hc, int64_t d, int64_t vocab, int id_bytes, int dtype,
+                   float scale, const void *ids, const void *table, uint16_t *x,
+                   hc_stream_t stream);
+
+/*
+ * hc_embed_backward -- the gradient of hc_embed's table from dx, the gradient of x:
+ *   dtable_{v,c} = scale * sum_{t: id_t = v} sum_j dx_{t,j,c}
+ * The sums are binary32 and are rounded to the table's type once.
+ *   ids, scale, vocab as in hc_embed;  dx [n, hc, d] bf16 (in); the gradients of
+ *   tokens whose id names no row are not read
+ *   dtable [vocab, d], dtype.  accumulate == 0: written, rows that no token names
+ *   become zeros.  accumulate != 0: added to what is there (in binary32, rounded
+ *   once), rows that no token names are left as they are.
+ *   workspace: hc_embed_backward_bytes(n, d, vocab) bytes, 256-byte aligned, not
+ *   shared with another call in flight; its contents need not be kept.
+ * Tokens are sorted by id inside the call and summed in an order that depends on
+ * the ids alone: the same call gives the same bits.
+ */
+size_t hc_embed_backward_bytes(int64_t n, int64_t d, int64_t vocab);
+hc_status hc_embed_backward(int64_t n, int hc, int64_t d, int64_t vocab, int id_bytes, int dtype,
+                            float scale, int accumulate, const void *ids, const uint16_t *dx,
+                            void *dtable, void *workspace, size_t workspace_bytes,
+                            hc_stream_t stream);
 
 /* Number of kernels this library has enqueued in this process (all devices,
  * all threads) since it was loaded.  Host-only counter for diagnostics. */

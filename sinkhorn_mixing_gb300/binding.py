@@ -64,6 +64,16 @@ def lib():
                                             P, P, P, P, P, P, P, ctypes.c_size_t, P]
         L.hc_mixes_pre_backward_bytes.argtypes = [i64, i32, i64]
         L.hc_mixes_pre_backward_bytes.restype = ctypes.c_size_t
+        L.hc_norm.argtypes = [i64, i64, i32, i32, f32, P, P, P, P, P]
+        L.hc_norm_backward.argtypes = [i64, i64, i32, i32, f32, P, P, P, P, P, P, P,
+                                       ctypes.c_size_t, P]
+        L.hc_norm_backward_bytes.argtypes = [i64, i64]
+        L.hc_norm_backward_bytes.restype = ctypes.c_size_t
+        L.hc_embed.argtypes = [i64, i32, i64, i64, i32, i32, f32, P, P, P, P]
+        L.hc_embed_backward.argtypes = [i64, i32, i64, i64, i32, i32, f32, i32, P, P, P, P,
+                                        ctypes.c_size_t, P]
+        L.hc_embed_backward_bytes.argtypes = [i64, i64, i64]
+        L.hc_embed_backward_bytes.restype = ctypes.c_size_t
         L.hc_workspace_bytes.argtypes = [i64, i32, i64]
         L.hc_workspace_bytes.restype = ctypes.c_size_t
         L.hc_device_error.argtypes = [ctypes.POINTER(ctypes.c_uint), i32]
@@ -73,7 +83,8 @@ def lib():
         for f in ("hc_mixes", "hc_split_sinkhorn", "hc_pre", "hc_post", "hc_mixes_pre",
                   "hc_mixes_pre_norm", "hc_post_mixes_pre", "hc_device_error", "hc_checkpoint",
                   "hc_restore", "hc_pre_restore", "hc_post_checkpoint", "hc_post_backward",
-                  "hc_mixes_pre_backward"):
+                  "hc_mixes_pre_backward", "hc_norm", "hc_norm_backward", "hc_embed",
+                  "hc_embed_backward"):
             getattr(L, f).restype = i32
         _lib = L
     return _lib
@@ -570,6 +581,134 @@ def hc_mixes_pre_backward(dy, x, mixes, w_mix, hc_scale, hc_base, dpost, dcomb, 
          dy.data_ptr(), xp, xsp, mp, wp, sp, bp, pp, cp, gp, dx.data_ptr(), dw_mix.data_ptr(),
          dscale.data_ptr(), dbase.data_ptr(), workspace.data_ptr(), workspace.numel())
     return dx, dw_mix, dscale, dbase
+
+
+_ROW_TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}  # hcmix.h, hc_dtype
+
+
+def _row_type(dtype, name):
+    code = _ROW_TYPES.get(dtype)
+    if code is None:
+        raise TypeError("%s must be bfloat16, float16 or float32, got %s" % (name, dtype))
+    return code
+
+
+def _param(t, name, d, index):
+    """An optional fp32 parameter of d values: its pointer, or None."""
+    return None if t is None else _sized(t, name, d, _F32, index)
+
+
+def hc_norm(x, weight=None, bias=None, eps: float = 1e-20, center: bool = False, y=None,
+            stream=None):
+    """x [..., d] bf16, fp16 or fp32 -> (x - mean) / sqrt(variance + eps) * weight + bias over
+    each row, in x's type (y may be x itself).  center=False leaves the mean in and takes the
+    mean square (RMS norm).  weight, bias [d] fp32, or None."""
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("x must be a torch.Tensor")
+    code = _row_type(x.dtype, "x")
+    _need(x, "x", x.dtype)
+    dev = x.device
+    shape, n, d = _rows_of(x)
+    wp, bp = _param(weight, "weight", d, dev.index), _param(bias, "bias", d, dev.index)
+    y = _made(y, "y", shape, x.dtype, dev, stream)
+    _run("hc_norm", dev, stream, n, d, code, int(center), eps, x.data_ptr(), wp, bp, y.data_ptr())
+    return y
+
+
+@functools.lru_cache(maxsize=256)
+def hc_norm_backward_bytes(rows: int, d: int) -> int:
+    return int(lib().hc_norm_backward_bytes(int(rows), int(d)))
+
+
+def hc_norm_backward(dy, x, weight=None, eps: float = 1e-20, center: bool = False,
+                     want_dweight: bool = True, want_dbias: bool = False, dx=None, dweight=None,
+                     dbias=None, workspace=None, stream=None):
+    """Gradients of hc_norm from dy [..., d], of x's type, and x, the forward call's input.
+    Returns (dx, dweight-or-None, dbias-or-None); dx may be dy itself."""
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("x must be a torch.Tensor")
+    code = _row_type(x.dtype, "x")
+    _need(x, "x", x.dtype)
+    dev = x.device
+    shape, n, d = _rows_of(x)
+    _on(dy, "dy", x.dtype, dev.index)
+    if dy.shape != shape:
+        raise ValueError("dy must have shape %s, got %s" % (shape, tuple(dy.shape)))
+    wp = _param(weight, "weight", d, dev.index)
+    dx = _made(dx, "dx", shape, x.dtype, dev, stream)
+    if want_dweight or dweight is not None:
+        dweight = _made(dweight, "dweight", (d,), _F32, dev, stream)
+    if want_dbias or dbias is not None:
+        dbias = _made(dbias, "dbias", (d,), _F32, dev, stream)
+    if workspace is None:
+        workspace = _made(None, "workspace", (hc_norm_backward_bytes(n, d),), _U8, dev, stream)
+    else:
+        _need(workspace, "workspace", _U8, dev)
+    _run("hc_norm_backward", dev, stream, n, d, code, int(center), eps, dy.data_ptr(),
+         x.data_ptr(), wp, dx.data_ptr(), _ptr(dweight), _ptr(dbias), workspace.data_ptr(),
+         workspace.numel())
+    return dx, dweight, dbias
+
+
+def _ids_of(ids):
+    """Token ids, int32 or int64: their device, shape, count and bytes each."""
+    if not isinstance(ids, torch.Tensor):
+        raise TypeError("ids must be a torch.Tensor")
+    if ids.dtype not in (torch.int32, torch.int64):
+        raise TypeError("ids must be int32 or int64, got %s" % ids.dtype)
+    _need(ids, "ids", ids.dtype)
+    return ids.device, tuple(ids.shape), ids.numel(), ids.element_size()
+
+
+def hc_embed(ids, table, hc_mult: int = 4, scale: float = 1.0, x=None, stream=None):
+    """ids [...] int32 or int64, table [vocab, d] bf16, fp16 or fp32 -> the first stream
+    x [..., hc_mult, d] bf16, scale * table[id] in every copy (zeros for an id outside the
+    table, such as -1).  hc_mult is 1, 4 or 8."""
+    dev, shape, n, size = _ids_of(ids)
+    if not isinstance(table, torch.Tensor) or table.dim() != 2:
+        raise TypeError("table must be a tensor [vocab, d]")
+    code = _row_type(table.dtype, "table")
+    _on(table, "table", table.dtype, dev.index)
+    vocab, d = table.shape
+    x = _made(x, "x", shape + (int(hc_mult), d), _BF16, dev, stream)
+    _run("hc_embed", dev, stream, n, int(hc_mult), d, vocab, size, code, scale, ids.data_ptr(),
+         table.data_ptr(), x.data_ptr())
+    return x
+
+
+@functools.lru_cache(maxsize=256)
+def hc_embed_backward_bytes(n: int, d: int, vocab: int) -> int:
+    return int(lib().hc_embed_backward_bytes(int(n), int(d), int(vocab)))
+
+
+def hc_embed_backward(dx, ids, vocab: int, scale: float = 1.0, dtable=None,
+                      accumulate: bool = False, dtype=torch.float32, workspace=None, stream=None):
+    """The gradient of hc_embed's table [vocab, d] from dx [..., hc, d] bf16 and ids [...].
+    accumulate=False writes dtable (a new one of `dtype` where none is given) and clears the
+    rows that no token names; accumulate=True adds to the given dtable.  Returns dtable."""
+    dev, shape, n, size = _ids_of(ids)
+    _on(dx, "dx", _BF16, dev.index)
+    dims = _tokens_of(dx)
+    if dims[0][:-2] != shape:
+        raise ValueError("dx must be %s + (hc, d), got %s" % (shape, dims[0]))
+    hc, d, vocab = dims[2], dims[3], int(vocab)
+    if dtable is None and accumulate:
+        raise ValueError("accumulate needs a dtable to add to")
+    if dtable is not None:
+        if not isinstance(dtable, torch.Tensor):
+            raise TypeError("dtable must be a torch.Tensor")
+        dtype = dtable.dtype
+    code = _row_type(dtype, "dtable")
+    dtable = _made(dtable, "dtable", (vocab, d), dtype, dev, stream)
+    if workspace is None:
+        workspace = _made(None, "workspace", (hc_embed_backward_bytes(n, d, vocab),), _U8, dev,
+                          stream)
+    else:
+        _need(workspace, "workspace", _U8, dev)
+    _run("hc_embed_backward", dev, stream, n, hc, d, vocab, size, code, scale, int(accumulate),
+         ids.data_ptr(), dx.data_ptr(), dtable.data_ptr(), workspace.data_ptr(),
+         workspace.numel())
+    return dtable
 
 
 def hc_launch_count() -> int:

@@ -174,24 +174,4 @@ cudaError_t launch_post_backward(int64_t n, int hc, int64_t d, const uint16_t *g
                                  uint16_t *dout, float *dpost, float *dcomb, uint16_t *dres,
                                  const DeviceInfo &di, cudaStream_t s);
 
-// Programmatic dependent launch of a kernel that starts with
-// griddep_wait_then_release() (see overlap_launches).
-template <typename... P, typename... A>
-cudaError_t launch_overlapped(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem,
-                              cudaStream_t s, A... args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = block;
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = overlap_launches() ? 1 : 0;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
-    if (e != cudaSuccess) return e;
-    return launched();
-}
-
 }  // namespace hc
