@@ -6,21 +6,182 @@
 //
 // The sums over rows: every block adds up the rows it has, in registers, and
 // leaves one row of partial sums; k_norm_sum adds those up in a fixed order.
+#include <algorithm>
+
 #include "hc_rows.cuh"
 
 namespace hc {
 namespace {
 
-constexpr int kMaxParts = 304;  // rows of partial sums: two for each of a GB300's 152 SMs
+constexpr int kStages = 3;         // rows a group has under way
+constexpr int kRingThreads = 512;  // of a block at most: 128 registers each
+constexpr int kParts = 304;        // rows of partial sums: two for each of a GB300's 152 SMs
 
-// rows of partial sums at most, by the width
+// Rows of partial sums at most, by the width: up to four blocks an SM where rows are
+// narrow, and no more than 10 MB of them.
 int64_t max_parts(int64_t rows, int64_t d) {
-    int64_t m = d <= 16384 ? kMaxParts : (int64_t)kMaxParts * 4096 / d;
-    m = m < 1 ? 1 : m;
+    int64_t m = (int64_t)kParts * 8192 / d;
+    m = m > 2 * kParts ? 2 * kParts : m < 1 ? 1 : m;
     return rows < m ? rows : m;
 }
 
 size_t align256(size_t b) { return (b + 255) & ~(size_t)255; }
+
+template <int E>
+__device__ __forceinline__ void put_sums(float *row, int64_t v, const float a[E]) {
+#pragma unroll
+    for (int q = 0; q < E / 4; ++q)
+        reinterpret_cast<float4 *>(row)[v * (E / 4) + q] =
+            make_float4(a[4 * q], a[4 * q + 1], a[4 * q + 2], a[4 * q + 3]);
+}
+
+// Rows of up to 4 x kRingThreads vectors, shared out as in the forward kernel: a group
+// of threads has a row, each thread V vecs of it, copied to shared memory kStages - 1
+// rows ahead.  A thread's channels are the same in every row, so their weights and
+// the sums over the block's rows stay in its registers.  DB: dbias as well.
+//
+// A row takes one round of sums (sum x^2, sum g x) or, for layer norm, two (sum x;
+// then those of (x - mu)^2, g and g (x - mu)); x and dy are read from shared memory
+// again after each, not held.
+template <int DT, bool CENTER, bool DB, int V, bool BLOCK>
+__global__ void __launch_bounds__(BLOCK ? kRingThreads : 256, BLOCK ? 1 : V < 3 ? 2 : 1)
+    k_norm_backward(int64_t rows, int nv, int lg, float eps, const uint4 *dy0,
+                    const uint4 *__restrict__ x0, const float *__restrict__ w, uint4 *dx0,
+                    float *__restrict__ part_w, float *__restrict__ part_b) {
+    constexpr int E = RowVec<DT>::E, NS = CENTER ? 3 : 2;
+    extern __shared__ uint4 ring[];
+    __shared__ __align__(16) float red[2][NS][32];
+    if (BLOCK) clear_red(&red[0][0][0], 2 * NS * 32);
+    griddep_wait_then_release();
+    const int lanes = BLOCK ? blockDim.x : 1 << lg;
+    const int l = BLOCK ? threadIdx.x : threadIdx.x & (lanes - 1);
+    const int groups = BLOCK ? 1 : 256 >> lg;
+    const int64_t step = (int64_t)gridDim.x * groups;
+    int64_t t = (int64_t)blockIdx.x * groups + (BLOCK ? 0 : threadIdx.x >> lg);
+    const float inv_d = 1.0f / (float)(nv * E);
+    auto slot = [&](int stage, int array, int i) {
+        return ring + ((stage * 2 + array) * V + i) * blockDim.x + threadIdx.x;
+    };
+    auto copy = [&](int64_t row, int stage) {
+        if (row < rows) {
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (l + i * lanes < nv) {
+                    copy16_async(slot(stage, 0, i), x0 + row * nv + l + i * lanes);
+                    copy16_async(slot(stage, 1, i), dy0 + row * nv + l + i * lanes);
+                }
+        }
+        copies_commit();
+    };
+#pragma unroll
+    for (int k = 0; k < kStages - 1; ++k) copy(t + k * step, k);
+    float wk[V][E], aw[V][E], ab[DB ? V : 1][E];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        if (l + i * lanes < nv) row_params<E>(w, l + i * lanes, 1.0f, wk[i]);
+#pragma unroll
+        for (int e = 0; e < E; ++e) aw[i][e] = ab[DB ? i : 0][e] = 0.0f;
+    }
+    int at = 0, odd = 0;
+    // a warp stays together until the last of its rows
+    for (int64_t first = t - (BLOCK ? 0 : (threadIdx.x & 31) >> lg); first < rows;
+         first += step, t += step) {
+        copies_wait<kStages - 2>();
+        copy(t + (kStages - 1) * step, at == 0 ? kStages - 1 : at - 1);
+        const bool in = t < rows;
+        float mu = 0.0f, s[NS], f[E], g[E];
+        if (CENTER) {
+            s[0] = 0.0f;
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (in && l + i * lanes < nv) {
+                    RowVec<DT>::get(*slot(at, 0, i), f);
+#pragma unroll
+                    for (int e = 0; e < E; ++e) s[0] += f[e];
+                }
+            group_sum<BLOCK, 1>(s, lg, red[0]);
+            mu = s[0] * inv_d;
+        }
+#pragma unroll
+        for (int i = 0; i < NS; ++i) s[i] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (in && l + i * lanes < nv) {
+                RowVec<DT>::get(*slot(at, 0, i), f);
+                RowVec<DT>::get(*slot(at, 1, i), g);
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    const float c = CENTER ? f[e] - mu : f[e], ge = g[e] * wk[i][e];
+                    s[0] = fmaf(c, c, s[0]);
+                    s[1] = fmaf(ge, c, s[1]);
+                    if (CENTER) s[NS - 1] += ge;
+                }
+            }
+        group_sum<BLOCK, NS>(s, lg, red[CENTER ? 1 : odd]);
+        const float r = rsqrtf(fmaf(s[0], inv_d, eps));
+        // mean(g h); 0 with r, whatever sum g x came to in a row too large for its squares
+        const float c2 = r == 0.0f ? 0.0f : s[1] * inv_d * r;
+        const float c1 = CENTER ? s[NS - 1] * inv_d : 0.0f;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (in && l + i * lanes < nv) {
+                RowVec<DT>::get(*slot(at, 0, i), f);
+                RowVec<DT>::get(*slot(at, 1, i), g);
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    const float h = (CENTER ? f[e] - mu : f[e]) * r;
+                    aw[i][e] = fmaf(g[e], h, aw[i][e]);
+                    if (DB) ab[DB ? i : 0][e] += g[e];
+                    f[e] = (fmaf(g[e], wk[i][e], -c1) - h * c2) * r;
+                }
+                st_stream(dx0 + t * nv + l + i * lanes, RowVec<DT>::set(f));
+            }
+        at = at + 1 == kStages ? 0 : at + 1, odd ^= 1;
+    }
+    const int64_t d = (int64_t)nv * E;
+    part_w += blockIdx.x * d, part_b += blockIdx.x * d;
+    if (BLOCK) {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (l + i * lanes < nv) {
+                put_sums<E>(part_w, l + i * lanes, aw[i]);
+                if (DB) put_sums<E>(part_b, l + i * lanes, ab[DB ? i : 0]);
+            }
+        return;
+    }
+    // the sums of a warp's groups, then of the block's warps, in the ring's memory
+    copies_wait<0>();
+    __syncthreads();
+    float *buf = reinterpret_cast<float *>(ring);
+    const int warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+#pragma unroll
+        for (int k = 0; k < 5; ++k)
+            if (k >= lg)
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    aw[i][e] += __shfl_xor_sync(0xFFFFFFFFu, aw[i][e], 1 << k);
+                    if (DB)
+                        ab[DB ? i : 0][e] += __shfl_xor_sync(0xFFFFFFFFu, ab[DB ? i : 0][e], 1 << k);
+                }
+        if ((int)(threadIdx.x & 31) < lanes && l + i * lanes < nv) {
+            put_sums<E>(buf + warp * d, l + i * lanes, aw[i]);
+            if (DB) put_sums<E>(buf + (8 + warp) * d, l + i * lanes, ab[DB ? i : 0]);
+        }
+    }
+    __syncthreads();
+    for (int c = threadIdx.x; c < (int)d; c += 256) {
+        float a = 0.0f, b = 0.0f;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            a += buf[q * d + c];
+            if (DB) b += buf[(8 + q) * d + c];
+        }
+        part_w[c] = a;
+        if (DB) part_b[c] = b;
+    }
+}
 
 // Any width, first part: a row's mean, r, mean(g) and mean(g h).
 template <int DT, bool CENTER>
@@ -29,7 +190,8 @@ __global__ void __launch_bounds__(256)
                  const uint4 *__restrict__ x0, const float *__restrict__ w,
                  float4 *__restrict__ stats) {
     constexpr int E = RowVec<DT>::E;
-    __shared__ float red[3][2][32];
+    __shared__ __align__(16) float red[3][2][32];
+    clear_red(&red[0][0][0], 192);
     griddep_wait_then_release();
     const float inv_d = 1.0f / (float)(nv * E);
     for (int64_t t = blockIdx.x; t < rows; t += gridDim.x) {
@@ -114,40 +276,102 @@ __global__ void __launch_bounds__(128)
     }
 }
 
-// out[c] = sum over the partial rows of part[p][c]: 8 warps of a block take every
-// eighth row of 128 channels, and their sums meet in shared memory.
+// out[c] = sum over the partial rows of part[p][c]: a block has 32 channels, and each
+// of its 32 groups of 8 lanes every 32nd row.
 __global__ void __launch_bounds__(256)
     k_norm_sum(int parts, int64_t d4, const float4 *__restrict__ part_w, float4 *__restrict__ dw,
                const float4 *__restrict__ part_b, float4 *__restrict__ db) {
-    __shared__ float4 red[8][32];
+    __shared__ float4 red[8][8];
     griddep_wait_then_release();
     const float4 *part = blockIdx.y == 0 ? part_w : part_b;
     float4 *out = blockIdx.y == 0 ? dw : db;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t c = (int64_t)blockIdx.x * 32 + lane;
+    if (out == nullptr) return;
+    const int l = threadIdx.x & 7, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t c = (int64_t)blockIdx.x * 8 + l;
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (out != nullptr && c < d4) {
-#pragma unroll 4
-        for (int p = warp; p < parts; p += 8) {
+    if (c < d4) {
+#pragma unroll 8
+        for (int p = threadIdx.x >> 3; p < parts; p += 32) {
             const float4 v = part[(int64_t)p * d4 + c];
             a.x += v.x, a.y += v.y, a.z += v.z, a.w += v.w;
         }
     }
-    red[warp][lane] = a;
+#pragma unroll
+    for (int off = 8; off < 32; off <<= 1) {
+        a.x += __shfl_xor_sync(0xFFFFFFFFu, a.x, off);
+        a.y += __shfl_xor_sync(0xFFFFFFFFu, a.y, off);
+        a.z += __shfl_xor_sync(0xFFFFFFFFu, a.z, off);
+        a.w += __shfl_xor_sync(0xFFFFFFFFu, a.w, off);
+    }
+    if (lane < 8) red[warp][l] = a;
     __syncthreads();
-    if (warp == 0 && out != nullptr && c < d4) {
+    if (threadIdx.x < 8 && c < d4) {
 #pragma unroll
         for (int i = 1; i < 8; ++i) {
-            const float4 v = red[i][lane];
+            const float4 v = red[i][l];
             a.x += v.x, a.y += v.y, a.z += v.z, a.w += v.w;
         }
         out[c] = a;
     }
 }
 
+cudaError_t launch_sums(const RowNormBackward &p, int parts, const float *part_w,
+                        const float *part_b, cudaStream_t s) {
+    if (p.dweight == nullptr && p.dbias == nullptr) return cudaSuccess;
+    const int64_t d4 = p.d / 4;
+    return launch_overlapped(&k_norm_sum, dim3((unsigned)((d4 + 7) / 8), p.dbias ? 2u : 1u),
+                             dim3(256), 0, s, parts, d4, reinterpret_cast<const float4 *>(part_w),
+                             reinterpret_cast<float4 *>(p.dweight),
+                             reinterpret_cast<const float4 *>(part_b),
+                             reinterpret_cast<float4 *>(p.dbias));
+}
+
+template <int DT, bool CENTER, bool DB, int V, bool BLOCK>
+cudaError_t launch_ring(const RowNormBackward &p, const RowPlan &plan, int64_t nv,
+                        const DeviceInfo &di, cudaStream_t s) {
+    static SmemState smem;
+    static std::atomic<int> regs;
+    auto *kernel = &k_norm_backward<DT, CENTER, DB, V, BLOCK>;
+    constexpr int most = kStages * 2 * V * (BLOCK ? kRingThreads : 256) * 16;
+    cudaError_t e = allow_smem(smem, reinterpret_cast<const void *>(kernel), most, di);
+    if (e != cudaSuccess) return e;
+    const int64_t want = (p.rows + plan.groups - 1) / plan.groups,
+                  cap = (int64_t)di.sms * blocks_per_sm(kernel, regs, plan),
+                  most_parts = max_parts(p.rows, p.d);
+    const int parts = (int)std::min(want, std::min(cap, most_parts));
+    float *part_w = reinterpret_cast<float *>(p.ws), *part_b = part_w + (size_t)parts * p.d;
+    e = launch_overlapped(kernel, dim3((unsigned)parts), dim3(plan.threads), plan.ring, s, p.rows,
+                          (int)nv, plan.lg, p.eps, static_cast<const uint4 *>(p.dy),
+                          static_cast<const uint4 *>(p.x), p.weight, static_cast<uint4 *>(p.dx),
+                          part_w, part_b);
+    return e != cudaSuccess ? e : launch_sums(p, parts, part_w, part_b, s);
+}
+
+template <int DT, bool CENTER, bool DB, int V>
+cudaError_t launch_ring(const RowNormBackward &p, int64_t nv, const DeviceInfo &di,
+                        cudaStream_t s) {
+    const RowPlan plan = row_plan(nv, V, 2, kStages);
+    return plan.lg == kBlockRow ? launch_ring<DT, CENTER, DB, V, true>(p, plan, nv, di, s)
+                                : launch_ring<DT, CENTER, DB, V, false>(p, plan, nv, di, s);
+}
+
+template <int DT, bool CENTER, bool DB>
+cudaError_t launch_ring(const RowNormBackward &p, int64_t nv, const DeviceInfo &di,
+                        cudaStream_t s) {
+    switch (row_vecs(nv, kRingThreads, 4)) {
+        case 1: return launch_ring<DT, CENTER, DB, 1>(p, nv, di, s);
+        case 2: return launch_ring<DT, CENTER, DB, 2>(p, nv, di, s);
+        case 3: return launch_ring<DT, CENTER, DB, 3>(p, nv, di, s);
+        default: return launch_ring<DT, CENTER, DB, 4>(p, nv, di, s);
+    }
+}
+
 template <int DT, bool CENTER>
 cudaError_t launch(const RowNormBackward &p, const DeviceInfo &di, cudaStream_t s) {
     const int64_t nv = p.d / RowVec<DT>::E, cap = (int64_t)di.sms * 64;
+    if (nv <= 4 * kRingThreads)
+        return CENTER || p.dbias ? launch_ring<DT, CENTER, true>(p, nv, di, s)
+                                 : launch_ring<DT, CENTER, CENTER>(p, nv, di, s);
     const uint4 *dy = static_cast<const uint4 *>(p.dy), *x = static_cast<const uint4 *>(p.x);
     float4 *stats = reinterpret_cast<float4 *>(p.ws);
     const int64_t most = max_parts(p.rows, p.d), run = (p.rows + most - 1) / most;
@@ -162,12 +386,8 @@ cudaError_t launch(const RowNormBackward &p, const DeviceInfo &di, cudaStream_t 
                           dim3(128), 0, s, p.rows, nv, run, dy, x, p.weight,
                           (const float4 *)stats, static_cast<uint4 *>(p.dx),
                           p.dweight ? part_w : nullptr, p.dbias ? part_b : nullptr);
-    if (e != cudaSuccess || (p.dweight == nullptr && p.dbias == nullptr)) return e;
-    const int64_t d4 = p.d / 4;
-    return launch_overlapped(&k_norm_sum, dim3((unsigned)((d4 + 31) / 32), p.dbias ? 2u : 1u),
-                             dim3(256), 0, s, parts, d4, (const float4 *)part_w,
-                             reinterpret_cast<float4 *>(p.dweight), (const float4 *)part_b,
-                             reinterpret_cast<float4 *>(p.dbias));
+    if (e != cudaSuccess) return e;
+    return launch_sums(p, parts, part_w, part_b, s);
 }
 
 template <int DT>

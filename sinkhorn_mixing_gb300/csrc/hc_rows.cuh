@@ -65,8 +65,9 @@ __device__ __forceinline__ void row_params(const float *p, int64_t v, float none
 }
 
 // Sums a[0..NS) over the block (whole warps, at most 32) in a fixed order; every
-// thread gets them.  `red` holds NS x 32 floats and may be used again after the
-// next barrier of the caller's.
+// thread gets them.  `red` holds NS x 32 floats, zeros behind the block's warps
+// (clear_red); it is free again after the block's next barrier, so calls that
+// take two of them in turn need no other barrier.
 template <int NS>
 __device__ __forceinline__ void block_sum(float a[NS], float (*red)[32]) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
@@ -79,11 +80,117 @@ __device__ __forceinline__ void block_sum(float a[NS], float (*red)[32]) {
         for (int i = 0; i < NS; ++i) red[i][warp] = a[i];
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < NS; ++i) a[i] = lane < warps ? red[i][lane] : 0.0f;
+    for (int i = 0; i < NS; ++i) a[i] = 0.0f;
+    for (int w = 0; w < warps; w += 4)
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1)
+        for (int i = 0; i < NS; ++i) {
+            const float4 v = *reinterpret_cast<const float4 *>(&red[i][w]);
+            a[i] += (v.x + v.y) + (v.z + v.w);
+        }
+}
+
+__device__ __forceinline__ void clear_red(float *red, int floats) {
+    for (int i = threadIdx.x; i < floats; i += blockDim.x) red[i] = 0.0f;
+    __syncthreads();
+}
+
+// A row is shared by a group of threads, and a block has several groups: 2^LG lanes
+// of a warp where `lg` < 5, a warp (5), or the whole block (kBlockRow).
+constexpr int kBlockRow = 6;
+
+// Sums a[0..NS) over the group; `red` as in block_sum.
+template <bool BLOCK, int NS>
+__device__ __forceinline__ void group_sum(float a[NS], int lg, float (*red)[32]) {
+    if (BLOCK) {
+        block_sum<NS>(a, red);
+    } else {
 #pragma unroll
-        for (int i = 0; i < NS; ++i) a[i] += __shfl_xor_sync(0xFFFFFFFFu, a[i], off);
+        for (int k = 0; k < 5; ++k)
+            if (k < lg)
+#pragma unroll
+                for (int i = 0; i < NS; ++i)
+                    a[i] += __shfl_xor_sync(0xFFFFFFFFu, a[i], 1 << k);
+    }
+}
+
+// Copies of 16 bytes from global to shared memory, in flight while the thread goes
+// on.  A thread waits for and reads what it copied itself, so no barrier is
+// needed between the two.
+__device__ __forceinline__ void copy16_async(uint4 *dst, const uint4 *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                     (uint32_t)__cvta_generic_to_shared(dst)),
+                 "l"(src)
+                 : "memory");
+}
+__device__ __forceinline__ void copies_commit() {
+    asm volatile("cp.async.commit_group;" ::: "memory");
+}
+// All but the newest `LEFT` groups of this thread's copies have landed.
+template <int LEFT>
+__device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
+}
+
+// How a kernel with a ring of copied rows is laid over the GPU.
+struct RowPlan {
+    int lg;        // a row's group (see kBlockRow)
+    int threads;   // of a block
+    int groups;    // rows a block has at a time
+    size_t ring;   // bytes of shared memory
+};
+
+// A row of nv vectors for a kernel whose threads have `vecs` of them at most;
+// `arrays` rows are copied for each step and `stages` steps are under way.
+inline RowPlan row_plan(int64_t nv, int vecs, int arrays, int stages) {
+    RowPlan p;
+    const int64_t need = (nv + vecs - 1) / vecs;
+    if (need <= 32) {
+        p.lg = 0;
+        while (((int64_t)1 << p.lg) < need) ++p.lg;
+        p.threads = 256;
+        p.groups = 256 >> p.lg;
+    } else {
+        p.lg = kBlockRow;
+        p.threads = (int)((need + 31) & ~(int64_t)31);
+        p.groups = 1;
+    }
+    p.ring = (size_t)stages * arrays * vecs * p.threads * 16;
+    return p;
+}
+
+// Vectors a thread has of a row of nv (max_vecs at most, 4 or 5): those that leave the fewest
+// places of a group empty (up to a sixteenth more is taken for more vectors a
+// thread, and a group of fewer than four lanes, whose accesses are less than 64
+// bytes wide, counts as a tenth empty).  100,000 x 520 in bf16, 65 vectors a row:
+// the norm 35.7 us with five a thread, 47.4 with four, two or one.
+inline int row_vecs(int64_t nv, int max_threads, int max_vecs) {
+    int best = 4;
+    float most = 0.0f;
+    for (int v : {4, 5, 3, 2, 1}) {
+        const RowPlan p = row_plan(nv, v, 1, 1);
+        if (p.threads > max_threads || v > max_vecs) continue;
+        const int lanes = p.lg == kBlockRow ? p.threads : 1 << p.lg;
+        const float fill = (float)nv / (float)(v * lanes) - (lanes < 4 ? 0.1f : 0.0f);
+        if (fill > most + 0.0625f) best = v, most = fill;
+    }
+    return best;
+}
+
+// Blocks of `kernel` that an SM holds, from its registers, threads and shared memory.
+template <typename K>
+int blocks_per_sm(K *kernel, std::atomic<int> &regs, const RowPlan &p) {
+    int r = regs.load(std::memory_order_relaxed);
+    if (r == 0) {
+        cudaFuncAttributes a;
+        if (cudaFuncGetAttributes(&a, kernel) != cudaSuccess) return 1;
+        r = (a.numRegs + 7) & ~7;
+        regs.store(r, std::memory_order_relaxed);
+    }
+    const int by_regs = 65536 / (r * p.threads), by_threads = 2048 / p.threads;
+    const int by_smem = (int)((size_t)(227 * 1024) / (p.ring + 2048));
+    int k = by_regs < by_threads ? by_regs : by_threads;
+    k = by_smem < k ? by_smem : k;
+    return k < 1 ? 1 : k;
 }
 
 }  // namespace hc
