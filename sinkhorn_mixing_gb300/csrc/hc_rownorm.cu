@@ -23,11 +23,11 @@ template <int DT, bool CENTER, int V, bool BLOCK>
 __global__ void __launch_bounds__(BLOCK ? kRingThreads : 256, BLOCK ? 1 : V < 3 ? 3 : 2)
     k_norm(int64_t rows, int nv, int lg, float eps, const uint4 *x0, const float *__restrict__ w,
            const float *__restrict__ b, uint4 *y0) {
-    constexpr int E = RowVec<DT>::E;
+    constexpr int E = RowVec<DT>::E, NS = CENTER ? 2 : 1, SLOTS = V + (CENTER ? 1 : 0);
     constexpr bool KEEP_B = CENTER && V * E <= 32;
     extern __shared__ uint4 ring[];
-    __shared__ __align__(16) float red[2][1][32];
-    if (BLOCK) clear_red(&red[0][0][0], 64);
+    __shared__ __align__(16) float red[2][NS][32];
+    if (BLOCK) clear_red(&red[0][0][0], 2 * NS * 32);
     griddep_wait_then_release();
     const int lanes = BLOCK ? blockDim.x : 1 << lg;
     const int l = BLOCK ? threadIdx.x : threadIdx.x & (lanes - 1);
@@ -35,12 +35,15 @@ __global__ void __launch_bounds__(BLOCK ? kRingThreads : 256, BLOCK ? 1 : V < 3 
     const int64_t step = (int64_t)gridDim.x * groups;
     int64_t t = (int64_t)blockIdx.x * groups + (BLOCK ? 0 : threadIdx.x >> lg);
     const float inv_d = 1.0f / (float)(nv * E);
-    auto slot = [&](int stage, int i) { return ring + (stage * V + i) * blockDim.x + threadIdx.x; };
+    auto slot = [&](int stage, int i) {
+        return ring + (stage * SLOTS + i) * blockDim.x + threadIdx.x;
+    };
     auto copy = [&](int64_t row, int stage) {
         if (row < rows) {
 #pragma unroll
             for (int i = 0; i < V; ++i)
                 if (l + i * lanes < nv) copy16_async(slot(stage, i), x0 + row * nv + l + i * lanes);
+            if (CENTER) copy16_async(slot(stage, V), x0 + row * nv);  // for row_guess
         }
         copies_commit();
     };
@@ -58,34 +61,45 @@ __global__ void __launch_bounds__(BLOCK ? kRingThreads : 256, BLOCK ? 1 : V < 3 
     for (int64_t first = t - (BLOCK ? 0 : (threadIdx.x & 31) >> lg); first < rows;
          first += step, t += step) {
         copies_wait<kStages - 2>();
-        float f[V][E], s[1] = {0.0f};
+        float mu = 0.0f, delta = 0.0f, var, f[V][E], s[NS];
+        auto read = [&]() {
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (t < rows && l + i * lanes < nv) v = *slot(at, i);
-            RowVec<DT>::get(v, f[i]);
-        }
+            for (int i = 0; i < V; ++i) {
+                uint4 v = make_uint4(0, 0, 0, 0);
+                const bool have = t < rows && l + i * lanes < nv;
+                if (have) v = *slot(at, i);
+                RowVec<DT>::get(v, f[i]);
+                if (CENTER)
+#pragma unroll
+                    for (int e = 0; e < E; ++e) f[i][e] = have ? f[i][e] - mu : 0.0f;
+            }
+        };
+        if (CENTER && t < rows) mu = row_guess<DT>(*slot(at, V));
+        read();
         copy(t + (kStages - 1) * step, at == 0 ? kStages - 1 : at - 1);
-        if (CENTER) {
+        for (int round = 0;; ++round) {
+            s[0] = s[NS - 1] = 0.0f;
 #pragma unroll
             for (int i = 0; i < V; ++i)
 #pragma unroll
-                for (int e = 0; e < E; ++e) s[0] += f[i][e];
-            group_sum<BLOCK, 1>(s, lg, red[0]);
-            const float mu = s[0] * inv_d;
-            s[0] = 0.0f;
-#pragma unroll
-            for (int i = 0; i < V; ++i)
-#pragma unroll
-                for (int e = 0; e < E; ++e)
-                    f[i][e] = l + i * lanes < nv ? f[i][e] - mu : 0.0f;
+                for (int e = 0; e < E; ++e) {
+                    s[0] = fmaf(f[i][e], f[i][e], s[0]);
+                    if (CENTER) s[NS - 1] += f[i][e];
+                }
+            group_sum<BLOCK, NS>(s, lg, red[odd]);
+            odd ^= 1;
+            var = s[0] * inv_d;
+            if (!CENTER) break;
+            delta = s[NS - 1] * inv_d;
+            var = fmaf(-delta, delta, var);
+            var = var < 0.0f ? 0.0f : var;  // a row of one number; NaN stays
+            // the same for all of a block; all of a warp go along, in vain but for those in need
+            const bool again = round == 0 && !(delta * delta <= var);
+            if (BLOCK ? !again : !__any_sync(0xFFFFFFFFu, again)) break;
+            if (again) mu += delta;
+            read();
         }
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-#pragma unroll
-            for (int e = 0; e < E; ++e) s[0] = fmaf(f[i][e], f[i][e], s[0]);
-        group_sum<BLOCK, 1>(s, lg, red[CENTER ? 1 : odd]);
-        const float r = rsqrtf(fmaf(s[0], inv_d, eps));
+        const float r = rsqrtf(var + eps), minus_dr = -delta * r;
         if (t < rows) {
 #pragma unroll
             for (int i = 0; i < V; ++i) {
@@ -94,12 +108,13 @@ __global__ void __launch_bounds__(BLOCK ? kRingThreads : 256, BLOCK ? 1 : V < 3 
                     if (!KEEP_B) row_params<E>(b, l + i * lanes, 0.0f, bv);
 #pragma unroll
                     for (int e = 0; e < E; ++e)
-                        f[i][e] = fmaf(f[i][e] * r, wk[i][e], KEEP_B ? bk[i][e] : bv[e]);
+                        f[i][e] = fmaf(CENTER ? fmaf(f[i][e], r, minus_dr) : f[i][e] * r, wk[i][e],
+                                       KEEP_B ? bk[i][e] : bv[e]);
                     st_stream(y0 + t * nv + l + i * lanes, RowVec<DT>::set(f[i]));
                 }
             }
         }
-        at = at + 1 == kStages ? 0 : at + 1, odd ^= 1;
+        at = at + 1 == kStages ? 0 : at + 1;
     }
 }
 
@@ -156,7 +171,7 @@ cudaError_t launch_ring(const RowNorm &p, const RowPlan &plan, int64_t nv, const
     static SmemState smem;
     static std::atomic<int> regs;
     auto *kernel = &k_norm<DT, CENTER, V, BLOCK>;
-    constexpr int most = kStages * V * (BLOCK ? kRingThreads : 256) * 16;
+    constexpr int most = kStages * (V + (CENTER ? 1 : 0)) * (BLOCK ? kRingThreads : 256) * 16;
     const cudaError_t e = allow_smem(smem, reinterpret_cast<const void *>(kernel), most, di);
     if (e != cudaSuccess) return e;
     const int64_t want = (p.rows + plan.groups - 1) / plan.groups,
@@ -169,7 +184,7 @@ cudaError_t launch_ring(const RowNorm &p, const RowPlan &plan, int64_t nv, const
 
 template <int DT, bool CENTER, int V>
 cudaError_t launch_ring(const RowNorm &p, int64_t nv, const DeviceInfo &di, cudaStream_t s) {
-    const RowPlan plan = row_plan(nv, V, 1, kStages);
+    const RowPlan plan = row_plan(nv, V, V + (CENTER ? 1 : 0), kStages);
     return plan.lg == kBlockRow ? launch_ring<DT, CENTER, V, true>(p, plan, nv, di, s)
                                 : launch_ring<DT, CENTER, V, false>(p, plan, nv, di, s);
 }

@@ -40,15 +40,15 @@ __device__ __forceinline__ void put_sums(float *row, int64_t v, const float a[E]
 // rows ahead.  A thread's channels are the same in every row, so their weights and
 // the sums over the block's rows stay in its registers.  DB: dbias as well.
 //
-// A row takes one round of sums (sum x^2, sum g x) or, for layer norm, two (sum x;
-// then those of (x - mu)^2, g and g (x - mu)); x and dy are read from shared memory
-// again after each, not held.
+// A row takes one round of sums: x^2 and g x or, for layer norm, x - p, (x - p)^2, g
+// and g (x - p) (see row_guess).  x and dy are read from shared memory again behind
+// it, not held.
 template <int DT, bool CENTER, bool DB, int V, bool BLOCK>
 __global__ void __launch_bounds__(BLOCK ? kRingThreads : 256, BLOCK ? 1 : V < 3 ? 2 : 1)
     k_norm_backward(int64_t rows, int nv, int lg, float eps, const uint4 *dy0,
                     const uint4 *__restrict__ x0, const float *__restrict__ w, uint4 *dx0,
                     float *__restrict__ part_w, float *__restrict__ part_b) {
-    constexpr int E = RowVec<DT>::E, NS = CENTER ? 3 : 2;
+    constexpr int E = RowVec<DT>::E, NS = CENTER ? 4 : 2, SLOTS = 2 * V + (CENTER ? 1 : 0);
     extern __shared__ uint4 ring[];
     __shared__ __align__(16) float red[2][NS][32];
     if (BLOCK) clear_red(&red[0][0][0], 2 * NS * 32);
@@ -60,7 +60,7 @@ __global__ void __launch_bounds__(BLOCK ? kRingThreads : 256, BLOCK ? 1 : V < 3 
     int64_t t = (int64_t)blockIdx.x * groups + (BLOCK ? 0 : threadIdx.x >> lg);
     const float inv_d = 1.0f / (float)(nv * E);
     auto slot = [&](int stage, int array, int i) {
-        return ring + ((stage * 2 + array) * V + i) * blockDim.x + threadIdx.x;
+        return ring + (stage * SLOTS + array * V + i) * blockDim.x + threadIdx.x;
     };
     auto copy = [&](int64_t row, int stage) {
         if (row < rows) {
@@ -70,17 +70,22 @@ __global__ void __launch_bounds__(BLOCK ? kRingThreads : 256, BLOCK ? 1 : V < 3 
                     copy16_async(slot(stage, 0, i), x0 + row * nv + l + i * lanes);
                     copy16_async(slot(stage, 1, i), dy0 + row * nv + l + i * lanes);
                 }
+            if (CENTER) copy16_async(slot(stage, 2, 0), x0 + row * nv);  // for row_guess
         }
         copies_commit();
     };
 #pragma unroll
     for (int k = 0; k < kStages - 1; ++k) copy(t + k * step, k);
-    float wk[V][E], aw[V][E], ab[DB ? V : 1][E];
+    uint64_t wk[V][E / 2], aw[V][E / 2], ab[DB ? V : 1][E / 2];  // pairs of channels
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        if (l + i * lanes < nv) row_params<E>(w, l + i * lanes, 1.0f, wk[i]);
+        float f[E];
+        if (l + i * lanes < nv) row_params<E>(w, l + i * lanes, 1.0f, f);
 #pragma unroll
-        for (int e = 0; e < E; ++e) aw[i][e] = ab[DB ? i : 0][e] = 0.0f;
+        for (int e = 0; e < E / 2; ++e) {
+            wk[i][e] = pack2(f[2 * e], f[2 * e + 1]);
+            aw[i][e] = ab[DB ? i : 0][e] = 0;
+        }
     }
     int at = 0, odd = 0;
     // a warp stays together until the last of its rows
@@ -89,63 +94,90 @@ __global__ void __launch_bounds__(BLOCK ? kRingThreads : 256, BLOCK ? 1 : V < 3 
         copies_wait<kStages - 2>();
         copy(t + (kStages - 1) * step, at == 0 ? kStages - 1 : at - 1);
         const bool in = t < rows;
-        float mu = 0.0f, s[NS], f[E], g[E];
-        if (CENTER) {
-            s[0] = 0.0f;
+        float s[NS], mu = 0.0f, delta = 0.0f, var;
+        uint64_t f[E / 2], g[E / 2];
+        if (CENTER && in) mu = row_guess<DT>(*slot(at, 2, 0));
+        uint4 xr[V], gr[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (in && l + i * lanes < nv) xr[i] = *slot(at, 0, i), gr[i] = *slot(at, 1, i);
+        auto sums = [&]() {
+            uint64_t sq = 0, sgc = 0, sg = 0, sc = 0;
+            const uint64_t minus_p = pack2(-mu, -mu);
 #pragma unroll
             for (int i = 0; i < V; ++i)
                 if (in && l + i * lanes < nv) {
-                    RowVec<DT>::get(*slot(at, 0, i), f);
+                    row_pairs<DT>(xr[i], f);
+                    row_pairs<DT>(gr[i], g);
 #pragma unroll
-                    for (int e = 0; e < E; ++e) s[0] += f[e];
+                    for (int e = 0; e < E / 2; ++e) {
+                        const uint64_t c = CENTER ? fadd2(f[e], minus_p) : f[e];
+                        const uint64_t gw = fmul2(g[e], wk[i][e]);
+                        ffma2(sq, c, c);
+                        ffma2(sgc, gw, c);
+                        if (CENTER) sc = fadd2(sc, c), sg = fadd2(sg, gw);
+                    }
                 }
-            group_sum<BLOCK, 1>(s, lg, red[0]);
-            mu = s[0] * inv_d;
+            s[0] = sum2(sq), s[1] = sum2(sgc);
+            if (CENTER) s[NS - 2] = sum2(sc), s[NS - 1] = sum2(sg);
+            group_sum<BLOCK, NS>(s, lg, red[odd]);
+            odd ^= 1;
+            var = s[0] * inv_d;
+            if (CENTER) {
+                delta = s[NS - 2] * inv_d;
+                var = fmaf(-delta, delta, var);
+                var = var < 0.0f ? 0.0f : var;  // a row of one number; NaN stays
+            }
+        };
+        sums();
+        if (CENTER) {
+            // the same for all of a block; all of a warp go along, in vain but for those in need
+            const bool again = !(delta * delta <= var);
+            if (BLOCK ? again : __any_sync(0xFFFFFFFFu, again)) {
+                if (again) mu += delta;
+                sums();
+            }
         }
-#pragma unroll
-        for (int i = 0; i < NS; ++i) s[i] = 0.0f;
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-            if (in && l + i * lanes < nv) {
-                RowVec<DT>::get(*slot(at, 0, i), f);
-                RowVec<DT>::get(*slot(at, 1, i), g);
-#pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    const float c = CENTER ? f[e] - mu : f[e], ge = g[e] * wk[i][e];
-                    s[0] = fmaf(c, c, s[0]);
-                    s[1] = fmaf(ge, c, s[1]);
-                    if (CENTER) s[NS - 1] += ge;
-                }
-            }
-        group_sum<BLOCK, NS>(s, lg, red[CENTER ? 1 : odd]);
-        const float r = rsqrtf(fmaf(s[0], inv_d, eps));
+        const float r = rsqrtf(var + eps);
         // mean(g h); 0 with r, whatever sum g x came to in a row too large for its squares
-        const float c2 = r == 0.0f ? 0.0f : s[1] * inv_d * r;
         const float c1 = CENTER ? s[NS - 1] * inv_d : 0.0f;
+        const float gc = CENTER ? fmaf(-delta, c1, s[1] * inv_d) : s[1] * inv_d;
+        const float c2 = r == 0.0f ? 0.0f : gc * r;
+        const float mr = -(mu + delta) * r, rc1 = -c1 * r, rc2 = -c2 * r;
+        const uint64_t rr = pack2(r, r), minus_mr = pack2(mr, mr), minus_rc1 = pack2(rc1, rc1),
+                       minus_rc2 = pack2(rc2, rc2);
 #pragma unroll
         for (int i = 0; i < V; ++i)
             if (in && l + i * lanes < nv) {
-                RowVec<DT>::get(*slot(at, 0, i), f);
-                RowVec<DT>::get(*slot(at, 1, i), g);
+                row_pairs<DT>(xr[i], f);
+                row_pairs<DT>(gr[i], g);
 #pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    const float h = (CENTER ? f[e] - mu : f[e]) * r;
-                    aw[i][e] = fmaf(g[e], h, aw[i][e]);
-                    if (DB) ab[DB ? i : 0][e] += g[e];
-                    f[e] = (fmaf(g[e], wk[i][e], -c1) - h * c2) * r;
+                for (int e = 0; e < E / 2; ++e) {
+                    const uint64_t h = CENTER ? ffma2_of(f[e], rr, minus_mr) : fmul2(f[e], rr);
+                    ffma2(aw[i][e], g[e], h);
+                    if (DB) ab[DB ? i : 0][e] = fadd2(ab[DB ? i : 0][e], g[e]);
+                    const uint64_t gw = fmul2(g[e], wk[i][e]);
+                    f[e] = ffma2_of(h, minus_rc2,
+                                    CENTER ? ffma2_of(gw, rr, minus_rc1) : fmul2(gw, rr));
                 }
-                st_stream(dx0 + t * nv + l + i * lanes, RowVec<DT>::set(f));
+                st_stream(dx0 + t * nv + l + i * lanes, row_from_pairs<DT>(f));
             }
-        at = at + 1 == kStages ? 0 : at + 1, odd ^= 1;
+        at = at + 1 == kStages ? 0 : at + 1;
     }
     const int64_t d = (int64_t)nv * E;
     part_w += blockIdx.x * d, part_b += blockIdx.x * d;
+    float sw[E], sb[E];
     if (BLOCK) {
 #pragma unroll
         for (int i = 0; i < V; ++i)
             if (l + i * lanes < nv) {
-                put_sums<E>(part_w, l + i * lanes, aw[i]);
-                if (DB) put_sums<E>(part_b, l + i * lanes, ab[DB ? i : 0]);
+#pragma unroll
+                for (int e = 0; e < E / 2; ++e) {
+                    unpack2(aw[i][e], sw[2 * e], sw[2 * e + 1]);
+                    if (DB) unpack2(ab[DB ? i : 0][e], sb[2 * e], sb[2 * e + 1]);
+                }
+                put_sums<E>(part_w, l + i * lanes, sw);
+                if (DB) put_sums<E>(part_b, l + i * lanes, sb);
             }
         return;
     }
@@ -157,17 +189,21 @@ __global__ void __launch_bounds__(BLOCK ? kRingThreads : 256, BLOCK ? 1 : V < 3 
 #pragma unroll
     for (int i = 0; i < V; ++i) {
 #pragma unroll
+        for (int e = 0; e < E / 2; ++e) {
+            unpack2(aw[i][e], sw[2 * e], sw[2 * e + 1]);
+            if (DB) unpack2(ab[DB ? i : 0][e], sb[2 * e], sb[2 * e + 1]);
+        }
+#pragma unroll
         for (int k = 0; k < 5; ++k)
             if (k >= lg)
 #pragma unroll
                 for (int e = 0; e < E; ++e) {
-                    aw[i][e] += __shfl_xor_sync(0xFFFFFFFFu, aw[i][e], 1 << k);
-                    if (DB)
-                        ab[DB ? i : 0][e] += __shfl_xor_sync(0xFFFFFFFFu, ab[DB ? i : 0][e], 1 << k);
+                    sw[e] += __shfl_xor_sync(0xFFFFFFFFu, sw[e], 1 << k);
+                    if (DB) sb[e] += __shfl_xor_sync(0xFFFFFFFFu, sb[e], 1 << k);
                 }
         if ((int)(threadIdx.x & 31) < lanes && l + i * lanes < nv) {
-            put_sums<E>(buf + warp * d, l + i * lanes, aw[i]);
-            if (DB) put_sums<E>(buf + (8 + warp) * d, l + i * lanes, ab[DB ? i : 0]);
+            put_sums<E>(buf + warp * d, l + i * lanes, sw);
+            if (DB) put_sums<E>(buf + (8 + warp) * d, l + i * lanes, sb);
         }
     }
     __syncthreads();
@@ -332,7 +368,7 @@ cudaError_t launch_ring(const RowNormBackward &p, const RowPlan &plan, int64_t n
     static SmemState smem;
     static std::atomic<int> regs;
     auto *kernel = &k_norm_backward<DT, CENTER, DB, V, BLOCK>;
-    constexpr int most = kStages * 2 * V * (BLOCK ? kRingThreads : 256) * 16;
+    constexpr int most = kStages * (2 * V + (CENTER ? 1 : 0)) * (BLOCK ? kRingThreads : 256) * 16;
     cudaError_t e = allow_smem(smem, reinterpret_cast<const void *>(kernel), most, di);
     if (e != cudaSuccess) return e;
     const int64_t want = (p.rows + plan.groups - 1) / plan.groups,
@@ -350,7 +386,7 @@ cudaError_t launch_ring(const RowNormBackward &p, const RowPlan &plan, int64_t n
 template <int DT, bool CENTER, bool DB, int V>
 cudaError_t launch_ring(const RowNormBackward &p, int64_t nv, const DeviceInfo &di,
                         cudaStream_t s) {
-    const RowPlan plan = row_plan(nv, V, 2, kStages);
+    const RowPlan plan = row_plan(nv, V, 2 * V + (CENTER ? 1 : 0), kStages);
     return plan.lg == kBlockRow ? launch_ring<DT, CENTER, DB, V, true>(p, plan, nv, di, s)
                                 : launch_ring<DT, CENTER, DB, V, false>(p, plan, nv, di, s);
 }
@@ -358,7 +394,7 @@ cudaError_t launch_ring(const RowNormBackward &p, int64_t nv, const DeviceInfo &
 template <int DT, bool CENTER, bool DB>
 cudaError_t launch_ring(const RowNormBackward &p, int64_t nv, const DeviceInfo &di,
                         cudaStream_t s) {
-    switch (row_vecs(nv, kRingThreads, 4)) {
+    switch (row_vecs(nv, kRingThreads, nv <= 128 || nv > 3 * kRingThreads ? 4 : 3)) {
         case 1: return launch_ring<DT, CENTER, DB, 1>(p, nv, di, s);
         case 2: return launch_ring<DT, CENTER, DB, 2>(p, nv, di, s);
         case 3: return launch_ring<DT, CENTER, DB, 3>(p, nv, di, s);

@@ -53,6 +53,39 @@ struct RowVec<HC_F32> {
     }
 };
 
+// The same in pairs, for the two-wide FMAs (fma.rn.f32x2 and its like): half the
+// instructions of the sums and products, which is what bounds a row's gradients.
+template <int DT>
+__device__ __forceinline__ void row_pairs(const uint4 &v, uint64_t p[RowVec<DT>::E / 2]) {
+    if (DT == HC_BF16) {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < RowVec<DT>::E / 2; ++i) p[i] = bf16x2_to_f32x2(w[i]);
+    } else {
+        float f[RowVec<DT>::E];
+        RowVec<DT>::get(v, f);
+#pragma unroll
+        for (int i = 0; i < RowVec<DT>::E / 2; ++i) p[i] = pack2(f[2 * i], f[2 * i + 1]);
+    }
+}
+template <int DT>
+__device__ __forceinline__ uint4 row_from_pairs(const uint64_t p[RowVec<DT>::E / 2]) {
+    float f[RowVec<DT>::E];
+#pragma unroll
+    for (int i = 0; i < RowVec<DT>::E / 2; ++i) unpack2(p[i], f[2 * i], f[2 * i + 1]);
+    return RowVec<DT>::set(f);
+}
+__device__ __forceinline__ uint64_t fadd2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t ffma2_of(uint64_t a, uint64_t b, uint64_t c) {  // a b + c
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+
 // E binary32 parameters (weight, bias) of vector v; `none` where there are none.
 template <int E>
 __device__ __forceinline__ void row_params(const float *p, int64_t v, float none, float f[E]) {
@@ -64,6 +97,34 @@ __device__ __forceinline__ void row_params(const float *p, int64_t v, float none
     }
 }
 
+// Sums a[0..NS) over the warp, NS = 1, 2 or 4; the sum that is returned to a lane is
+// number `which`.  Each step halves what a lane carries, so four sums take 6
+// shuffles, not 20.
+template <int NS>
+__device__ __forceinline__ float warp_sums(const float a[NS], int lane, int &which) {
+    static_assert(NS == 1 || NS == 2 || NS == 4, "a power of two");
+    float v = a[0];
+    which = 0;
+    int off = 16;
+    if constexpr (NS == 4) {
+        const bool up = (lane & 16) != 0, up2 = (lane & 8) != 0;
+        const float p = (up ? a[2] : a[0]) + __shfl_xor_sync(0xFFFFFFFFu, up ? a[0] : a[2], 16);
+        const float q = (up ? a[3] : a[1]) + __shfl_xor_sync(0xFFFFFFFFu, up ? a[1] : a[3], 16);
+        v = (up2 ? q : p) + __shfl_xor_sync(0xFFFFFFFFu, up2 ? p : q, 8);
+        which = (up ? 2 : 0) + (up2 ? 1 : 0);
+        off = 4;
+    } else if constexpr (NS == 2) {
+        const bool up = (lane & 16) != 0;
+        v = (up ? a[1] : a[0]) + __shfl_xor_sync(0xFFFFFFFFu, up ? a[0] : a[1], 16);
+        which = up ? 1 : 0;
+        off = 8;
+    }
+#pragma unroll
+    for (int k = 16; k > 0; k >>= 1)
+        if (k <= off) v += __shfl_xor_sync(0xFFFFFFFFu, v, k);
+    return v;
+}
+
 // Sums a[0..NS) over the block (whole warps, at most 32) in a fixed order; every
 // thread gets them.  `red` holds NS x 32 floats, zeros behind the block's warps
 // (clear_red); it is free again after the block's next barrier, so calls that
@@ -71,21 +132,17 @@ __device__ __forceinline__ void row_params(const float *p, int64_t v, float none
 template <int NS>
 __device__ __forceinline__ void block_sum(float a[NS], float (*red)[32]) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1)
-#pragma unroll
-        for (int i = 0; i < NS; ++i) a[i] += __shfl_xor_sync(0xFFFFFFFFu, a[i], off);
-    if (lane == 0)
-#pragma unroll
-        for (int i = 0; i < NS; ++i) red[i][warp] = a[i];
+    int which;
+    const float v = warp_sums<NS>(a, lane, which);
+    if ((lane & (32 / NS - 1)) == 0) red[which][warp] = v;
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < NS; ++i) a[i] = 0.0f;
     for (int w = 0; w < warps; w += 4)
 #pragma unroll
         for (int i = 0; i < NS; ++i) {
-            const float4 v = *reinterpret_cast<const float4 *>(&red[i][w]);
-            a[i] += (v.x + v.y) + (v.z + v.w);
+            const float4 q = *reinterpret_cast<const float4 *>(&red[i][w]);
+            a[i] += (q.x + q.y) + (q.z + q.w);
         }
 }
 
@@ -111,6 +168,20 @@ __device__ __forceinline__ void group_sum(float a[NS], int lg, float (*red)[32])
                 for (int i = 0; i < NS; ++i)
                     a[i] += __shfl_xor_sync(0xFFFFFFFFu, a[i], 1 << k);
     }
+}
+
+// A row's variance comes from one round of sums of (x - p) and (x - p)^2 about a
+// number p near its values, the mean of the row's first 16 bytes: with delta =
+// mean(x - p), the mean is p + delta and the variance mean((x - p)^2) - delta^2,
+// which loses nothing worth naming while delta^2 is at most the variance.  Where it is
+// not (or either is not finite) the round is repeated about p + delta.
+template <int DT>
+__device__ __forceinline__ float row_guess(const uint4 &v) {
+    float f[RowVec<DT>::E], s = 0.0f;
+    RowVec<DT>::get(v, f);
+#pragma unroll
+    for (int e = 0; e < RowVec<DT>::E; ++e) s += f[e];
+    return s * (1.0f / RowVec<DT>::E);
 }
 
 // Copies of 16 bytes from global to shared memory, in flight while the thread goes
@@ -139,9 +210,9 @@ struct RowPlan {
     size_t ring;   // bytes of shared memory
 };
 
-// A row of nv vectors for a kernel whose threads have `vecs` of them at most;
-// `arrays` rows are copied for each step and `stages` steps are under way.
-inline RowPlan row_plan(int64_t nv, int vecs, int arrays, int stages) {
+// A row of nv vectors for a kernel whose threads have `vecs` of them at most and copy
+// `slots` vectors in all a step, with `stages` steps under way.
+inline RowPlan row_plan(int64_t nv, int vecs, int slots, int stages) {
     RowPlan p;
     const int64_t need = (nv + vecs - 1) / vecs;
     if (need <= 32) {
@@ -154,7 +225,7 @@ inline RowPlan row_plan(int64_t nv, int vecs, int arrays, int stages) {
         p.threads = (int)((need + 31) & ~(int64_t)31);
         p.groups = 1;
     }
-    p.ring = (size_t)stages * arrays * vecs * p.threads * 16;
+    p.ring = (size_t)stages * slots * p.threads * 16;
     return p;
 }
 

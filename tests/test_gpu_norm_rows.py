@@ -302,3 +302,19 @@ def test_refusals(hc):
         hc.hc_norm_backward(x[:4], x)
     with pytest.raises(hc.HcError, match="INVALID"):
         hc.hc_norm_backward(x, x, workspace=torch.empty(0, dtype=torch.uint8, device="cuda"))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("d", [8, 40, 128, 1000, 5120, 32776])
+def test_layer_norm_of_rows_that_start_apart(hc, d, dtype):
+    """Rows whose first channels say nothing of their mean, beside ordinary ones: outliers in front,
+    a far mean behind zeros, one number in all channels but the last."""
+    x, dy, w, b = case(41, d, dtype, 11)
+    x[1, 0], x[2, :4] = 3000.0, -2000.0
+    x[5] = 700.0 + x[5]
+    x[5, :8] = 0.0
+    x[9], x[9, -1] = 2.5, 2.0
+    x[13] = -1.0
+    x[20] += 500.0
+    check_norm(hc, x, w, b, True, 1e-5)
+    check_backward(hc, dy, x, w, True, 1e-5)
