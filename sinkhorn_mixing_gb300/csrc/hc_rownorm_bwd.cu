@@ -44,7 +44,7 @@ __device__ __forceinline__ void put_sums(float *row, int64_t v, const float a[E]
 // and g (x - p) (see row_guess).  x and dy are read from shared memory again behind
 // it, not held.
 template <int DT, bool CENTER, bool DB, int V, bool BLOCK>
-__global__ void __launch_bounds__(BLOCK ? kRingThreads : 256, BLOCK ? 1 : V < 3 ? 2 : 1)
+__global__ void __launch_bounds__(BLOCK ? kRingThreads : 256, BLOCK ? 1 : V < 3 || (V == 3 && !DB) ? 2 : 1)
     k_norm_backward(int64_t rows, int nv, int lg, float eps, const uint4 *dy0,
                     const uint4 *__restrict__ x0, const float *__restrict__ w, uint4 *dx0,
                     float *__restrict__ part_w, float *__restrict__ part_b) {
@@ -394,10 +394,15 @@ cudaError_t launch_ring(const RowNormBackward &p, int64_t nv, const DeviceInfo &
 template <int DT, bool CENTER, bool DB>
 cudaError_t launch_ring(const RowNormBackward &p, int64_t nv, const DeviceInfo &di,
                         cudaStream_t s) {
-    switch (row_vecs(nv, kRingThreads, nv <= 128 || nv > 3 * kRingThreads ? 4 : 3)) {
+    // four vectors a thread, or five, where a warp has the row; three in blocks where they do
+    const int most = nv <= 160 ? 5 : nv <= 3 * kRingThreads ? 3 : 4;
+    switch (row_vecs(nv, kRingThreads, most)) {
         case 1: return launch_ring<DT, CENTER, DB, 1>(p, nv, di, s);
         case 2: return launch_ring<DT, CENTER, DB, 2>(p, nv, di, s);
         case 3: return launch_ring<DT, CENTER, DB, 3>(p, nv, di, s);
+        case 5:
+            return launch_ring<DT, CENTER, DB, 5, false>(
+                p, row_plan(nv, 5, 10 + (CENTER ? 1 : 0), kStages), nv, di, s);
         default: return launch_ring<DT, CENTER, DB, 4>(p, nv, di, s);
     }
 }
