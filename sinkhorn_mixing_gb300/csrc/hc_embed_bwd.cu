@@ -1,24 +1,30 @@
 // hc_embed_bwd.cu -- the gradient of an embedding table:
 //   dtable[v, :] (+)= scale * sum over the tokens t with id_t = v, over the copies j, of dx[t, j, :].
 //
-// Tokens are sorted by id, those of one id by position (a radix sort, stable in
-// each pass), so that a sum's order depends on nothing but the ids.  The sorted
-// tokens are cut into windows of C places, and each id's tokens into pieces of C from
-// its first one on; the block of a window sums the pieces that start in it.  An id
-// with C tokens or fewer is one piece, and its sum is written to the table at once.
-// Longer ones leave a row of partial sums per piece, which k_embed_join adds up in
-// order.  So every gradient is read once and a frequent id's sum is spread over the
-// GPU.
+// Tokens are put in order of their ids, those of one id by position, so that a sum's
+// order depends on nothing but the ids.  The ordered tokens are cut into windows of
+// C places, and each id's tokens into pieces of C from its first one on; the block
+// of a window sums the pieces that start in it.  An id with C tokens or fewer is
+// one piece, and its sum is written to the table at once.  Longer ones leave a row of
+// partial sums per piece, which k_embed_join adds up in order.  So every gradient
+// is read once and a frequent id's sum is spread over the GPU.
 #include "hc_rows.cuh"
 
 namespace hc {
 namespace {
 
-constexpr int kTile = 2048;      // tokens a block sorts at a time: 256 threads, 8 each
+constexpr int kSortThreads = 512;
+constexpr int kSortWarps = kSortThreads / 32;
+constexpr int kTile = 2048;  // tokens a block of the radix sort has at a time
+constexpr int kItems = kTile / kSortThreads;
 constexpr int kSortBlocks = 304;
 constexpr int kMaxDigitBits = 9;
-constexpr int kMaxBins = 1 << kMaxDigitBits;
+constexpr int kMaxBins = 1 << kMaxDigitBits;  // as many as threads
 constexpr int kMaxPiece = 32;
+constexpr int kRankTokens = 4096;  // up to which tokens are ranked by comparing them all
+constexpr int kRankRows = 8192;    // table rows whose presence a block of k_rank notes
+constexpr int kRankThreads = 1024;
+constexpr int kRankWarps = kRankThreads / 32;
 
 int bits_of(int64_t v) {  // of the numbers 0 .. v
     int b = 1;
@@ -27,55 +33,133 @@ int bits_of(int64_t v) {  // of the numbers 0 .. v
 }
 
 // Tokens a piece: 32, fewer where there are too few of them to fill the GPU (in
-// pieces times slices of 1,024 channels).
+// pieces times slices of 1,024 channels).  4,096 tokens of 4 x 5120 into 32,768 rows:
+// 101 us with 32 a piece, 106 with 16, 122 with 8 (the pieces' sums are written, read
+// and joined); 1,537 of 8 x 1032 into 50,001: 47, 48 and 55.
 int piece_tokens(int64_t n, int64_t d) {
     const int64_t slices = (d + 1023) / 1024;
     int c = kMaxPiece;
-    while (c > 1 && n * slices < (int64_t)c * 1216) c /= 2;
+    while (c > 1 && n * slices < (int64_t)c * 608) c /= 2;
     return c;
 }
 
 size_t align256(size_t b) { return (b + 255) & ~(size_t)255; }
 
 struct Workspace {
-    uint2 *sorted[2];  // (id, token): the last pass leaves them in [0]
-    uint32_t *hist;    // [blocks, bins]
-    uint32_t *longs;   // count, then first places of the ids with more than C tokens
-    uint32_t *start;   // [vocab + 1], place + 1 of an id's first token, 0 where there is none
-    uint32_t *end;     // [vocab + 1]
-    float *part;       // [windows, 2, d]
+    uint2 *sorted[2];   // (id, token): the last pass leaves them in [0]
+    uint32_t *hist;     // [blocks, bins]
+    uint32_t *count;    // of `longs`
+    uint4 *longs;       // ids with more than C tokens: id, first window, pieces
+    uint32_t *present;  // a bit for each row of the table: some token names it
+    uint32_t *start;    // [vocab], first place of an id that is present
+    uint32_t *end;      // [vocab], the place behind its last
+    float *part;        // [windows, 2, d]
     size_t bytes;
 };
 
+// The parts of a workspace at `base`, and its size.
 Workspace layout(uint8_t *base, int64_t n, int64_t d, int64_t vocab) {
     const int64_t c = piece_tokens(n, d), windows = (n + c - 1) / c;
-    Workspace w;
     size_t at = 0;
     auto take = [&](size_t b) {
-        uint8_t *p = base + at;
+        const size_t here = at;
         at += align256(b);
-        return p;
+        return base == nullptr ? nullptr : base + here;
     };
+    Workspace w;
     w.sorted[0] = reinterpret_cast<uint2 *>(take((size_t)n * 8));
     w.sorted[1] = reinterpret_cast<uint2 *>(take((size_t)n * 8));
     w.hist = reinterpret_cast<uint32_t *>(take((size_t)kSortBlocks * kMaxBins * 4));
-    w.longs = reinterpret_cast<uint32_t *>(take((size_t)(windows + 1) * 4));
-    w.start = reinterpret_cast<uint32_t *>(take((size_t)(vocab + 1) * 4));
-    w.end = reinterpret_cast<uint32_t *>(take((size_t)(vocab + 1) * 4));
+    w.count = reinterpret_cast<uint32_t *>(take(4));
+    w.longs = reinterpret_cast<uint4 *>(take((size_t)windows * 16));
+    w.present = reinterpret_cast<uint32_t *>(take((size_t)((vocab + 31) / 32) * 4));
+    w.start = reinterpret_cast<uint32_t *>(take((size_t)vocab * 4));
+    w.end = reinterpret_cast<uint32_t *>(take((size_t)vocab * 4));
     w.part = reinterpret_cast<float *>(take((size_t)windows * 2 * d * 4));
     w.bytes = at;
     return w;
 }
 
-// Where the sort's first pass reads: the ids themselves; ids outside the table sort
-// behind it, as `vocab`.
+// An id as it is ordered: those outside the table come behind it, as `vocab`.
+template <typename ID>
+__device__ __forceinline__ uint32_t row_of(const ID *ids, int64_t i, int64_t vocab) {
+    const int64_t id = (int64_t)__ldg(ids + i);
+    return (uint32_t)(id >= 0 && id < vocab ? id : vocab);
+}
+
+// Few tokens: a token's place is the number of tokens with a smaller id, and of those
+// before it with its own.  A block has 32 of them, one a lane, and all ids in shared
+// memory; its warps share the comparisons.  n^2 of them take 1.4 us at 4,096 tokens,
+// where the passes of the sort below take 20.  A block also notes which of
+// kRankRows rows of the table are present.
+template <typename ID>
+__global__ void __launch_bounds__(kRankThreads)
+    k_rank(int n, int64_t vocab, const ID *__restrict__ ids, uint2 *__restrict__ sorted,
+           uint32_t *__restrict__ longs_count, uint32_t *__restrict__ present,
+           uint32_t *__restrict__ start, uint32_t *__restrict__ end) {
+    __shared__ __align__(16) uint32_t id[kRankTokens];
+    __shared__ uint32_t bits[kRankRows / 32], count[kRankWarps][3][32];
+    griddep_wait_then_release();
+    if (blockIdx.x == 0 && threadIdx.x == 0) *longs_count = 0;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t row0 = (int64_t)blockIdx.x * kRankRows;
+    for (int i = threadIdx.x; i < kRankRows / 32; i += kRankThreads) bits[i] = 0;
+    __syncthreads();
+    const int padded = (n + 31) & ~31;  // places behind the last token: no id is larger
+    uint32_t own[kRankTokens / kRankThreads];
+#pragma unroll
+    for (int k = 0; k < kRankTokens / kRankThreads; ++k) {
+        const int i = threadIdx.x + k * kRankThreads;
+        own[k] = i < n ? row_of(ids, i, vocab) : 0xFFFFFFFFu;
+    }
+#pragma unroll
+    for (int k = 0; k < kRankTokens / kRankThreads; ++k) {
+        const int i = threadIdx.x + k * kRankThreads;
+        if (i < padded) id[i] = own[k];
+        if (own[k] < vocab && own[k] >= row0 && own[k] < row0 + kRankRows)
+            atomicOr(&bits[(own[k] - row0) >> 5], 1u << (own[k] & 31));
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < kRankRows / 32; i += kRankThreads)
+        if (row0 + i * 32 < vocab) present[row0 / 32 + i] = bits[i];
+    if ((int64_t)blockIdx.x * 32 >= n) return;
+    const int t0 = blockIdx.x * 32, t = t0 + lane;
+    const uint32_t mine = id[t];
+    // groups of 32 tokens, the block's own among them
+    uint32_t less = 0, same = 0, before = 0;
+    for (int g = warp * 32; g < padded; g += kRankThreads) {
+        uint32_t here = 0;
+#pragma unroll
+        for (int k = 0; k < 32; k += 4) {
+            const uint4 o = *reinterpret_cast<const uint4 *>(&id[g + k]);
+            less += (o.x < mine) + (o.y < mine) + (o.z < mine) + (o.w < mine);
+            here += (o.x == mine) + (o.y == mine) + (o.z == mine) + (o.w == mine);
+        }
+        same += here;
+        if (g < t0) before += here;
+        if (g == t0)
+            for (int k = 0; k < lane; ++k) before += id[g + k] == mine;
+    }
+    count[warp][0][lane] = less, count[warp][1][lane] = same, count[warp][2][lane] = before;
+    __syncthreads();
+    if (warp != 0 || t >= n) return;
+#pragma unroll
+    for (int w = 1; w < kRankWarps; ++w)
+        less += count[w][0][lane], same += count[w][1][lane], before += count[w][2][lane];
+    sorted[less + before] = make_uint2(mine, (uint32_t)t);
+    if (mine < vocab && before == 0) {
+        start[mine] = less;
+        end[mine] = less + same;
+    }
+}
+
+// Where a pass of the radix sort reads: the ids themselves, or the pass before.
 template <typename ID>
 struct FromIds {
     const ID *ids;
     int64_t vocab;
     __device__ __forceinline__ uint2 get(int64_t i) const {
-        const int64_t id = (int64_t)__ldg(ids + i);
-        return make_uint2((uint32_t)(id >= 0 && id < vocab ? id : vocab), (uint32_t)i);
+        return make_uint2(row_of(ids, i, vocab), (uint32_t)i);
     }
 };
 struct FromPairs {
@@ -90,31 +174,31 @@ __device__ __forceinline__ int64_t first_token(int64_t n, int blocks, int b) {
     return at < n ? at : n;
 }
 
-// How many of a block's tokens have each digit.  The first pass also clears the
-// words that the kernels behind the sort fill.
+// How many of a block's tokens have each digit.  The first pass also clears what
+// k_embed_places adds to.
 template <typename SRC>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(kSortThreads)
     k_sort_count(int64_t n, SRC src, int shift, int bins, uint32_t *__restrict__ hist,
-                 uint32_t *__restrict__ longs, uint32_t *__restrict__ start, int64_t ids) {
+                 uint32_t *__restrict__ longs_count, uint32_t *__restrict__ present,
+                 int64_t words) {
     __shared__ uint32_t cnt[kMaxBins];
     griddep_wait_then_release();
-    for (int i = threadIdx.x; i < bins; i += 256) cnt[i] = 0;
-    if (start != nullptr) {
-        for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < ids;
-             i += (int64_t)gridDim.x * 256)
-            start[i] = 0;
-        if (blockIdx.x == 0 && threadIdx.x == 0) longs[0] = 0;
-    }
+    cnt[threadIdx.x] = 0;
+    for (int64_t i = (int64_t)blockIdx.x * kSortThreads + threadIdx.x; i < words;
+         i += (int64_t)gridDim.x * kSortThreads)
+        present[i] = 0;
+    if (words != 0 && blockIdx.x == 0 && threadIdx.x == 0) *longs_count = 0;
     __syncthreads();
     const int64_t i1 = first_token(n, gridDim.x, blockIdx.x + 1);
-    for (int64_t i = first_token(n, gridDim.x, blockIdx.x) + threadIdx.x; i < i1; i += 256)
+    for (int64_t i = first_token(n, gridDim.x, blockIdx.x) + threadIdx.x; i < i1;
+         i += kSortThreads)
         atomicAdd(&cnt[(src.get(i).x >> shift) & (bins - 1)], 1u);
     __syncthreads();
-    for (int i = threadIdx.x; i < bins; i += 256) hist[(int64_t)blockIdx.x * bins + i] = cnt[i];
+    if ((int)threadIdx.x < bins) hist[(int64_t)blockIdx.x * bins + threadIdx.x] = cnt[threadIdx.x];
 }
 
-// Exclusive sums of v over the 256 threads.
-__device__ __forceinline__ uint32_t exclusive_256(uint32_t v, uint32_t *red) {
+// Exclusive sums of v over the block's threads.
+__device__ __forceinline__ uint32_t exclusive_sum(uint32_t v, uint32_t *red) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     uint32_t s = v;
 #pragma unroll
@@ -126,44 +210,44 @@ __device__ __forceinline__ uint32_t exclusive_256(uint32_t v, uint32_t *red) {
     __syncthreads();
     uint32_t before = 0;
 #pragma unroll
-    for (int w = 0; w < 8; ++w) before += w < warp ? red[w] : 0;
+    for (int w = 0; w < kSortWarps; ++w) before += w < warp ? red[w] : 0;
     return before + s - v;
 }
 
 // A block's tokens to their places in the digit's order.  A place: tokens with a
 // smaller digit, then those of blocks, tiles, warps and lanes before this one.
 template <typename SRC>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(kSortThreads)
     k_sort_move(int64_t n, SRC src, int shift, int bins, const uint32_t *__restrict__ hist,
                 uint2 *__restrict__ out) {
-    __shared__ uint32_t base[kMaxBins], cnt[8][kMaxBins], red[8];
+    __shared__ uint32_t cnt[kSortWarps][kMaxBins], red[kSortWarps];
     griddep_wait_then_release();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, blocks = gridDim.x;
-    // two neighbouring digits a thread
-    uint32_t total[2] = {0, 0}, before[2] = {0, 0};
-    const int d0 = 2 * threadIdx.x;
-    for (int b = 0; b < blocks; ++b) {
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const uint32_t c = d0 + k < bins ? hist[(int64_t)b * bins + d0 + k] : 0;
-            total[k] += c;
-            before[k] += b < (int)blockIdx.x ? c : 0;
+    const int mine = threadIdx.x;  // the digit whose places this thread counts
+    uint32_t total = 0, before = 0;
+    if (mine < bins) {
+#pragma unroll 8
+        for (int b = 0; b < blocks; ++b) {
+            const uint32_t c = hist[(int64_t)b * bins + mine];
+            total += c;
+            before += b < (int)blockIdx.x ? c : 0;
         }
     }
-    const uint32_t lower = exclusive_256(total[0] + total[1], red);
-    base[d0] = lower + before[0];
-    base[d0 + 1] = lower + total[0] + before[1];
+    uint32_t base = exclusive_sum(total, red) + before;
     const int64_t i1 = first_token(n, blocks, blockIdx.x + 1);
     for (int64_t i0 = first_token(n, blocks, blockIdx.x); i0 < i1; i0 += kTile) {
-        for (int i = threadIdx.x; i < 8 * kMaxBins; i += 256) (&cnt[0][0])[i] = 0;
-        __syncthreads();
-        uint2 e[8];
-        uint32_t rank[8];
+        uint2 e[kItems];
+        uint32_t rank[kItems];
+        const int64_t first = i0 + warp * (32 * kItems) + lane;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const int64_t i = i0 + warp * 256 + k * 32 + lane;
-            const bool in = i < i1;
-            e[k] = in ? src.get(i) : make_uint2(0, 0);
+        for (int k = 0; k < kItems; ++k)
+            e[k] = first + k * 32 < i1 ? src.get(first + k * 32) : make_uint2(0, 0);
+        for (int i = threadIdx.x; i < kSortWarps * kMaxBins; i += kSortThreads)
+            (&cnt[0][0])[i] = 0;
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < kItems; ++k) {
+            const bool in = first + k * 32 < i1;
             const uint32_t digit = (e[k].x >> shift) & (bins - 1);
             // lanes past the end have a group of their own
             const uint32_t same = __match_any_sync(0xFFFFFFFFu, in ? digit : 0xFFFFFFFFu);
@@ -175,31 +259,30 @@ __global__ void __launch_bounds__(256)
             rank[k] = had + __popc(below);
         }
         __syncthreads();
-        for (int g = threadIdx.x; g < bins; g += 256) {
-            uint32_t at = base[g];
+        if (mine < bins) {
+            uint32_t c[kSortWarps];
 #pragma unroll
-            for (int w = 0; w < 8; ++w) {
-                const uint32_t c = cnt[w][g];
-                cnt[w][g] = at;
-                at += c;
+            for (int w = 0; w < kSortWarps; ++w) c[w] = cnt[w][mine];
+#pragma unroll
+            for (int w = 0; w < kSortWarps; ++w) {
+                cnt[w][mine] = base;
+                base += c[w];
             }
-            base[g] = at;
         }
         __syncthreads();
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            if (i0 + warp * 256 + k * 32 + lane < i1)
+        for (int k = 0; k < kItems; ++k) {
+            if (first + k * 32 < i1)
                 out[cnt[warp][(e[k].x >> shift) & (bins - 1)] + rank[k]] = e[k];
         }
         __syncthreads();
     }
 }
 
-// First and last places of every id, and the ids with more than c tokens (in any
-// order: each is summed by itself).
+// First and last places of every id, and which ids are present.
 __global__ void __launch_bounds__(256)
-    k_embed_places(int64_t n, int c, uint32_t vocab, const uint2 *__restrict__ sorted,
-                   uint32_t *__restrict__ longs, uint32_t *__restrict__ start,
+    k_embed_places(int64_t n, uint32_t vocab, const uint2 *__restrict__ sorted,
+                   uint32_t *__restrict__ present, uint32_t *__restrict__ start,
                    uint32_t *__restrict__ end) {
     griddep_wait_then_release();
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
@@ -207,106 +290,157 @@ __global__ void __launch_bounds__(256)
     const uint32_t id = sorted[i].x;
     if (id == vocab) return;
     if (i == 0 || sorted[i - 1].x != id) {
-        start[id] = (uint32_t)i + 1;
-        if (i + c < n && sorted[i + c].x == id) longs[1 + atomicAdd(longs, 1u)] = (uint32_t)i;
+        start[id] = (uint32_t)i;
+        atomicOr(&present[id >> 5], 1u << (id & 31));
     }
     if (i + 1 == n || sorted[i + 1].x != id) end[id] = (uint32_t)i + 1;
 }
 
-// Eight channels of a row of the table's gradient: scale * a, written or added.
+// Eight channels of a row of the table's gradient: scale * a, written or added to
+// what was there.
 template <int DT>
-__device__ __forceinline__ void put(uint4 *table, int64_t at, const float a[8], float scale,
-                                    bool accumulate) {
-    constexpr int E = RowVec<DT>::E;
+struct Out {
+    static constexpr int E = RowVec<DT>::E, Q = 8 / E;
+    uint4 old[Q];
+    __device__ __forceinline__ void load(const uint4 *table, int64_t at) {
 #pragma unroll
-    for (int q = 0; q < 8 / E; ++q) {
-        uint4 *p = table + at * (8 / E) + q;
-        float f[E];
-        if (accumulate) {
-            RowVec<DT>::get(*p, f);
+        for (int q = 0; q < Q; ++q) old[q] = table[at * Q + q];
+    }
+    __device__ __forceinline__ void put(uint4 *table, int64_t at, const float a[8], float scale,
+                                        bool accumulate) const {
 #pragma unroll
-            for (int e = 0; e < E; ++e) f[e] = fmaf(scale, a[q * E + e], f[e]);
-        } else {
+        for (int q = 0; q < Q; ++q) {
+            float f[E];
+            if (accumulate) {
+                RowVec<DT>::get(old[q], f);
 #pragma unroll
-            for (int e = 0; e < E; ++e) f[e] = scale * a[q * E + e];
+                for (int e = 0; e < E; ++e) f[e] = fmaf(scale, a[q * E + e], f[e]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < E; ++e) f[e] = scale * a[q * E + e];
+            }
+            st_stream(table + at * Q + q, RowVec<DT>::set(f));
         }
-        st_stream(p, RowVec<DT>::set(f));
+    }
+};
+
+// Zeros to the rows that no token names.  A warp takes 32 rows (a word of `present`)
+// and 4 KB of each of them at a time.
+__device__ void clear_rows(int64_t vocab, int64_t row16, const uint32_t *present, uint4 *table,
+                           int64_t warp, int64_t warps) {
+    const int lane = threadIdx.x & 31;
+    const int64_t parts = (row16 + 255) / 256, units = ((vocab + 31) / 32) * parts;
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    for (int64_t u = warp; u < units; u += warps) {
+        const int64_t word = u / parts, at = (u - word * parts) * 256 + lane;
+        uint32_t absent = ~__ldg(present + word);
+        if (word * 32 + 32 > vocab) absent &= (1u << (vocab - word * 32)) - 1u;
+        while (absent != 0) {
+            const int64_t row = word * 32 + __ffs(absent) - 1;
+            absent &= absent - 1;
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (at + k * 32 < row16) st_stream(table + row * row16 + at + k * 32, zero);
+        }
     }
 }
 
-// Sums of the pieces that start in a window of c sorted tokens, for the vectors of
-// a slice (blockIdx.y).  Blocks behind the windows clear rows that no token names.
+template <int HC>
+constexpr int sum_stages() {
+    return HC == 1 ? 16 : HC == 4 ? 5 : 3;  // tokens under way: 16 to 24 vectors a thread
+}
+
+// Sums of the pieces that start in a window of c ordered tokens, for the vectors of
+// a slice (blockIdx.y).  The window's tokens follow one another, whatever ids they
+// have; each thread copies its vector of the tokens to come to shared memory ahead of
+// the sums.  Blocks behind the windows clear the rows that no token names.
 template <int DT, int HC>
 __global__ void __launch_bounds__(256)
-    k_embed_sum(int64_t n, int64_t nv, int64_t windows, int c, uint32_t vocab, float scale,
+    k_embed_sum(int64_t n, int64_t nv, int64_t windows, int c, int64_t vocab, float scale,
                 bool accumulate, const uint2 *__restrict__ sorted,
-                const uint32_t *__restrict__ start, const uint32_t *__restrict__ end,
-                const uint4 *__restrict__ dx, uint4 *__restrict__ table, float4 *__restrict__ part) {
-    __shared__ uint32_t token[2 * kMaxPiece], ids[kMaxPiece], len[kMaxPiece], kind[kMaxPiece];
+                uint32_t *__restrict__ longs_count, uint4 *__restrict__ longs,
+                const uint32_t *__restrict__ present, const uint32_t *__restrict__ start,
+                const uint32_t *__restrict__ end, const uint4 *__restrict__ dx,
+                uint4 *__restrict__ table, float4 *__restrict__ part) {
+    constexpr int S = sum_stages<HC>();
+    enum { kLast = 1, kWhole = 2, kFirst = 4 };
+    extern __shared__ uint4 ring[];
+    __shared__ uint32_t token[2 * kMaxPiece], ids[2 * kMaxPiece], flags[2 * kMaxPiece], from, count;
     griddep_wait_then_release();
-    const int64_t v = (int64_t)blockIdx.y * blockDim.x + threadIdx.x;
     const int64_t w = blockIdx.x;
     if (w >= windows) {
-        if (v >= nv) return;
-        const float zero[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        for (int64_t r = w - windows; r < vocab; r += gridDim.x - windows)
-            if (start[r] == 0) put<DT>(table, r * nv + v, zero, 1.0f, false);
+        const int64_t wpb = blockDim.x >> 5;
+        clear_rows(vocab, nv * 8 / RowVec<DT>::E, present, table,
+                   ((w - windows) * gridDim.y + blockIdx.y) * wpb + (threadIdx.x >> 5),
+                   (gridDim.x - windows) * gridDim.y * wpb);
         return;
     }
-    const int64_t p0 = w * c;
+    if (threadIdx.x == 0) from = 2 * kMaxPiece, count = 0;
+    __syncthreads();
     for (int i = threadIdx.x; i < 2 * c; i += blockDim.x) {
-        const bool in = p0 + i < n;
-        const uint2 e = in ? sorted[p0 + i] : make_uint2(vocab, 0);
+        const int64_t p = w * c + i;
+        if (p >= n) break;
+        const uint2 e = sorted[p];
+        if (e.x == (uint32_t)vocab) break;
+        const uint32_t s = start[e.x], t = end[e.x];
+        const int in_piece = (int)(((uint32_t)p - s) & (uint32_t)(c - 1));
+        // pieces that start in this window, up to their ends in the next
+        if (in_piece > i || i - in_piece >= c) continue;
+        const bool whole = t - s <= (uint32_t)c, first = (uint32_t)p - s < (uint32_t)c;
         token[i] = e.y;
-        if (i < c) {
-            ids[i] = e.x;
-            len[i] = 0;
-            if (e.x != vocab) {
-                const uint32_t p = (uint32_t)(p0 + i), s = start[e.x] - 1, t = end[e.x];
-                if ((p - s) % c == 0) {
-                    len[i] = min((uint32_t)c, t - p);
-                    // 0: all of an id; 1 and 2: a later and the first piece of a long one
-                    kind[i] = t - s <= (uint32_t)c ? 0 : p != s ? 1 : 2;
-                }
-            }
-        }
+        ids[i] = e.x;
+        flags[i] = (in_piece == c - 1 || p + 1 == t ? kLast : 0) | (whole ? kWhole : 0) |
+                   (first ? kFirst : 0);
+        atomicMin(&from, (uint32_t)i);
+        atomicAdd(&count, 1u);
+        if (p == s && !whole && blockIdx.y == 0)
+            longs[atomicAdd(longs_count, 1u)] =
+                make_uint4(e.x, (uint32_t)w, (t - s + (uint32_t)c - 1) / (uint32_t)c, 0);
     }
     __syncthreads();
-    if (v >= nv) return;
-    for (int i = 0; i < c; ++i) {
-        const int m = len[i];
-        if (m == 0) continue;
-        float a[8];
+    const int64_t v = (int64_t)blockIdx.y * blockDim.x + threadIdx.x;
+    const int i0 = (int)from, i1 = i0 + (int)count;
+    if (v >= nv || count == 0) return;
+    auto slot = [&](int stage, int j) { return ring + (stage * HC + j) * blockDim.x + threadIdx.x; };
+    auto copy = [&](int i, int stage) {
+        if (i < i1) {
+            const uint4 *g = dx + (int64_t)token[i] * HC * nv + v;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) a[e] = 0.0f;
-        constexpr int T = 8 / HC;  // tokens whose vectors are in flight together
-        for (int k = 0; k < m; k += T) {
-            uint4 g[T * HC];
-#pragma unroll
-            for (int q = 0; q < T; ++q) {
-                const int64_t t = token[i + min(k + q, m - 1)];
-#pragma unroll
-                for (int j = 0; j < HC; ++j) g[q * HC + j] = ld_stream(dx + (t * HC + j) * nv + v);
-            }
-#pragma unroll
-            for (int q = 0; q < T; ++q) {
-                if (k + q < m) {
-#pragma unroll
-                    for (int j = 0; j < HC; ++j) {
-                        float f[8];
-                        unpack8(g[q * HC + j], f);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) a[e] += f[e];
-                    }
-                }
-            }
+            for (int j = 0; j < HC; ++j) copy16_async(slot(stage, j), g + j * nv);
         }
-        if (kind[i] == 0) {
-            put<DT>(table, (int64_t)ids[i] * nv + v, a, scale, accumulate);
-        } else {
-            float4 *p = part + ((w * 2 + (kind[i] - 1)) * nv + v) * 2;
-            p[0] = make_float4(a[0], a[1], a[2], a[3]);
-            p[1] = make_float4(a[4], a[5], a[6], a[7]);
+        copies_commit();
+    };
+#pragma unroll
+    for (int k = 0; k < S - 1; ++k) copy(i0 + k, k);
+    float a[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) a[e] = 0.0f;
+    int at = 0;
+    for (int i = i0; i < i1; ++i) {
+        const uint32_t f = flags[i];
+        const int64_t row = (int64_t)ids[i] * nv + v;
+        Out<DT> out;
+        if (accumulate && (f & (kLast | kWhole)) == (kLast | kWhole)) out.load(table, row);
+        copies_wait<S - 2>();
+#pragma unroll
+        for (int j = 0; j < HC; ++j) {
+            float x[8];
+            unpack8(*slot(at, j), x);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) a[e] += x[e];
+        }
+        copy(i + S - 1, at == 0 ? S - 1 : at - 1);
+        at = at + 1 == S ? 0 : at + 1;
+        if (f & kLast) {
+            if (f & kWhole) {
+                out.put(table, row, a, scale, accumulate);
+            } else {
+                float4 *p = part + ((w * 2 + (f & kFirst ? 1 : 0)) * nv + v) * 2;
+                p[0] = make_float4(a[0], a[1], a[2], a[3]);
+                p[1] = make_float4(a[4], a[5], a[6], a[7]);
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) a[e] = 0.0f;
         }
     }
 }
@@ -315,17 +449,19 @@ __global__ void __launch_bounds__(256)
 // eighth of them for 32 vectors (blockIdx.y), and their sums meet in shared memory.
 template <int DT>
 __global__ void __launch_bounds__(256)
-    k_embed_join(int64_t nv, int c, float scale, bool accumulate, const uint2 *__restrict__ sorted,
-                 const uint32_t *__restrict__ longs, const uint32_t *__restrict__ end,
-                 const float4 *__restrict__ part, uint4 *__restrict__ table) {
+    k_embed_join(int64_t nv, float scale, bool accumulate, const uint32_t *__restrict__ longs_count,
+                 const uint4 *__restrict__ longs, const float4 *__restrict__ part,
+                 uint4 *__restrict__ table) {
     __shared__ float red[8][32][9];
     griddep_wait_then_release();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t v = (int64_t)blockIdx.y * 32 + lane;
-    const uint32_t count = longs[0];
+    const uint32_t count = *longs_count;
     for (uint32_t i = blockIdx.x; i < count; i += gridDim.x) {
-        const uint32_t s = longs[1 + i], id = sorted[s].x;
-        const int64_t w = s / c, pieces = (end[id] - s + c - 1) / c;
+        const uint4 entry = longs[i];
+        const int64_t id = entry.x, w = entry.y, pieces = entry.z;
+        Out<DT> out;
+        if (accumulate && warp == 0 && v < nv) out.load(table, id * nv + v);
         float a[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) a[e] = 0.0f;
@@ -346,66 +482,82 @@ __global__ void __launch_bounds__(256)
             for (int q = 1; q < 8; ++q)
 #pragma unroll
                 for (int e = 0; e < 8; ++e) a[e] += red[q][lane][e];
-            put<DT>(table, (int64_t)id * nv + v, a, scale, accumulate);
+            out.put(table, id * nv + v, a, scale, accumulate);
         }
         __syncthreads();
     }
 }
 
-// Places a pass of the sort: ids (or the pairs of the pass before) to `out`.
 template <typename SRC>
 cudaError_t sort_pass(int64_t n, SRC src, int shift, int bins, const Workspace &w, uint2 *out,
-                      int64_t clear, cudaStream_t s) {
+                      int64_t clear_words, cudaStream_t s) {
     const int64_t tiles = (n + kTile - 1) / kTile;
     const dim3 grid((unsigned)(tiles < kSortBlocks ? tiles : kSortBlocks));
-    cudaError_t e = launch_overlapped(&k_sort_count<SRC>, grid, dim3(256), 0, s, n, src, shift,
-                                      bins, w.hist, w.longs, clear ? w.start : nullptr, clear);
+    cudaError_t e = launch_overlapped(&k_sort_count<SRC>, grid, dim3(kSortThreads), 0, s, n, src,
+                                      shift, bins, w.hist, w.count, w.present, clear_words);
     if (e != cudaSuccess) return e;
-    return launch_overlapped(&k_sort_move<SRC>, grid, dim3(256), 0, s, n, src, shift, bins,
+    return launch_overlapped(&k_sort_move<SRC>, grid, dim3(kSortThreads), 0, s, n, src, shift, bins,
                              (const uint32_t *)w.hist, out);
 }
 
+// Tokens in order of their ids, and each id's places.
 template <typename ID>
-cudaError_t sort_ids(const EmbedBackward &p, const Workspace &w, cudaStream_t s) {
+cudaError_t order_tokens(const EmbedBackward &p, const Workspace &w, cudaStream_t s) {
+    const ID *ids = static_cast<const ID *>(p.ids);
+    if (p.n <= kRankTokens) {
+        const int64_t by_tokens = (p.n + 31) / 32, by_rows = (p.vocab + kRankRows - 1) / kRankRows;
+        return launch_overlapped(&k_rank<ID>,
+                                 dim3((unsigned)(by_tokens > by_rows ? by_tokens : by_rows)),
+                                 dim3(kRankThreads), 0, s, (int)p.n, p.vocab, ids, w.sorted[0], w.count,
+                                 w.present, w.start, w.end);
+    }
     const int bits = bits_of(p.vocab), passes = (bits + kMaxDigitBits - 1) / kMaxDigitBits;
     const int digit = (bits + passes - 1) / passes, bins = 1 << digit;
     int to = (passes - 1) & 1;
-    cudaError_t e = sort_pass(p.n, FromIds<ID>{static_cast<const ID *>(p.ids), p.vocab}, 0, bins, w,
-                              w.sorted[to], p.vocab + 1, s);
+    cudaError_t e = sort_pass(p.n, FromIds<ID>{ids, p.vocab}, 0, bins, w, w.sorted[to],
+                              (p.vocab + 31) / 32, s);
     for (int i = 1; i < passes && e == cudaSuccess; ++i, to ^= 1)
         e = sort_pass(p.n, FromPairs{w.sorted[to]}, i * digit, bins, w, w.sorted[to ^ 1], 0, s);
-    return e;
+    if (e != cudaSuccess) return e;
+    return launch_overlapped(&k_embed_places, dim3((unsigned)((p.n + 255) / 256)), dim3(256), 0, s,
+                             p.n, (uint32_t)p.vocab, (const uint2 *)w.sorted[0], w.present, w.start,
+                             w.end);
 }
 
 template <int DT, int HC>
 cudaError_t launch(const EmbedBackward &p, const DeviceInfo &di, cudaStream_t s) {
+    static SmemState smem;
     const Workspace w = layout(p.ws, p.n, p.d, p.vocab);
     const int c = piece_tokens(p.n, p.d);
     const int64_t nv = p.d / 8, windows = (p.n + c - 1) / c;
-    cudaError_t e = p.id_bytes == 4 ? sort_ids<int32_t>(p, w, s) : sort_ids<int64_t>(p, w, s);
-    if (e != cudaSuccess) return e;
-    const uint2 *sorted = w.sorted[0];
-    e = launch_overlapped(&k_embed_places, dim3((unsigned)((p.n + 255) / 256)), dim3(256), 0, s,
-                          p.n, c, (uint32_t)p.vocab, sorted, w.longs, w.start, w.end);
+    cudaError_t e = p.id_bytes == 4 ? order_tokens<int32_t>(p, w, s) : order_tokens<int64_t>(p, w, s);
     if (e != cudaSuccess) return e;
     // slices of at most 256 vectors, as even as whole warps make them
     const int64_t slices = (nv + 255) / 256;
     const int threads = (int)(((nv + slices - 1) / slices + 31) & ~(int64_t)31);
+    constexpr int per_thread = sum_stages<HC>() * HC * 16;
+    auto *kernel = &k_embed_sum<DT, HC>;
+    e = allow_smem(smem, reinterpret_cast<const void *>(kernel), per_thread * 256, di);
+    if (e != cudaSuccess) return e;
     uint4 *table = static_cast<uint4 *>(p.dtable);
-    const int64_t cap = (int64_t)di.sms * 16;
-    const int64_t clear = p.accumulate ? 0 : p.vocab < cap ? p.vocab : cap;
-    e = launch_overlapped(&k_embed_sum<DT, HC>, dim3((unsigned)(windows + clear), (unsigned)slices),
-                          dim3(threads), 0, s, p.n, nv, windows, c, (uint32_t)p.vocab, p.scale,
-                          p.accumulate, sorted, (const uint32_t *)w.start, (const uint32_t *)w.end,
+    const uint2 *sorted = w.sorted[0];
+    // to clear rows: a few blocks an SM, no more than there is work for
+    const int64_t work = (p.vocab * p.d + (1 << 16) - 1) >> 16, cap = (int64_t)di.sms * 4;
+    const int64_t clear = p.accumulate ? 0 : work < cap ? work : cap;
+    e = launch_overlapped(kernel, dim3((unsigned)(windows + clear), (unsigned)slices), dim3(threads),
+                          (size_t)per_thread * threads, s, p.n, nv, windows, c, p.vocab, p.scale,
+                          p.accumulate, sorted, w.count, w.longs, (const uint32_t *)w.present,
+                          (const uint32_t *)w.start, (const uint32_t *)w.end,
                           reinterpret_cast<const uint4 *>(p.dx), table,
                           reinterpret_cast<float4 *>(w.part));
     if (e != cudaSuccess) return e;
-    return launch_overlapped(&k_embed_join<DT>,
-                             dim3((unsigned)(windows < 64 ? windows : 64),
-                                  (unsigned)((nv + 31) / 32)),
-                             dim3(256), 0, s, nv, c, p.scale, p.accumulate, sorted,
-                             (const uint32_t *)w.longs, (const uint32_t *)w.end,
-                             (const float4 *)w.part, table);
+    // ids with more than c tokens: no more than windows, and few of them as a rule
+    const int64_t parts = (nv + 31) / 32;
+    int64_t joins = parts < 152 ? 2432 / parts : 16;
+    joins = joins < windows ? joins : windows;
+    return launch_overlapped(&k_embed_join<DT>, dim3((unsigned)joins, (unsigned)parts), dim3(256), 0,
+                             s, nv, p.scale, p.accumulate, (const uint32_t *)w.count,
+                             (const uint4 *)w.longs, (const float4 *)w.part, table);
 }
 
 template <int DT>
