@@ -8,6 +8,8 @@
 // one piece, and its sum is written to the table at once.  Longer ones leave a row of
 // partial sums per piece, which k_embed_join adds up in order.  So every gradient
 // is read once and a frequent id's sum is spread over the GPU.
+#include <algorithm>
+
 #include "hc_rows.cuh"
 
 namespace hc {
@@ -445,8 +447,8 @@ __global__ void __launch_bounds__(256)
     }
 }
 
-// The partial sums of an id with more than c tokens, in order: 8 warps take every
-// eighth of them for 32 vectors (blockIdx.y), and their sums meet in shared memory.
+// The partial sums of an id with more than C tokens, in order: 8 warps take every
+// eighth of them for 32 vectors, and their sums meet in shared memory.
 template <int DT>
 __global__ void __launch_bounds__(256)
     k_embed_join(int64_t nv, float scale, bool accumulate, const uint32_t *__restrict__ longs_count,
@@ -455,36 +457,38 @@ __global__ void __launch_bounds__(256)
     __shared__ float red[8][32][9];
     griddep_wait_then_release();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t v = (int64_t)blockIdx.y * 32 + lane;
     const uint32_t count = *longs_count;
     for (uint32_t i = blockIdx.x; i < count; i += gridDim.x) {
         const uint4 entry = longs[i];
         const int64_t id = entry.x, w = entry.y, pieces = entry.z;
-        Out<DT> out;
-        if (accumulate && warp == 0 && v < nv) out.load(table, id * nv + v);
-        float a[8];
+        for (int64_t v0 = (int64_t)blockIdx.y * 32; v0 < nv; v0 += (int64_t)gridDim.y * 32) {
+            const int64_t v = v0 + lane;
+            Out<DT> out;
+            if (accumulate && warp == 0 && v < nv) out.load(table, id * nv + v);
+            float a[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) a[e] = 0.0f;
-        if (v < nv) {
+            for (int e = 0; e < 8; ++e) a[e] = 0.0f;
+            if (v < nv) {
 #pragma unroll 4
-            for (int64_t k = warp; k < pieces; k += 8) {
-                const float4 *p = part + (((w + k) * 2 + (k == 0 ? 1 : 0)) * nv + v) * 2;
-                const float4 lo = p[0], hi = p[1];
-                a[0] += lo.x, a[1] += lo.y, a[2] += lo.z, a[3] += lo.w;
-                a[4] += hi.x, a[5] += hi.y, a[6] += hi.z, a[7] += hi.w;
+                for (int64_t k = warp; k < pieces; k += 8) {
+                    const float4 *p = part + (((w + k) * 2 + (k == 0 ? 1 : 0)) * nv + v) * 2;
+                    const float4 lo = p[0], hi = p[1];
+                    a[0] += lo.x, a[1] += lo.y, a[2] += lo.z, a[3] += lo.w;
+                    a[4] += hi.x, a[5] += hi.y, a[6] += hi.z, a[7] += hi.w;
+                }
             }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) red[warp][lane][e] = a[e];
+            __syncthreads();
+            if (warp == 0 && v < nv) {
+#pragma unroll
+                for (int q = 1; q < 8; ++q)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) a[e] += red[q][lane][e];
+                out.put(table, id * nv + v, a, scale, accumulate);
+            }
+            __syncthreads();
         }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) red[warp][lane][e] = a[e];
-        __syncthreads();
-        if (warp == 0 && v < nv) {
-#pragma unroll
-            for (int q = 1; q < 8; ++q)
-#pragma unroll
-                for (int e = 0; e < 8; ++e) a[e] += red[q][lane][e];
-            out.put(table, id * nv + v, a, scale, accumulate);
-        }
-        __syncthreads();
     }
 }
 
@@ -542,8 +546,8 @@ cudaError_t launch(const EmbedBackward &p, const DeviceInfo &di, cudaStream_t s)
     uint4 *table = static_cast<uint4 *>(p.dtable);
     const uint2 *sorted = w.sorted[0];
     // to clear rows: a few blocks an SM, no more than there is work for
-    const int64_t work = (p.vocab * p.d + (1 << 16) - 1) >> 16, cap = (int64_t)di.sms * 4;
-    const int64_t clear = p.accumulate ? 0 : work < cap ? work : cap;
+    const int64_t work = (p.vocab * p.d + (1 << 16) - 1) >> 16;
+    const int64_t clear = p.accumulate ? 0 : std::min(work, (int64_t)di.sms * 4);
     e = launch_overlapped(kernel, dim3((unsigned)(windows + clear), (unsigned)slices), dim3(threads),
                           (size_t)per_thread * threads, s, p.n, nv, windows, c, p.vocab, p.scale,
                           p.accumulate, sorted, w.count, w.longs, (const uint32_t *)w.present,
@@ -552,9 +556,8 @@ cudaError_t launch(const EmbedBackward &p, const DeviceInfo &di, cudaStream_t s)
                           reinterpret_cast<float4 *>(w.part));
     if (e != cudaSuccess) return e;
     // ids with more than c tokens: no more than windows, and few of them as a rule
-    const int64_t parts = (nv + 31) / 32;
-    int64_t joins = parts < 152 ? 2432 / parts : 16;
-    joins = joins < windows ? joins : windows;
+    const int64_t parts = std::min<int64_t>((nv + 31) / 32, 1024);
+    const int64_t joins = std::min(windows, std::max<int64_t>(2432 / parts, 16));
     return launch_overlapped(&k_embed_join<DT>, dim3((unsigned)joins, (unsigned)parts), dim3(256), 0,
                              s, nv, p.scale, p.accumulate, (const uint32_t *)w.count,
                              (const uint4 *)w.longs, (const float4 *)w.part, table);

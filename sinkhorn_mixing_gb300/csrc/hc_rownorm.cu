@@ -91,15 +91,14 @@ __global__ void __launch_bounds__(BLOCK ? kRingThreads : 256, BLOCK ? 1 : V < 3 
             var = s[0] * inv_d;
             if (!CENTER) break;
             delta = s[NS - 1] * inv_d;
-            var = fmaf(-delta, delta, var);
-            var = var < 0.0f ? 0.0f : var;  // a row of one number; NaN stays
+            var = row_variance(var, delta);
             // the same for all of a block; all of a warp go along, in vain but for those in need
-            const bool again = round == 0 && !(delta * delta <= var);
+            const bool again = round == 0 && row_again(var, delta);
             if (BLOCK ? !again : !__any_sync(0xFFFFFFFFu, again)) break;
             if (again) mu += delta;
             read();
         }
-        const float r = rsqrtf(var + eps), minus_dr = -delta * r;
+        const float r = rsqrtf(var + eps), minus_dr = r == 0.0f ? 0.0f : -delta * r;
         if (t < rows) {
 #pragma unroll
             for (int i = 0; i < V; ++i) {

@@ -125,14 +125,13 @@ __global__ void __launch_bounds__(BLOCK ? kRingThreads : 256, BLOCK ? 1 : V < 3 
             var = s[0] * inv_d;
             if (CENTER) {
                 delta = s[NS - 2] * inv_d;
-                var = fmaf(-delta, delta, var);
-                var = var < 0.0f ? 0.0f : var;  // a row of one number; NaN stays
+                var = row_variance(var, delta);
             }
         };
         sums();
         if (CENTER) {
             // the same for all of a block; all of a warp go along, in vain but for those in need
-            const bool again = !(delta * delta <= var);
+            const bool again = row_again(var, delta);
             if (BLOCK ? again : __any_sync(0xFFFFFFFFu, again)) {
                 if (again) mu += delta;
                 sums();
@@ -143,9 +142,9 @@ __global__ void __launch_bounds__(BLOCK ? kRingThreads : 256, BLOCK ? 1 : V < 3 
         const float c1 = CENTER ? s[NS - 1] * inv_d : 0.0f;
         const float gc = CENTER ? fmaf(-delta, c1, s[1] * inv_d) : s[1] * inv_d;
         const float c2 = r == 0.0f ? 0.0f : gc * r;
-        const float mr = -(mu + delta) * r, rc1 = -c1 * r, rc2 = -c2 * r;
-        const uint64_t rr = pack2(r, r), minus_mr = pack2(mr, mr), minus_rc1 = pack2(rc1, rc1),
-                       minus_rc2 = pack2(rc2, rc2);
+        const float minus_mean = -(mu + delta), rc1 = -c1 * r, rc2 = -c2 * r;
+        const uint64_t rr = pack2(r, r), minus_mu = pack2(minus_mean, minus_mean),
+                       minus_rc1 = pack2(rc1, rc1), minus_rc2 = pack2(rc2, rc2);
 #pragma unroll
         for (int i = 0; i < V; ++i)
             if (in && l + i * lanes < nv) {
@@ -153,7 +152,7 @@ __global__ void __launch_bounds__(BLOCK ? kRingThreads : 256, BLOCK ? 1 : V < 3 
                 row_pairs<DT>(gr[i], g);
 #pragma unroll
                 for (int e = 0; e < E / 2; ++e) {
-                    const uint64_t h = CENTER ? ffma2_of(f[e], rr, minus_mr) : fmul2(f[e], rr);
+                    const uint64_t h = fmul2(CENTER ? fadd2(f[e], minus_mu) : f[e], rr);
                     ffma2(aw[i][e], g[e], h);
                     if (DB) ab[DB ? i : 0][e] = fadd2(ab[DB ? i : 0][e], g[e]);
                     const uint64_t gw = fmul2(g[e], wk[i][e]);

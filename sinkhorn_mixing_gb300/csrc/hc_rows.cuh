@@ -174,7 +174,16 @@ __device__ __forceinline__ void group_sum(float a[NS], int lg, float (*red)[32])
 // number p near its values, the mean of the row's first 16 bytes: with delta =
 // mean(x - p), the mean is p + delta and the variance mean((x - p)^2) - delta^2,
 // which loses nothing worth naming while delta^2 is at most the variance.  Where it is
-// not (or either is not finite) the round is repeated about p + delta.
+// not (or is not finite) the round is repeated about p + delta.  Squares above
+// binary32's range make the variance infinite, whatever delta is.
+__device__ __forceinline__ float row_variance(float mean_sq, float delta) {
+    if (mean_sq == __int_as_float(0x7F800000)) return mean_sq;
+    const float var = fmaf(-delta, delta, mean_sq);
+    return var < 0.0f ? 0.0f : var;  // a row of one number; NaN stays
+}
+__device__ __forceinline__ bool row_again(float var, float delta) {
+    return !(delta * delta <= var) || var == __int_as_float(0x7F800000);
+}
 template <int DT>
 __device__ __forceinline__ float row_guess(const uint4 &v) {
     float f[RowVec<DT>::E], s = 0.0f;

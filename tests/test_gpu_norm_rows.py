@@ -207,6 +207,32 @@ def test_extremes(hc):
     check_norm(hc, far, None, None, True, 1e-5)
 
 
+@pytest.mark.parametrize("d", [64, 1000, 5120, 32776])
+def test_squares_out_of_range(hc, d):
+    """Rows whose squares leave binary32 have r = 0: y is the bias, dx is zero, and the row adds
+    nothing to the weight's gradient.  The rows beside them are as they would be."""
+    x, dy, w, b = case(12, d, BF16, 12)
+    big = [1, 2, 5, 8]
+    x[1], x[2] = 1e30, torch.linspace(-3e25, 2e25, d).to(BF16)
+    x[5, 3], x[8, -1] = 1e33, -1e33
+    rest = [i for i in range(12) if i not in big]
+    for center in (False, True):
+        y = hc.hc_norm(*dev(x, w, b), eps=1e-5, center=center).cpu()
+        assert torch.equal(y[big], b.to(BF16).expand(4, d))
+        dx, dw, db = (t.cpu() for t in hc.hc_norm_backward(*dev(dy, x, w), eps=1e-5, center=center,
+                                                           want_dbias=True))
+        # row 1 is one number: about its mean it has no squares, and its gradient is its own
+        assert not dx[big[1:] if center else big].any()
+        a, g = f64(x[rest], w, b), f64(dy[rest], x[rest], w)
+        within(y[rest], ref.norm(*a, center, 1e-5), ref.norm_bound(*a, center, 1e-5, BF16), "y")
+        want = ref.norm_backward(*g, center, 1e-5)
+        bound = ref.norm_backward_bound(*g, center, 1e-5, BF16)
+        within(dx[rest], want[0], bound[0], "dx")
+        within(dw, want[1], bound[1], "dweight")
+        all_dy = dy.double()
+        within(db, all_dy.sum(0), bound[2] + 32 * ref.U32 * all_dy.abs().sum(0), "dbias")
+
+
 def test_empty_and_shapes(hc):
     x = torch.empty(0, 64, dtype=BF16, device="cuda")
     assert hc.hc_norm(x).shape == (0, 64)
