@@ -10,52 +10,32 @@
 // is read once and a frequent id's sum is spread over the GPU.
 #include <algorithm>
 
+#include "hc_embed_order.h"
 #include "hc_rows.cuh"
 
 namespace hc {
 namespace {
 
-constexpr int kSortThreads = 512;
-constexpr int kSortWarps = kSortThreads / 32;
-constexpr int kTile = 2048;  // tokens a block of the radix sort has at a time
-constexpr int kItems = kTile / kSortThreads;
-constexpr int kSortBlocks = 304;
-constexpr int kMaxDigitBits = 9;
-constexpr int kMaxBins = 1 << kMaxDigitBits;  // as many as threads
 constexpr int kMaxPiece = 32;
-constexpr int kRankTokens = 4096;  // up to which tokens are ranked by comparing them all
-constexpr int kRankRows = 8192;    // table rows whose presence a block of k_rank notes
-constexpr int kRankThreads = 1024;
-constexpr int kRankWarps = kRankThreads / 32;
 
-int bits_of(int64_t v) {  // of the numbers 0 .. v
-    int b = 1;
-    while ((v >> b) != 0) ++b;
-    return b;
-}
-
-// Tokens a piece: 32, fewer where there are too few of them to fill the GPU (in
-// pieces times slices of 1,024 channels).  4,096 tokens of 4 x 5120 into 32,768 rows:
-// 101 us with 32 a piece, 106 with 16, 122 with 8 (the pieces' sums are written, read
-// and joined); 1,537 of 8 x 1032 into 50,001: 47, 48 and 55.
+// Tokens a piece: 32, down to 4 where there are too few of them to fill the GPU (in
+// pieces times slices of 1,024 channels): a block's tokens follow one another, but
+// ids with more than a piece's tokens pay for a second launch's work.  In us, with
+// 4, 8, 16 and 32 a piece: 300 tokens of 1 x 1000 8.6, 10, 13, 17; 1,500 into 1,000
+// rows 15.7, 14.6, 13.7, 13.2 (21 with two); 4,096 of 4 x 5120 122, 106, 101 from 8 on.
 int piece_tokens(int64_t n, int64_t d) {
     const int64_t slices = (d + 1023) / 1024;
     int c = kMaxPiece;
-    while (c > 1 && n * slices < (int64_t)c * 608) c /= 2;
+    while (c > 4 && n * slices < (int64_t)c * 256) c /= 2;
     return c;
 }
 
 size_t align256(size_t b) { return (b + 255) & ~(size_t)255; }
 
 struct Workspace {
-    uint2 *sorted[2];   // (id, token): the last pass leaves them in [0]
-    uint32_t *hist;     // [blocks, bins]
-    uint32_t *count;    // of `longs`
-    uint4 *longs;       // ids with more than C tokens: id, first window, pieces
-    uint32_t *present;  // a bit for each row of the table: some token names it
-    uint32_t *start;    // [vocab], first place of an id that is present
-    uint32_t *end;      // [vocab], the place behind its last
-    float *part;        // [windows, 2, d]
+    TokenOrder order;
+    uint4 *longs;  // ids with more than C tokens: id, first window, pieces
+    float *part;   // [windows, 2, d]
     size_t bytes;
 };
 
@@ -69,233 +49,17 @@ Workspace layout(uint8_t *base, int64_t n, int64_t d, int64_t vocab) {
         return base == nullptr ? nullptr : base + here;
     };
     Workspace w;
-    w.sorted[0] = reinterpret_cast<uint2 *>(take((size_t)n * 8));
-    w.sorted[1] = reinterpret_cast<uint2 *>(take((size_t)n * 8));
-    w.hist = reinterpret_cast<uint32_t *>(take((size_t)kSortBlocks * kMaxBins * 4));
-    w.count = reinterpret_cast<uint32_t *>(take(4));
+    w.order.sorted[0] = reinterpret_cast<uint2 *>(take((size_t)n * 8));
+    w.order.sorted[1] = reinterpret_cast<uint2 *>(take((size_t)n * 8));
+    w.order.hist = reinterpret_cast<uint32_t *>(take(order_hist_bytes(n)));
+    w.order.present = reinterpret_cast<uint32_t *>(take((size_t)((vocab + 31) / 32) * 4));
+    w.order.start = reinterpret_cast<uint32_t *>(take((size_t)vocab * 4));
+    w.order.end = reinterpret_cast<uint32_t *>(take((size_t)vocab * 4));
+    w.order.count = reinterpret_cast<uint32_t *>(take(4));
     w.longs = reinterpret_cast<uint4 *>(take((size_t)windows * 16));
-    w.present = reinterpret_cast<uint32_t *>(take((size_t)((vocab + 31) / 32) * 4));
-    w.start = reinterpret_cast<uint32_t *>(take((size_t)vocab * 4));
-    w.end = reinterpret_cast<uint32_t *>(take((size_t)vocab * 4));
     w.part = reinterpret_cast<float *>(take((size_t)windows * 2 * d * 4));
     w.bytes = at;
     return w;
-}
-
-// An id as it is ordered: those outside the table come behind it, as `vocab`.
-template <typename ID>
-__device__ __forceinline__ uint32_t row_of(const ID *ids, int64_t i, int64_t vocab) {
-    const int64_t id = (int64_t)__ldg(ids + i);
-    return (uint32_t)(id >= 0 && id < vocab ? id : vocab);
-}
-
-// Few tokens: a token's place is the number of tokens with a smaller id, and of those
-// before it with its own.  A block has 32 of them, one a lane, and all ids in shared
-// memory; its warps share the comparisons.  n^2 of them take 1.4 us at 4,096 tokens,
-// where the passes of the sort below take 20.  A block also notes which of
-// kRankRows rows of the table are present.
-template <typename ID>
-__global__ void __launch_bounds__(kRankThreads)
-    k_rank(int n, int64_t vocab, const ID *__restrict__ ids, uint2 *__restrict__ sorted,
-           uint32_t *__restrict__ longs_count, uint32_t *__restrict__ present,
-           uint32_t *__restrict__ start, uint32_t *__restrict__ end) {
-    __shared__ __align__(16) uint32_t id[kRankTokens];
-    __shared__ uint32_t bits[kRankRows / 32], count[kRankWarps][3][32];
-    griddep_wait_then_release();
-    if (blockIdx.x == 0 && threadIdx.x == 0) *longs_count = 0;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t row0 = (int64_t)blockIdx.x * kRankRows;
-    for (int i = threadIdx.x; i < kRankRows / 32; i += kRankThreads) bits[i] = 0;
-    __syncthreads();
-    const int padded = (n + 31) & ~31;  // places behind the last token: no id is larger
-    uint32_t own[kRankTokens / kRankThreads];
-#pragma unroll
-    for (int k = 0; k < kRankTokens / kRankThreads; ++k) {
-        const int i = threadIdx.x + k * kRankThreads;
-        own[k] = i < n ? row_of(ids, i, vocab) : 0xFFFFFFFFu;
-    }
-#pragma unroll
-    for (int k = 0; k < kRankTokens / kRankThreads; ++k) {
-        const int i = threadIdx.x + k * kRankThreads;
-        if (i < padded) id[i] = own[k];
-        if (own[k] < vocab && own[k] >= row0 && own[k] < row0 + kRankRows)
-            atomicOr(&bits[(own[k] - row0) >> 5], 1u << (own[k] & 31));
-    }
-    __syncthreads();
-    for (int i = threadIdx.x; i < kRankRows / 32; i += kRankThreads)
-        if (row0 + i * 32 < vocab) present[row0 / 32 + i] = bits[i];
-    if ((int64_t)blockIdx.x * 32 >= n) return;
-    const int t0 = blockIdx.x * 32, t = t0 + lane;
-    const uint32_t mine = id[t];
-    // groups of 32 tokens, the block's own among them
-    uint32_t less = 0, same = 0, before = 0;
-    for (int g = warp * 32; g < padded; g += kRankThreads) {
-        uint32_t here = 0;
-#pragma unroll
-        for (int k = 0; k < 32; k += 4) {
-            const uint4 o = *reinterpret_cast<const uint4 *>(&id[g + k]);
-            less += (o.x < mine) + (o.y < mine) + (o.z < mine) + (o.w < mine);
-            here += (o.x == mine) + (o.y == mine) + (o.z == mine) + (o.w == mine);
-        }
-        same += here;
-        if (g < t0) before += here;
-        if (g == t0)
-            for (int k = 0; k < lane; ++k) before += id[g + k] == mine;
-    }
-    count[warp][0][lane] = less, count[warp][1][lane] = same, count[warp][2][lane] = before;
-    __syncthreads();
-    if (warp != 0 || t >= n) return;
-#pragma unroll
-    for (int w = 1; w < kRankWarps; ++w)
-        less += count[w][0][lane], same += count[w][1][lane], before += count[w][2][lane];
-    sorted[less + before] = make_uint2(mine, (uint32_t)t);
-    if (mine < vocab && before == 0) {
-        start[mine] = less;
-        end[mine] = less + same;
-    }
-}
-
-// Where a pass of the radix sort reads: the ids themselves, or the pass before.
-template <typename ID>
-struct FromIds {
-    const ID *ids;
-    int64_t vocab;
-    __device__ __forceinline__ uint2 get(int64_t i) const {
-        return make_uint2(row_of(ids, i, vocab), (uint32_t)i);
-    }
-};
-struct FromPairs {
-    const uint2 *pairs;
-    __device__ __forceinline__ uint2 get(int64_t i) const { return pairs[i]; }
-};
-
-// A block's tokens in a pass: whole tiles, in order.
-__device__ __forceinline__ int64_t first_token(int64_t n, int blocks, int b) {
-    const int64_t tiles = (n + kTile - 1) / kTile, per = (tiles + blocks - 1) / blocks;
-    const int64_t at = (int64_t)b * per * kTile;
-    return at < n ? at : n;
-}
-
-// How many of a block's tokens have each digit.  The first pass also clears what
-// k_embed_places adds to.
-template <typename SRC>
-__global__ void __launch_bounds__(kSortThreads)
-    k_sort_count(int64_t n, SRC src, int shift, int bins, uint32_t *__restrict__ hist,
-                 uint32_t *__restrict__ longs_count, uint32_t *__restrict__ present,
-                 int64_t words) {
-    __shared__ uint32_t cnt[kMaxBins];
-    griddep_wait_then_release();
-    cnt[threadIdx.x] = 0;
-    for (int64_t i = (int64_t)blockIdx.x * kSortThreads + threadIdx.x; i < words;
-         i += (int64_t)gridDim.x * kSortThreads)
-        present[i] = 0;
-    if (words != 0 && blockIdx.x == 0 && threadIdx.x == 0) *longs_count = 0;
-    __syncthreads();
-    const int64_t i1 = first_token(n, gridDim.x, blockIdx.x + 1);
-    for (int64_t i = first_token(n, gridDim.x, blockIdx.x) + threadIdx.x; i < i1;
-         i += kSortThreads)
-        atomicAdd(&cnt[(src.get(i).x >> shift) & (bins - 1)], 1u);
-    __syncthreads();
-    if ((int)threadIdx.x < bins) hist[(int64_t)blockIdx.x * bins + threadIdx.x] = cnt[threadIdx.x];
-}
-
-// Exclusive sums of v over the block's threads.
-__device__ __forceinline__ uint32_t exclusive_sum(uint32_t v, uint32_t *red) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    uint32_t s = v;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-        const uint32_t o = __shfl_up_sync(0xFFFFFFFFu, s, off);
-        if (lane >= off) s += o;
-    }
-    if (lane == 31) red[warp] = s;
-    __syncthreads();
-    uint32_t before = 0;
-#pragma unroll
-    for (int w = 0; w < kSortWarps; ++w) before += w < warp ? red[w] : 0;
-    return before + s - v;
-}
-
-// A block's tokens to their places in the digit's order.  A place: tokens with a
-// smaller digit, then those of blocks, tiles, warps and lanes before this one.
-template <typename SRC>
-__global__ void __launch_bounds__(kSortThreads)
-    k_sort_move(int64_t n, SRC src, int shift, int bins, const uint32_t *__restrict__ hist,
-                uint2 *__restrict__ out) {
-    __shared__ uint32_t cnt[kSortWarps][kMaxBins], red[kSortWarps];
-    griddep_wait_then_release();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, blocks = gridDim.x;
-    const int mine = threadIdx.x;  // the digit whose places this thread counts
-    uint32_t total = 0, before = 0;
-    if (mine < bins) {
-#pragma unroll 8
-        for (int b = 0; b < blocks; ++b) {
-            const uint32_t c = hist[(int64_t)b * bins + mine];
-            total += c;
-            before += b < (int)blockIdx.x ? c : 0;
-        }
-    }
-    uint32_t base = exclusive_sum(total, red) + before;
-    const int64_t i1 = first_token(n, blocks, blockIdx.x + 1);
-    for (int64_t i0 = first_token(n, blocks, blockIdx.x); i0 < i1; i0 += kTile) {
-        uint2 e[kItems];
-        uint32_t rank[kItems];
-        const int64_t first = i0 + warp * (32 * kItems) + lane;
-#pragma unroll
-        for (int k = 0; k < kItems; ++k)
-            e[k] = first + k * 32 < i1 ? src.get(first + k * 32) : make_uint2(0, 0);
-        for (int i = threadIdx.x; i < kSortWarps * kMaxBins; i += kSortThreads)
-            (&cnt[0][0])[i] = 0;
-        __syncthreads();
-#pragma unroll
-        for (int k = 0; k < kItems; ++k) {
-            const bool in = first + k * 32 < i1;
-            const uint32_t digit = (e[k].x >> shift) & (bins - 1);
-            // lanes past the end have a group of their own
-            const uint32_t same = __match_any_sync(0xFFFFFFFFu, in ? digit : 0xFFFFFFFFu);
-            const uint32_t below = same & ((1u << lane) - 1u);
-            const uint32_t had = in ? cnt[warp][digit] : 0;
-            __syncwarp();
-            if (in && below == 0) cnt[warp][digit] = had + __popc(same);
-            __syncwarp();
-            rank[k] = had + __popc(below);
-        }
-        __syncthreads();
-        if (mine < bins) {
-            uint32_t c[kSortWarps];
-#pragma unroll
-            for (int w = 0; w < kSortWarps; ++w) c[w] = cnt[w][mine];
-#pragma unroll
-            for (int w = 0; w < kSortWarps; ++w) {
-                cnt[w][mine] = base;
-                base += c[w];
-            }
-        }
-        __syncthreads();
-#pragma unroll
-        for (int k = 0; k < kItems; ++k) {
-            if (first + k * 32 < i1)
-                out[cnt[warp][(e[k].x >> shift) & (bins - 1)] + rank[k]] = e[k];
-        }
-        __syncthreads();
-    }
-}
-
-// First and last places of every id, and which ids are present.
-__global__ void __launch_bounds__(256)
-    k_embed_places(int64_t n, uint32_t vocab, const uint2 *__restrict__ sorted,
-                   uint32_t *__restrict__ present, uint32_t *__restrict__ start,
-                   uint32_t *__restrict__ end) {
-    griddep_wait_then_release();
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= n) return;
-    const uint32_t id = sorted[i].x;
-    if (id == vocab) return;
-    if (i == 0 || sorted[i - 1].x != id) {
-        start[id] = (uint32_t)i;
-        atomicOr(&present[id >> 5], 1u << (id & 31));
-    }
-    if (i + 1 == n || sorted[i + 1].x != id) end[id] = (uint32_t)i + 1;
 }
 
 // Eight channels of a row of the table's gradient: scale * a, written or added to
@@ -326,23 +90,39 @@ struct Out {
     }
 };
 
-// Zeros to the rows that no token names.  A warp takes 32 rows (a word of `present`)
-// and 4 KB of each of them at a time.
+// Zeros to the rows that no token names.  A warp takes a part of 32 rows at a time (a
+// word of `present`): 8 KB of them as one run where rows are shorter than 4 KB, else
+// 1 KB of each (64 tokens into 32,768 fp32 rows of 5120: 98 us, with 4 KB 108).
+inline __host__ __device__ int64_t clear_parts(int64_t row16) {
+    return row16 < 256 ? (32 * row16 + 511) / 512 : (row16 + 63) / 64;
+}
 __device__ void clear_rows(int64_t vocab, int64_t row16, const uint32_t *present, uint4 *table,
                            int64_t warp, int64_t warps) {
     const int lane = threadIdx.x & 31;
-    const int64_t parts = (row16 + 255) / 256, units = ((vocab + 31) / 32) * parts;
+    const int64_t parts = clear_parts(row16), units = (vocab + 31) / 32 * parts;
     const uint4 zero = make_uint4(0, 0, 0, 0);
     for (int64_t u = warp; u < units; u += warps) {
-        const int64_t word = u / parts, at = (u - word * parts) * 256 + lane;
+        const int64_t word = u / parts;
+        const int part = (int)(u - word * parts);
         uint32_t absent = ~__ldg(present + word);
         if (word * 32 + 32 > vocab) absent &= (1u << (vocab - word * 32)) - 1u;
+        uint4 *rows = table + word * 32 * row16;
+        if (row16 < 256) {
+            const uint32_t r16 = (uint32_t)row16, all = 32 * r16;
+#pragma unroll 4
+            for (int k = 0; k < 16; ++k) {
+                const uint32_t i = part * 512 + k * 32 + lane;
+                if (i < all && (absent >> (i / r16) & 1u)) st_stream(rows + i, zero);
+            }
+            continue;
+        }
+        const int64_t at = (int64_t)part * 64 + lane;
         while (absent != 0) {
-            const int64_t row = word * 32 + __ffs(absent) - 1;
+            uint4 *row = rows + (__ffs(absent) - 1) * row16 + at;
             absent &= absent - 1;
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-                if (at + k * 32 < row16) st_stream(table + row * row16 + at + k * 32, zero);
+            for (int k = 0; k < 2; ++k)
+                if (at + k * 32 < row16) st_stream(row + k * 32, zero);
         }
     }
 }
@@ -492,49 +272,14 @@ __global__ void __launch_bounds__(256)
     }
 }
 
-template <typename SRC>
-cudaError_t sort_pass(int64_t n, SRC src, int shift, int bins, const Workspace &w, uint2 *out,
-                      int64_t clear_words, cudaStream_t s) {
-    const int64_t tiles = (n + kTile - 1) / kTile;
-    const dim3 grid((unsigned)(tiles < kSortBlocks ? tiles : kSortBlocks));
-    cudaError_t e = launch_overlapped(&k_sort_count<SRC>, grid, dim3(kSortThreads), 0, s, n, src,
-                                      shift, bins, w.hist, w.count, w.present, clear_words);
-    if (e != cudaSuccess) return e;
-    return launch_overlapped(&k_sort_move<SRC>, grid, dim3(kSortThreads), 0, s, n, src, shift, bins,
-                             (const uint32_t *)w.hist, out);
-}
-
-// Tokens in order of their ids, and each id's places.
-template <typename ID>
-cudaError_t order_tokens(const EmbedBackward &p, const Workspace &w, cudaStream_t s) {
-    const ID *ids = static_cast<const ID *>(p.ids);
-    if (p.n <= kRankTokens) {
-        const int64_t by_tokens = (p.n + 31) / 32, by_rows = (p.vocab + kRankRows - 1) / kRankRows;
-        return launch_overlapped(&k_rank<ID>,
-                                 dim3((unsigned)(by_tokens > by_rows ? by_tokens : by_rows)),
-                                 dim3(kRankThreads), 0, s, (int)p.n, p.vocab, ids, w.sorted[0], w.count,
-                                 w.present, w.start, w.end);
-    }
-    const int bits = bits_of(p.vocab), passes = (bits + kMaxDigitBits - 1) / kMaxDigitBits;
-    const int digit = (bits + passes - 1) / passes, bins = 1 << digit;
-    int to = (passes - 1) & 1;
-    cudaError_t e = sort_pass(p.n, FromIds<ID>{ids, p.vocab}, 0, bins, w, w.sorted[to],
-                              (p.vocab + 31) / 32, s);
-    for (int i = 1; i < passes && e == cudaSuccess; ++i, to ^= 1)
-        e = sort_pass(p.n, FromPairs{w.sorted[to]}, i * digit, bins, w, w.sorted[to ^ 1], 0, s);
-    if (e != cudaSuccess) return e;
-    return launch_overlapped(&k_embed_places, dim3((unsigned)((p.n + 255) / 256)), dim3(256), 0, s,
-                             p.n, (uint32_t)p.vocab, (const uint2 *)w.sorted[0], w.present, w.start,
-                             w.end);
-}
-
 template <int DT, int HC>
 cudaError_t launch(const EmbedBackward &p, const DeviceInfo &di, cudaStream_t s) {
     static SmemState smem;
     const Workspace w = layout(p.ws, p.n, p.d, p.vocab);
     const int c = piece_tokens(p.n, p.d);
     const int64_t nv = p.d / 8, windows = (p.n + c - 1) / c;
-    cudaError_t e = p.id_bytes == 4 ? order_tokens<int32_t>(p, w, s) : order_tokens<int64_t>(p, w, s);
+    const TokenOrder &o = w.order;
+    cudaError_t e = launch_order(p.n, p.vocab, p.id_bytes, p.ids, o, s);
     if (e != cudaSuccess) return e;
     // slices of at most 256 vectors, as even as whole warps make them
     const int64_t slices = (nv + 255) / 256;
@@ -544,14 +289,17 @@ cudaError_t launch(const EmbedBackward &p, const DeviceInfo &di, cudaStream_t s)
     e = allow_smem(smem, reinterpret_cast<const void *>(kernel), per_thread * 256, di);
     if (e != cudaSuccess) return e;
     uint4 *table = static_cast<uint4 *>(p.dtable);
-    const uint2 *sorted = w.sorted[0];
-    // to clear rows: a few blocks an SM, no more than there is work for
-    const int64_t work = (p.vocab * p.d + (1 << 16) - 1) >> 16;
-    const int64_t clear = p.accumulate ? 0 : std::min(work, (int64_t)di.sms * 4);
+    const uint2 *sorted = o.sorted[0];
+    // to clear rows: a warp for each part of them, up to 64 blocks an SM and slice (16,384 x 4 x
+    // 5120 into 131,072 fp32 rows: 498 us, with 16 blocks 502, with 4 about 520)
+    const int64_t warps = slices * (threads / 32),
+                  units = (p.vocab + 31) / 32 * clear_parts(p.d * row_type_bytes(p.dtype) / 16);
+    const int64_t clear =
+        p.accumulate ? 0 : std::min((units + warps - 1) / warps, (int64_t)di.sms * 64);
     e = launch_overlapped(kernel, dim3((unsigned)(windows + clear), (unsigned)slices), dim3(threads),
                           (size_t)per_thread * threads, s, p.n, nv, windows, c, p.vocab, p.scale,
-                          p.accumulate, sorted, w.count, w.longs, (const uint32_t *)w.present,
-                          (const uint32_t *)w.start, (const uint32_t *)w.end,
+                          p.accumulate, sorted, o.count, w.longs, (const uint32_t *)o.present,
+                          (const uint32_t *)o.start, (const uint32_t *)o.end,
                           reinterpret_cast<const uint4 *>(p.dx), table,
                           reinterpret_cast<float4 *>(w.part));
     if (e != cudaSuccess) return e;
@@ -559,7 +307,7 @@ cudaError_t launch(const EmbedBackward &p, const DeviceInfo &di, cudaStream_t s)
     const int64_t parts = std::min<int64_t>((nv + 31) / 32, 1024);
     const int64_t joins = std::min(windows, std::max<int64_t>(2432 / parts, 16));
     return launch_overlapped(&k_embed_join<DT>, dim3((unsigned)joins, (unsigned)parts), dim3(256), 0,
-                             s, nv, p.scale, p.accumulate, (const uint32_t *)w.count,
+                             s, nv, p.scale, p.accumulate, (const uint32_t *)o.count,
                              (const uint4 *)w.longs, (const float4 *)w.part, table);
 }
 

@@ -103,6 +103,11 @@ SIZES = [(1, 8, 1), (2, 8, 2), (31, 64, 7), (33, 5120, 40), (64, 1032, 511), (65
          (5000, 5120, 64), (20011, 72, 1 << 20), (66000, 64, 50001)]
 
 
+# either side of where the tokens are put in order another way
+SIZES += [(4095, 16, 4095), (4096, 16, 70000), (4097, 8, 3), (8191, 24, 300), (16400, 16, 1 << 19),
+          (65535, 8, 131072), (65536, 16, 97), (65537, 8, 1000)]
+
+
 @pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("n,d,vocab", SIZES)
 def test_embed_backward_whole_numbers(hc, n, d, vocab, kind):
@@ -237,6 +242,24 @@ def test_embed_backward_long(hc):
     got = hc.hc_embed_backward(dx, ids, vocab, dtype=BF16)
     assert torch.all(got[-1] == 8.0) and torch.all(got[(n - 2) % 1000] == 16.0)
     assert int(torch.count_nonzero(got)) == 2 * d
+
+
+@pytest.mark.parametrize("n", [3000, 9000])
+def test_embed_backward_most_rows(hc, n):
+    """Ids of all 31 bits; only the rows that tokens name are touched."""
+    vocab, d = (1 << 31) - 2, 8
+    g = gen(n)
+    ids = torch.randint(0, vocab, (n,), generator=g)
+    ids[::3], ids[5], ids[6] = ids[0].item(), vocab - 1, 0
+    dx = whole((n, 1, d), g)
+    table = torch.empty(vocab, d, dtype=BF16, device="cuda")
+    rows, at = ids.unique(return_inverse=True)
+    table[rows.cuda()] = 1.0
+    hc.hc_embed_backward(dx.cuda(), ids.cuda(), vocab, dtable=table, accumulate=True)
+    want = torch.ones(rows.numel(), d).index_add_(0, at, dx[:, 0].float()).to(BF16)
+    assert torch.equal(table[rows.cuda()].cpu(), want)
+    x = hc.hc_embed(ids.to(torch.int32).cuda(), table, hc_mult=1)
+    assert torch.equal(x[:, 0].cpu(), want[at])
 
 
 def test_refusals(hc):
