@@ -62,33 +62,29 @@ Workspace layout(uint8_t *base, int64_t n, int64_t d, int64_t vocab) {
     return w;
 }
 
-// Eight channels of a row of the table's gradient: scale * a, written or added to
-// what was there.
+// Eight channels of a row of the table's gradient lie in ROW16 vectors.
 template <int DT>
-struct Out {
-    static constexpr int E = RowVec<DT>::E, Q = 8 / E;
-    uint4 old[Q];
-    __device__ __forceinline__ void load(const uint4 *table, int64_t at) {
+constexpr int kRow16 = 8 / RowVec<DT>::E;
+
+// scale * a, or that and what was there (`old`), rounded once.
+template <int DT, bool ADD>
+__device__ __forceinline__ void put(uint4 *table, int64_t at, const float a[8], float scale,
+                                    const uint4 old[kRow16<DT>]) {
+    constexpr int E = RowVec<DT>::E;
 #pragma unroll
-        for (int q = 0; q < Q; ++q) old[q] = table[at * Q + q];
-    }
-    __device__ __forceinline__ void put(uint4 *table, int64_t at, const float a[8], float scale,
-                                        bool accumulate) const {
+    for (int q = 0; q < kRow16<DT>; ++q) {
+        float f[E];
+        if (ADD) {
+            RowVec<DT>::get(old[q], f);
 #pragma unroll
-        for (int q = 0; q < Q; ++q) {
-            float f[E];
-            if (accumulate) {
-                RowVec<DT>::get(old[q], f);
+            for (int e = 0; e < E; ++e) f[e] = fmaf(scale, a[q * E + e], f[e]);
+        } else {
 #pragma unroll
-                for (int e = 0; e < E; ++e) f[e] = fmaf(scale, a[q * E + e], f[e]);
-            } else {
-#pragma unroll
-                for (int e = 0; e < E; ++e) f[e] = scale * a[q * E + e];
-            }
-            st_stream(table + at * Q + q, RowVec<DT>::set(f));
+            for (int e = 0; e < E; ++e) f[e] = scale * a[q * E + e];
         }
+        st_stream(table + at * kRow16<DT> + q, RowVec<DT>::set(f));
     }
-};
+}
 
 // Zeros to the rows that no token names.  A warp takes a part of 32 rows at a time (a
 // word of `present`): 8 KB of them as one run where rows are shorter than 4 KB, else
@@ -127,25 +123,25 @@ __device__ void clear_rows(int64_t vocab, int64_t row16, const uint32_t *present
     }
 }
 
+// Tokens under way in k_embed_sum, 16 to 24 vectors a thread.
 template <int HC>
-constexpr int sum_stages() {
-    return HC == 1 ? 16 : HC == 4 ? 5 : 3;  // tokens under way: 16 to 24 vectors a thread
-}
+constexpr int kSumStages = HC == 1 ? 16 : HC == 4 ? 5 : 3;
 
 // Sums of the pieces that start in a window of c ordered tokens, for the vectors of
 // a slice (blockIdx.y).  The window's tokens follow one another, whatever ids they
 // have; each thread copies its vector of the tokens to come to shared memory ahead of
-// the sums.  Blocks behind the windows clear the rows that no token names.
-template <int DT, int HC>
+// the sums.  (What the sums are added to is read when they are due: copied ahead as
+// well, 65,536 tokens took 614 us in place of 566.)  Blocks behind the windows clear
+// the rows that no token names.
+template <int DT, int HC, bool ADD>
 __global__ void __launch_bounds__(256)
     k_embed_sum(int64_t n, int64_t nv, int64_t windows, int c, int64_t vocab, float scale,
-                bool accumulate, const uint2 *__restrict__ sorted,
-                uint32_t *__restrict__ longs_count, uint4 *__restrict__ longs,
-                const uint32_t *__restrict__ present, const uint32_t *__restrict__ start,
-                const uint32_t *__restrict__ end, const uint4 *__restrict__ dx,
-                uint4 *__restrict__ table, float4 *__restrict__ part) {
-    constexpr int S = sum_stages<HC>();
-    enum { kLast = 1, kWhole = 2, kFirst = 4 };
+                const uint2 *__restrict__ sorted, uint32_t *__restrict__ longs_count,
+                uint4 *__restrict__ longs, const uint32_t *__restrict__ present,
+                const uint32_t *__restrict__ start, const uint32_t *__restrict__ end,
+                const uint4 *__restrict__ dx, uint4 *table, float4 *__restrict__ part) {
+    constexpr int S = kSumStages<HC>, Q = kRow16<DT>;
+    enum { kLast = 1, kWhole = 2, kFirst = 4, kRow = kLast | kWhole };
     extern __shared__ uint4 ring[];
     __shared__ uint32_t token[2 * kMaxPiece], ids[2 * kMaxPiece], flags[2 * kMaxPiece], from, count;
     griddep_wait_then_release();
@@ -183,7 +179,9 @@ __global__ void __launch_bounds__(256)
     const int64_t v = (int64_t)blockIdx.y * blockDim.x + threadIdx.x;
     const int i0 = (int)from, i1 = i0 + (int)count;
     if (v >= nv || count == 0) return;
-    auto slot = [&](int stage, int j) { return ring + (stage * HC + j) * blockDim.x + threadIdx.x; };
+    auto slot = [&](int stage, int j) {
+        return ring + (stage * HC + j) * blockDim.x + threadIdx.x;
+    };
     auto copy = [&](int i, int stage) {
         if (i < i1) {
             const uint4 *g = dx + (int64_t)token[i] * HC * nv + v;
@@ -201,8 +199,10 @@ __global__ void __launch_bounds__(256)
     for (int i = i0; i < i1; ++i) {
         const uint32_t f = flags[i];
         const int64_t row = (int64_t)ids[i] * nv + v;
-        Out<DT> out;
-        if (accumulate && (f & (kLast | kWhole)) == (kLast | kWhole)) out.load(table, row);
+        uint4 old[Q];
+        if (ADD && (f & kRow) == kRow)
+#pragma unroll
+            for (int q = 0; q < Q; ++q) old[q] = table[row * Q + q];
         copies_wait<S - 2>();
 #pragma unroll
         for (int j = 0; j < HC; ++j) {
@@ -211,11 +211,11 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
             for (int e = 0; e < 8; ++e) a[e] += x[e];
         }
-        copy(i + S - 1, at == 0 ? S - 1 : at - 1);
-        at = at + 1 == S ? 0 : at + 1;
+        const int next = at == 0 ? S - 1 : at - 1;
+        if (ADD) copy(i + S - 1, next);  // `old` is on its way; else the row goes out first
         if (f & kLast) {
             if (f & kWhole) {
-                out.put(table, row, a, scale, accumulate);
+                put<DT, ADD>(table, row, a, scale, old);
             } else {
                 float4 *p = part + ((w * 2 + (f & kFirst ? 1 : 0)) * nv + v) * 2;
                 p[0] = make_float4(a[0], a[1], a[2], a[3]);
@@ -224,14 +224,16 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
             for (int e = 0; e < 8; ++e) a[e] = 0.0f;
         }
+        if (!ADD) copy(i + S - 1, next);
+        at = at + 1 == S ? 0 : at + 1;
     }
 }
 
 // The partial sums of an id with more than C tokens, in order: 8 warps take every
 // eighth of them for 32 vectors, and their sums meet in shared memory.
-template <int DT>
+template <int DT, bool ADD>
 __global__ void __launch_bounds__(256)
-    k_embed_join(int64_t nv, float scale, bool accumulate, const uint32_t *__restrict__ longs_count,
+    k_embed_join(int64_t nv, float scale, const uint32_t *__restrict__ longs_count,
                  const uint4 *__restrict__ longs, const float4 *__restrict__ part,
                  uint4 *__restrict__ table) {
     __shared__ float red[8][32][9];
@@ -243,8 +245,10 @@ __global__ void __launch_bounds__(256)
         const int64_t id = entry.x, w = entry.y, pieces = entry.z;
         for (int64_t v0 = (int64_t)blockIdx.y * 32; v0 < nv; v0 += (int64_t)gridDim.y * 32) {
             const int64_t v = v0 + lane;
-            Out<DT> out;
-            if (accumulate && warp == 0 && v < nv) out.load(table, id * nv + v);
+            uint4 old[kRow16<DT>];
+            if (ADD && warp == 0 && v < nv)
+#pragma unroll
+                for (int q = 0; q < kRow16<DT>; ++q) old[q] = table[(id * nv + v) * kRow16<DT> + q];
             float a[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) a[e] = 0.0f;
@@ -265,14 +269,14 @@ __global__ void __launch_bounds__(256)
                 for (int q = 1; q < 8; ++q)
 #pragma unroll
                     for (int e = 0; e < 8; ++e) a[e] += red[q][lane][e];
-                out.put(table, id * nv + v, a, scale, accumulate);
+                put<DT, ADD>(table, id * nv + v, a, scale, old);
             }
             __syncthreads();
         }
     }
 }
 
-template <int DT, int HC>
+template <int DT, int HC, bool ADD>
 cudaError_t launch(const EmbedBackward &p, const DeviceInfo &di, cudaStream_t s) {
     static SmemState smem;
     const Workspace w = layout(p.ws, p.n, p.d, p.vocab);
@@ -284,8 +288,8 @@ cudaError_t launch(const EmbedBackward &p, const DeviceInfo &di, cudaStream_t s)
     // slices of at most 256 vectors, as even as whole warps make them
     const int64_t slices = (nv + 255) / 256;
     const int threads = (int)(((nv + slices - 1) / slices + 31) & ~(int64_t)31);
-    constexpr int per_thread = sum_stages<HC>() * HC * 16;
-    auto *kernel = &k_embed_sum<DT, HC>;
+    constexpr int per_thread = kSumStages<HC> * HC * 16;
+    auto *kernel = &k_embed_sum<DT, HC, ADD>;
     e = allow_smem(smem, reinterpret_cast<const void *>(kernel), per_thread * 256, di);
     if (e != cudaSuccess) return e;
     uint4 *table = static_cast<uint4 *>(p.dtable);
@@ -295,10 +299,10 @@ cudaError_t launch(const EmbedBackward &p, const DeviceInfo &di, cudaStream_t s)
     const int64_t warps = slices * (threads / 32),
                   units = (p.vocab + 31) / 32 * clear_parts(p.d * row_type_bytes(p.dtype) / 16);
     const int64_t clear =
-        p.accumulate ? 0 : std::min((units + warps - 1) / warps, (int64_t)di.sms * 64);
+        ADD ? 0 : std::min((units + warps - 1) / warps, (int64_t)di.sms * 64);
     e = launch_overlapped(kernel, dim3((unsigned)(windows + clear), (unsigned)slices), dim3(threads),
                           (size_t)per_thread * threads, s, p.n, nv, windows, c, p.vocab, p.scale,
-                          p.accumulate, sorted, o.count, w.longs, (const uint32_t *)o.present,
+                          sorted, o.count, w.longs, (const uint32_t *)o.present,
                           (const uint32_t *)o.start, (const uint32_t *)o.end,
                           reinterpret_cast<const uint4 *>(p.dx), table,
                           reinterpret_cast<float4 *>(w.part));
@@ -306,16 +310,21 @@ cudaError_t launch(const EmbedBackward &p, const DeviceInfo &di, cudaStream_t s)
     // ids with more than c tokens: no more than windows, and few of them as a rule
     const int64_t parts = std::min<int64_t>((nv + 31) / 32, 1024);
     const int64_t joins = std::min(windows, std::max<int64_t>(2432 / parts, 16));
-    return launch_overlapped(&k_embed_join<DT>, dim3((unsigned)joins, (unsigned)parts), dim3(256), 0,
-                             s, nv, p.scale, p.accumulate, (const uint32_t *)o.count,
+    return launch_overlapped(&k_embed_join<DT, ADD>, dim3((unsigned)joins, (unsigned)parts), dim3(256), 0,
+                             s, nv, p.scale, (const uint32_t *)o.count,
                              (const uint4 *)w.longs, (const float4 *)w.part, table);
+}
+
+template <int DT, bool ADD>
+cudaError_t launch(const EmbedBackward &p, const DeviceInfo &di, cudaStream_t s) {
+    return p.hc == 1   ? launch<DT, 1, ADD>(p, di, s)
+           : p.hc == 4 ? launch<DT, 4, ADD>(p, di, s)
+                       : launch<DT, 8, ADD>(p, di, s);
 }
 
 template <int DT>
 cudaError_t launch(const EmbedBackward &p, const DeviceInfo &di, cudaStream_t s) {
-    return p.hc == 1   ? launch<DT, 1>(p, di, s)
-           : p.hc == 4 ? launch<DT, 4>(p, di, s)
-                       : launch<DT, 8>(p, di, s);
+    return p.accumulate ? launch<DT, true>(p, di, s) : launch<DT, false>(p, di, s);
 }
 
 }  // namespace
