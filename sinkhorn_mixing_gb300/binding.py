@@ -593,9 +593,18 @@ def _row_type(dtype, name):
     return code
 
 
-def _param(t, name, d, index):
-    """An optional fp32 parameter of d values: its pointer, or None."""
-    return None if t is None else _sized(t, name, d, _F32, index)
+def _row_tensor(t, name):
+    """A tensor of rows [..., d]: its device, shape, rows, width, type and the type's code."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    dtype, shape = t.dtype, t.shape
+    code = _row_type(dtype, name)
+    if not (t.is_cuda and t.is_contiguous()):
+        _need(t, name, dtype)
+    if len(shape) < 1:
+        raise ValueError("a row of channels at least is needed")
+    d = shape[-1]
+    return t.device, shape, t.numel() // d if d else 0, d, dtype, code
 
 
 def hc_norm(x, weight=None, bias=None, eps: float = 1e-20, center: bool = False, y=None,
@@ -603,15 +612,11 @@ def hc_norm(x, weight=None, bias=None, eps: float = 1e-20, center: bool = False,
     """x [..., d] bf16, fp16 or fp32 -> (x - mean) / sqrt(variance + eps) * weight + bias over
     each row, in x's type (y may be x itself).  center=False leaves the mean in and takes the
     mean square (RMS norm).  weight, bias [d] fp32, or None."""
-    if not isinstance(x, torch.Tensor):
-        raise TypeError("x must be a torch.Tensor")
-    code = _row_type(x.dtype, "x")
-    _need(x, "x", x.dtype)
-    dev = x.device
-    shape, n, d = _rows_of(x)
-    wp, bp = _param(weight, "weight", d, dev.index), _param(bias, "bias", d, dev.index)
-    y = _made(y, "y", shape, x.dtype, dev, stream)
-    _run("hc_norm", dev, stream, n, d, code, int(center), eps, x.data_ptr(), wp, bp, y.data_ptr())
+    dev, shape, n, d, dtype, code = _row_tensor(x, "x")
+    wp = None if weight is None else _sized(weight, "weight", d, _F32, dev.index)
+    bp = None if bias is None else _sized(bias, "bias", d, _F32, dev.index)
+    y = _made(y, "y", shape, dtype, dev, stream)
+    _run("hc_norm", dev, stream, n, d, code, bool(center), eps, x.data_ptr(), wp, bp, y.data_ptr())
     return y
 
 
@@ -625,17 +630,12 @@ def hc_norm_backward(dy, x, weight=None, eps: float = 1e-20, center: bool = Fals
                      dbias=None, workspace=None, stream=None):
     """Gradients of hc_norm from dy [..., d], of x's type, and x, the forward call's input.
     Returns (dx, dweight-or-None, dbias-or-None); dx may be dy itself."""
-    if not isinstance(x, torch.Tensor):
-        raise TypeError("x must be a torch.Tensor")
-    code = _row_type(x.dtype, "x")
-    _need(x, "x", x.dtype)
-    dev = x.device
-    shape, n, d = _rows_of(x)
-    _on(dy, "dy", x.dtype, dev.index)
+    dev, shape, n, d, dtype, code = _row_tensor(x, "x")
+    _on(dy, "dy", dtype, dev.index)
     if dy.shape != shape:
-        raise ValueError("dy must have shape %s, got %s" % (shape, tuple(dy.shape)))
-    wp = _param(weight, "weight", d, dev.index)
-    dx = _made(dx, "dx", shape, x.dtype, dev, stream)
+        raise ValueError("dy must have shape %s, got %s" % (tuple(shape), tuple(dy.shape)))
+    wp = None if weight is None else _sized(weight, "weight", d, _F32, dev.index)
+    dx = _made(dx, "dx", shape, dtype, dev, stream)
     if want_dweight or dweight is not None:
         dweight = _made(dweight, "dweight", (d,), _F32, dev, stream)
     if want_dbias or dbias is not None:
@@ -644,7 +644,7 @@ def hc_norm_backward(dy, x, weight=None, eps: float = 1e-20, center: bool = Fals
         workspace = _made(None, "workspace", (hc_norm_backward_bytes(n, d),), _U8, dev, stream)
     else:
         _need(workspace, "workspace", _U8, dev)
-    _run("hc_norm_backward", dev, stream, n, d, code, int(center), eps, dy.data_ptr(),
+    _run("hc_norm_backward", dev, stream, n, d, code, bool(center), eps, dy.data_ptr(),
          x.data_ptr(), wp, dx.data_ptr(), _ptr(dweight), _ptr(dbias), workspace.data_ptr(),
          workspace.numel())
     return dx, dweight, dbias
