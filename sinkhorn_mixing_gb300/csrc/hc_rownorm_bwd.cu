@@ -17,11 +17,15 @@ constexpr int kStages = 3;         // rows a group has under way
 constexpr int kRingThreads = 512;  // of a block at most: 128 registers each
 constexpr int kParts = 304;        // rows of partial sums: two for each of a GB300's 152 SMs
 
+constexpr int kLongChannels = 40;  // a thread's of a row that does not fit the ring
+constexpr int kLongRow = kLongChannels * kRingThreads;
+
 // Rows of partial sums at most, by the width: up to four blocks an SM where rows are
-// narrow, and no more than 10 MB of them.
+// narrow, one for each SM of a GB300 where they are long, and about 10 MB of them.
 int64_t max_parts(int64_t rows, int64_t d) {
     int64_t m = (int64_t)kParts * 8192 / d;
     m = m > 2 * kParts ? 2 * kParts : m < 1 ? 1 : m;
+    if (d <= kLongRow && m < kParts / 2) m = kParts / 2;
     return rows < m ? rows : m;
 }
 
@@ -218,6 +222,131 @@ __global__ void __launch_bounds__(BLOCK ? kRingThreads : 256, BLOCK ? 1 : V < 3 
     }
 }
 
+// Rows of up to kLongRow channels that do not fit the ring: a block of kRingThreads has a row,
+// reads it for the sums and, from L2, again for the outputs, while the next row is on
+// its way from HBM to L2.  The sums over the block's rows stay in registers as above.
+template <int DT, bool CENTER, bool DB>
+__global__ void __launch_bounds__(kRingThreads)
+    k_norm_backward_long(int64_t rows, int nv, float eps, const uint4 *dy0,
+                         const uint4 *__restrict__ x0, const float *__restrict__ w, uint4 *dx0,
+                         float *__restrict__ part_w, float *__restrict__ part_b) {
+    constexpr int E = RowVec<DT>::E, V = kLongChannels / E, NS = CENTER ? 4 : 2;
+    __shared__ __align__(16) float red[2][NS][32];
+    clear_red(&red[0][0][0], 2 * NS * 32);
+    griddep_wait_then_release();
+    const int l = threadIdx.x;
+    const float inv_d = 1.0f / (float)(nv * E);
+    uint64_t aw[V][E / 2], ab[DB ? V : 1][E / 2];
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+        for (int e = 0; e < E / 2; ++e) aw[i][e] = ab[DB ? i : 0][e] = 0;
+    auto weights = [&](int v, uint64_t k[E / 2]) {
+        float f[E];
+        row_params<E>(w, v, 1.0f, f);
+#pragma unroll
+        for (int e = 0; e < E / 2; ++e) k[e] = pack2(f[2 * e], f[2 * e + 1]);
+    };
+    int odd = 0;
+    for (int64_t t = blockIdx.x; t < rows; t += gridDim.x) {
+        const uint4 *x = x0 + t * nv, *dy = dy0 + t * nv;
+        uint64_t f[E / 2], g[E / 2], wk[E / 2];
+        // TOGETHER: the loads are behind no branch (past the row's end a thread reads its first
+        // vector for nothing), so that as many go out together as registers allow.  8,192 x
+        // 20480: RMS in bf16 234 us in place of 282, but fp32 483 in place of 372 and layer norm
+        // in bf16 322 in place of 246, whose registers the loads take from the sums.
+        constexpr bool TOGETHER = !DB && E == 8;
+        auto read = [&](int i, uint64_t a[E / 2], uint64_t b[E / 2], uint64_t c[E / 2]) {
+            const int at = l + i * kRingThreads, v = !TOGETHER || at < nv ? at : l;
+            row_pairs<DT>(__ldg(x + v), a);
+            row_pairs<DT>(dy[v], b);
+            weights(v, c);
+        };
+        float s[NS], mu = CENTER ? row_guess<DT>(__ldg(x)) : 0.0f, delta = 0.0f, var;
+        for (int round = 0;; ++round) {
+            uint64_t sq = 0, sgc = 0, sg = 0, sc = 0;
+            const uint64_t minus_p = pack2(-mu, -mu);
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const bool in = l + i * kRingThreads < nv;
+                if (!TOGETHER && !in) break;
+                read(i, f, g, wk);
+                if (in)
+#pragma unroll
+                    for (int e = 0; e < E / 2; ++e) {
+                        const uint64_t c = CENTER ? fadd2(f[e], minus_p) : f[e];
+                        const uint64_t gw = fmul2(g[e], wk[e]);
+                        ffma2(sq, c, c);
+                        ffma2(sgc, gw, c);
+                        if (CENTER) sc = fadd2(sc, c), sg = fadd2(sg, gw);
+                    }
+            }
+            s[0] = sum2(sq), s[1] = sum2(sgc);
+            if (CENTER) s[NS - 2] = sum2(sc), s[NS - 1] = sum2(sg);
+            block_sum<NS>(s, red[odd]);
+            odd ^= 1;
+            var = s[0] * inv_d;
+            if (!CENTER) break;
+            delta = s[NS - 2] * inv_d;
+            var = row_variance(var, delta);
+            if (round != 0 || !row_again(var, delta)) break;  // the same for all of the block
+            mu += delta;
+        }
+        if (t + gridDim.x < rows) {
+            // a line of 128 bytes for each eighth thread's vector
+            const int64_t ahead = (int64_t)gridDim.x * nv;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const int v = l + i * kRingThreads;
+                if (v < nv && (l & 7) == 0) {
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(x + ahead + v));
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(dy + ahead + v));
+                }
+            }
+        }
+        const float r = rsqrtf(var + eps);
+        const float c1 = CENTER ? s[NS - 1] * inv_d : 0.0f;
+        const float gc = CENTER ? fmaf(-delta, c1, s[1] * inv_d) : s[1] * inv_d;
+        const float c2 = r == 0.0f ? 0.0f : gc * r;
+        const float minus_mean = -(mu + delta), rc1 = -c1 * r, rc2 = -c2 * r;
+        const uint64_t rr = pack2(r, r), minus_mu = pack2(minus_mean, minus_mean),
+                       minus_rc1 = pack2(rc1, rc1), minus_rc2 = pack2(rc2, rc2);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int v = l + i * kRingThreads;
+            if (!TOGETHER && v >= nv) break;
+            read(i, f, g, wk);
+            if (v < nv) {
+#pragma unroll
+                for (int e = 0; e < E / 2; ++e) {
+                    const uint64_t h = fmul2(CENTER ? fadd2(f[e], minus_mu) : f[e], rr);
+                    ffma2(aw[i][e], g[e], h);
+                    if (DB) ab[DB ? i : 0][e] = fadd2(ab[DB ? i : 0][e], g[e]);
+                    const uint64_t gw = fmul2(g[e], wk[e]);
+                    f[e] = ffma2_of(h, minus_rc2,
+                                    CENTER ? ffma2_of(gw, rr, minus_rc1) : fmul2(gw, rr));
+                }
+                st_stream(dx0 + t * nv + v, row_from_pairs<DT>(f));
+            }
+        }
+    }
+    const int64_t d = (int64_t)nv * E;
+    part_w += blockIdx.x * d, part_b += blockIdx.x * d;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int v = l + i * kRingThreads;
+        if (v >= nv) break;
+        float sw[E], sb[E];
+#pragma unroll
+        for (int e = 0; e < E / 2; ++e) {
+            unpack2(aw[i][e], sw[2 * e], sw[2 * e + 1]);
+            if (DB) unpack2(ab[DB ? i : 0][e], sb[2 * e], sb[2 * e + 1]);
+        }
+        put_sums<E>(part_w, v, sw);
+        if (DB) put_sums<E>(part_b, v, sb);
+    }
+}
+
 // Any width, first part: a row's mean, r, mean(g) and mean(g h).
 template <int DT, bool CENTER>
 __global__ void __launch_bounds__(256)
@@ -406,12 +535,27 @@ cudaError_t launch_ring(const RowNormBackward &p, int64_t nv, const DeviceInfo &
     }
 }
 
+template <int DT, bool CENTER, bool DB>
+cudaError_t launch_long(const RowNormBackward &p, int64_t nv, const DeviceInfo &di,
+                        cudaStream_t s) {
+    const int parts = (int)std::min((int64_t)di.sms, max_parts(p.rows, p.d));
+    float *part_w = reinterpret_cast<float *>(p.ws), *part_b = part_w + (size_t)parts * p.d;
+    const cudaError_t e = launch_overlapped(
+        &k_norm_backward_long<DT, CENTER, DB>, dim3((unsigned)parts), dim3(kRingThreads), 0, s,
+        p.rows, (int)nv, p.eps, static_cast<const uint4 *>(p.dy), static_cast<const uint4 *>(p.x),
+        p.weight, static_cast<uint4 *>(p.dx), part_w, part_b);
+    return e != cudaSuccess ? e : launch_sums(p, parts, part_w, part_b, s);
+}
+
 template <int DT, bool CENTER>
 cudaError_t launch(const RowNormBackward &p, const DeviceInfo &di, cudaStream_t s) {
     const int64_t nv = p.d / RowVec<DT>::E, cap = (int64_t)di.sms * 64;
     if (nv <= 4 * kRingThreads)
         return CENTER || p.dbias ? launch_ring<DT, CENTER, true>(p, nv, di, s)
                                  : launch_ring<DT, CENTER, CENTER>(p, nv, di, s);
+    if (p.d <= kLongRow)
+        return CENTER || p.dbias ? launch_long<DT, CENTER, true>(p, nv, di, s)
+                                 : launch_long<DT, CENTER, CENTER>(p, nv, di, s);
     const uint4 *dy = static_cast<const uint4 *>(p.dy), *x = static_cast<const uint4 *>(p.x);
     float4 *stats = reinterpret_cast<float4 *>(p.ws);
     const int64_t most = max_parts(p.rows, p.d), run = (p.rows + most - 1) / most;

@@ -58,7 +58,8 @@ def check_backward(hc, dy, x, w, center, eps):
 # every way in which rows are shared out: rows narrower than a warp's vectors, rows of whole and of
 # broken numbers of warps, rows that fill a block's registers and rows that do not fit them
 WIDTHS = [8, 16, 24, 40, 64, 120, 128, 136, 256, 264, 512, 520, 1000, 1024, 1032, 1536, 2048, 2056,
-          4096, 4104, 5120, 5128, 8192, 8200, 16384, 16392, 20480, 32768, 32776, 65544]
+          4096, 4104, 5120, 5128, 8192, 8200, 12288, 12296, 16384, 16392, 20480, 20488, 32768, 32776,
+          65544]
 
 
 @pytest.mark.parametrize("center", [False, True])
@@ -74,7 +75,8 @@ def test_widths(hc, d, dtype, center):
 @pytest.mark.parametrize("center", [False, True])
 @pytest.mark.parametrize("rows,d", [(1, 8), (1, 5120), (2, 1000), (63, 5120), (151, 2048),
                                     (305, 1032), (613, 5120), (1001, 128), (2500, 1000),
-                                    (70001, 16), (9999, 40), (1217, 8192), (700, 20480)])
+                                    (70001, 16), (9999, 40), (1217, 8192), (700, 20480), (153, 16392),
+                                    (400, 20488)])
 def test_rows(hc, rows, d, center):
     for dtype in (BF16, F32):
         x, dy, w, b = case(rows, d, dtype, 1)
@@ -82,7 +84,7 @@ def test_rows(hc, rows, d, center):
         check_backward(hc, dy, x, w, center, 1e-20)
 
 
-@pytest.mark.parametrize("d", [40, 1000, 5120, 32776])
+@pytest.mark.parametrize("d", [40, 1000, 5120, 18440, 32776])
 @pytest.mark.parametrize("center", [False, True])
 def test_optional_parameters(hc, d, center):
     x, dy, w, b = case(33, d, BF16, 2)
@@ -121,7 +123,7 @@ def test_against_differences(hc, d, center):
 
 
 @pytest.mark.parametrize("center", [False, True])
-@pytest.mark.parametrize("d", [128, 1000, 5120, 32776])
+@pytest.mark.parametrize("d", [128, 1000, 5120, 18440, 32776])
 def test_same_bits_and_in_place(hc, d, center):
     x, dy, w, b = dev(*case(777 if d < 8192 else 50, d, BF16, 4))
     kw = dict(eps=1e-5, center=center)
@@ -139,7 +141,7 @@ def test_same_bits_and_in_place(hc, d, center):
     assert torch.equal(hc.hc_norm(x.view(-1, 1, d), w, b, **kw).view_as(y), y)
 
 
-@pytest.mark.parametrize("d", [40, 128, 1000, 5120, 32776])
+@pytest.mark.parametrize("d", [40, 128, 1000, 5120, 18440, 32776])
 def test_guards(hc, d):
     """What lies before and behind the outputs stays as it is."""
     rows = 13
@@ -162,7 +164,7 @@ def test_guards(hc, d):
 
 
 @pytest.mark.parametrize("center", [False, True])
-@pytest.mark.parametrize("d", [128, 1000, 5120, 32776])
+@pytest.mark.parametrize("d", [128, 1000, 5120, 18440, 32776])
 def test_bad_rows_stay_alone(hc, d, center):
     """NaN, infinities and zeros spoil their own row's outputs and no other's."""
     x, dy, w, b = case(40, d, BF16, 6)
@@ -207,7 +209,7 @@ def test_extremes(hc):
     check_norm(hc, far, None, None, True, 1e-5)
 
 
-@pytest.mark.parametrize("d", [64, 1000, 5120, 32776])
+@pytest.mark.parametrize("d", [64, 1000, 5120, 18440, 32776])
 def test_squares_out_of_range(hc, d):
     """Rows whose squares leave binary32 have r = 0: y is the bias, dx is zero, and the row adds
     nothing to the weight's gradient.  The rows beside them are as they would be."""
@@ -331,7 +333,7 @@ def test_refusals(hc):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
-@pytest.mark.parametrize("d", [8, 40, 128, 1000, 5120, 32776])
+@pytest.mark.parametrize("d", [8, 40, 128, 1000, 5120, 18440, 32776])
 def test_layer_norm_of_rows_that_start_apart(hc, d, dtype):
     """Rows whose first channels say nothing of their mean, beside ordinary ones: outliers in front,
     a far mean behind zeros, one number in all channels but the last."""
