@@ -457,13 +457,14 @@ hc_status hc_norm(int64_t rows, int64_t d, int dtype, int center, float eps, con
  *   weight [d] float (in, may be NULL: ones)
  *   dweight, dbias [d] float (out, each may be NULL): sums over this call's rows,
  *   written and not added to; zeros for rows == 0
- *   workspace: hc_norm_backward_bytes(rows, d) bytes, 256-byte aligned, not shared
- *   with another call in flight; its contents need not be kept.
+ *   workspace: hc_norm_backward_bytes(rows, d, dtype) bytes, 256-byte aligned, not
+ *   shared with another call in flight; its contents need not be kept.  For few rows
+ *   that is 0, and the workspace is not looked at (NULL will do).
  * The sums run in a fixed order: the same call gives the same bits.  With
  * hc_mixes_pre_norm forward, x is hc_pre's y (hc_pre, hc_pre_restore) and dx is
  * the dy of hc_mixes_pre_backward.
  */
-size_t hc_norm_backward_bytes(int64_t rows, int64_t d);
+size_t hc_norm_backward_bytes(int64_t rows, int64_t d, int dtype);
 hc_status hc_norm_backward(int64_t rows, int64_t d, int dtype, int center, float eps,
                            const void *dy, const void *x, const float *weight, void *dx,
                            float *dweight, float *dbias, void *workspace, size_t workspace_bytes,

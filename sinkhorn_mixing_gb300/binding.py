@@ -67,7 +67,7 @@ def lib():
         L.hc_norm.argtypes = [i64, i64, i32, i32, f32, P, P, P, P, P]
         L.hc_norm_backward.argtypes = [i64, i64, i32, i32, f32, P, P, P, P, P, P, P,
                                        ctypes.c_size_t, P]
-        L.hc_norm_backward_bytes.argtypes = [i64, i64]
+        L.hc_norm_backward_bytes.argtypes = [i64, i64, i32]
         L.hc_norm_backward_bytes.restype = ctypes.c_size_t
         L.hc_embed.argtypes = [i64, i32, i64, i64, i32, i32, f32, P, P, P, P]
         L.hc_embed_backward.argtypes = [i64, i32, i64, i64, i32, i32, f32, i32, P, P, P, P,
@@ -621,8 +621,8 @@ def hc_norm(x, weight=None, bias=None, eps: float = 1e-20, center: bool = False,
 
 
 @functools.lru_cache(maxsize=256)
-def hc_norm_backward_bytes(rows: int, d: int) -> int:
-    return int(lib().hc_norm_backward_bytes(int(rows), int(d)))
+def hc_norm_backward_bytes(rows: int, d: int, dtype=torch.bfloat16) -> int:
+    return int(lib().hc_norm_backward_bytes(int(rows), int(d), _row_type(dtype, "rows")))
 
 
 def hc_norm_backward(dy, x, weight=None, eps: float = 1e-20, center: bool = False,
@@ -640,13 +640,15 @@ def hc_norm_backward(dy, x, weight=None, eps: float = 1e-20, center: bool = Fals
         dweight = _made(dweight, "dweight", (d,), _F32, dev, stream)
     if want_dbias or dbias is not None:
         dbias = _made(dbias, "dbias", (d,), _F32, dev, stream)
-    if workspace is None:
-        workspace = _made(None, "workspace", (hc_norm_backward_bytes(n, d),), _U8, dev, stream)
-    else:
+    if workspace is not None:
         _need(workspace, "workspace", _U8, dev)
+    else:
+        need = hc_norm_backward_bytes(n, d, dtype)   # 0 for few rows
+        if need:
+            workspace = _made(None, "workspace", (need,), _U8, dev, stream)
     _run("hc_norm_backward", dev, stream, n, d, code, bool(center), eps, dy.data_ptr(),
-         x.data_ptr(), wp, dx.data_ptr(), _ptr(dweight), _ptr(dbias), workspace.data_ptr(),
-         workspace.numel())
+         x.data_ptr(), wp, dx.data_ptr(), _ptr(dweight), _ptr(dbias), _ptr(workspace),
+         0 if workspace is None else workspace.numel())
     return dx, dweight, dbias
 
 

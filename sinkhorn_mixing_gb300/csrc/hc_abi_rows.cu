@@ -63,9 +63,9 @@ hc_status hc_norm(int64_t rows, int64_t d, int dtype, int center, float eps, con
         reinterpret_cast<cudaStream_t>(stream)));
 }
 
-size_t hc_norm_backward_bytes(int64_t rows, int64_t d) {
-    if (check_rows(rows, d) != HC_OK || rows == 0) return 0;
-    return hc::norm_backward_bytes(rows, d);
+size_t hc_norm_backward_bytes(int64_t rows, int64_t d, int dtype) {
+    if (check_rows(rows, d) != HC_OK || check_type(dtype) != HC_OK || rows == 0) return 0;
+    return hc::norm_backward_bytes(rows, d, dtype);
 }
 
 hc_status hc_norm_backward(int64_t rows, int64_t d, int dtype, int center, float eps,
@@ -87,10 +87,13 @@ hc_status hc_norm_backward(int64_t rows, int64_t d, int dtype, int center, float
         return from_cuda(e);
     }
     if ((st = ptrs_ok({dy, x, dx})) != HC_OK) return st;
-    if (workspace == nullptr || workspace_bytes < hc::norm_backward_bytes(rows, d))
-        return HC_ERR_INVALID_ARG;
-    if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return HC_ERR_MISALIGNED;
-    const Range rdx = rng(dx, bytes), rdy = rng(dy, bytes), rws = rng(workspace, workspace_bytes);
+    const size_t need = hc::norm_backward_bytes(rows, d, dtype);
+    if (need > 0) {
+        if (workspace == nullptr || workspace_bytes < need) return HC_ERR_INVALID_ARG;
+        if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return HC_ERR_MISALIGNED;
+    }
+    const Range rdx = rng(dx, bytes), rdy = rng(dy, bytes),
+                rws = need > 0 ? rng(workspace, workspace_bytes) : Range{0, 0};
     if ((dx != dy && overlap(rdx, rdy)) ||
         !disjoint({rdx, rw, rb, rws}, {rng(x, bytes), maybe(weight, par)}) ||
         !disjoint({rw, rb, rws}, {rdy}))

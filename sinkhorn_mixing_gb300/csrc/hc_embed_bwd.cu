@@ -24,6 +24,7 @@ constexpr int kMaxPiece = 32;
 // 4, 8, 16 and 32 a piece: 300 tokens of 1 x 1000 8.6, 10, 13, 17; 1,500 into 1,000
 // rows 15.7, 14.6, 13.7, 13.2 (21 with two); 4,096 of 4 x 5120 122, 106, 101 from 8 on.
 int piece_tokens(int64_t n, int64_t d) {
+    if (n <= 8) return 8;  // one piece holds them all: nothing to join
     const int64_t slices = (d + 1023) / 1024;
     int c = kMaxPiece;
     while (c > 4 && n * slices < (int64_t)c * 256) c /= 2;
@@ -306,7 +307,7 @@ cudaError_t launch(const EmbedBackward &p, const DeviceInfo &di, cudaStream_t s)
                           (const uint32_t *)o.start, (const uint32_t *)o.end,
                           reinterpret_cast<const uint4 *>(p.dx), table,
                           reinterpret_cast<float4 *>(w.part));
-    if (e != cudaSuccess) return e;
+    if (e != cudaSuccess || p.n <= c) return e;  // no id has more tokens than a piece
     // ids with more than c tokens: no more than windows, and few of them as a rule
     const int64_t parts = std::min<int64_t>((nv + 31) / 32, 1024);
     const int64_t joins = std::min(windows, std::max<int64_t>(2432 / parts, 16));

@@ -29,6 +29,22 @@ int64_t max_parts(int64_t rows, int64_t d) {
     return rows < m ? rows : m;
 }
 
+// So few rows that one block has them all: it writes dweight and dbias itself, and the call
+// needs neither partial sums nor a second launch (18 us of the host's time through Python
+// become 14).  A block takes about 1.2 us for the rows it has at a time; many blocks and the
+// second launch take 4 to 5 us in all.
+constexpr int kAloneSteps = 3;
+
+// Vectors of a row that a thread has.
+int ring_vecs(int64_t nv) {
+    // four vectors a thread, or five, where a warp has the row; three in blocks where they do
+    return row_vecs(nv, kRingThreads, nv <= 160 ? 5 : nv <= 3 * kRingThreads ? 3 : 4);
+}
+bool one_block(int64_t rows, int64_t nv) {
+    return nv <= 4 * kRingThreads &&
+           rows <= (int64_t)kAloneSteps * row_plan(nv, ring_vecs(nv), 1, 1).groups;
+}
+
 size_t align256(size_t b) { return (b + 255) & ~(size_t)255; }
 
 template <int E>
@@ -168,7 +184,8 @@ __global__ void __launch_bounds__(BLOCK ? kRingThreads : 256, BLOCK ? 1 : V < 3 
         at = at + 1 == kStages ? 0 : at + 1;
     }
     const int64_t d = (int64_t)nv * E;
-    part_w += blockIdx.x * d, part_b += blockIdx.x * d;
+    if (part_w != nullptr) part_w += blockIdx.x * d;
+    if (DB && part_b != nullptr) part_b += blockIdx.x * d;
     float sw[E], sb[E];
     if (BLOCK) {
 #pragma unroll
@@ -179,8 +196,8 @@ __global__ void __launch_bounds__(BLOCK ? kRingThreads : 256, BLOCK ? 1 : V < 3 
                     unpack2(aw[i][e], sw[2 * e], sw[2 * e + 1]);
                     if (DB) unpack2(ab[DB ? i : 0][e], sb[2 * e], sb[2 * e + 1]);
                 }
-                put_sums<E>(part_w, l + i * lanes, sw);
-                if (DB) put_sums<E>(part_b, l + i * lanes, sb);
+                if (part_w != nullptr) put_sums<E>(part_w, l + i * lanes, sw);
+                if (DB && part_b != nullptr) put_sums<E>(part_b, l + i * lanes, sb);
             }
         return;
     }
@@ -217,8 +234,8 @@ __global__ void __launch_bounds__(BLOCK ? kRingThreads : 256, BLOCK ? 1 : V < 3 
             a += buf[q * d + c];
             if (DB) b += buf[(8 + q) * d + c];
         }
-        part_w[c] = a;
-        if (DB) part_b[c] = b;
+        if (part_w != nullptr) part_w[c] = a;
+        if (DB && part_b != nullptr) part_b[c] = b;
     }
 }
 
@@ -499,16 +516,18 @@ cudaError_t launch_ring(const RowNormBackward &p, const RowPlan &plan, int64_t n
     constexpr int most = kStages * (2 * V + (CENTER ? 1 : 0)) * (BLOCK ? kRingThreads : 256) * 16;
     cudaError_t e = allow_smem(smem, reinterpret_cast<const void *>(kernel), most, di);
     if (e != cudaSuccess) return e;
+    const bool alone = one_block(p.rows, nv);
     const int64_t want = (p.rows + plan.groups - 1) / plan.groups,
                   cap = (int64_t)di.sms * blocks_per_sm(kernel, regs, plan),
                   most_parts = max_parts(p.rows, p.d);
-    const int parts = (int)std::min(want, std::min(cap, most_parts));
-    float *part_w = reinterpret_cast<float *>(p.ws), *part_b = part_w + (size_t)parts * p.d;
+    const int parts = alone ? 1 : (int)std::min(want, std::min(cap, most_parts));
+    float *part_w = alone ? p.dweight : reinterpret_cast<float *>(p.ws);
+    float *part_b = alone ? p.dbias : part_w + (size_t)parts * p.d;
     e = launch_overlapped(kernel, dim3((unsigned)parts), dim3(plan.threads), plan.ring, s, p.rows,
                           (int)nv, plan.lg, p.eps, static_cast<const uint4 *>(p.dy),
                           static_cast<const uint4 *>(p.x), p.weight, static_cast<uint4 *>(p.dx),
                           part_w, part_b);
-    return e != cudaSuccess ? e : launch_sums(p, parts, part_w, part_b, s);
+    return alone || e != cudaSuccess ? e : launch_sums(p, parts, part_w, part_b, s);
 }
 
 template <int DT, bool CENTER, bool DB, int V>
@@ -522,9 +541,7 @@ cudaError_t launch_ring(const RowNormBackward &p, int64_t nv, const DeviceInfo &
 template <int DT, bool CENTER, bool DB>
 cudaError_t launch_ring(const RowNormBackward &p, int64_t nv, const DeviceInfo &di,
                         cudaStream_t s) {
-    // four vectors a thread, or five, where a warp has the row; three in blocks where they do
-    const int most = nv <= 160 ? 5 : nv <= 3 * kRingThreads ? 3 : 4;
-    switch (row_vecs(nv, kRingThreads, most)) {
+    switch (ring_vecs(nv)) {
         case 1: return launch_ring<DT, CENTER, DB, 1>(p, nv, di, s);
         case 2: return launch_ring<DT, CENTER, DB, 2>(p, nv, di, s);
         case 3: return launch_ring<DT, CENTER, DB, 3>(p, nv, di, s);
@@ -581,7 +598,8 @@ cudaError_t launch(const RowNormBackward &p, const DeviceInfo &di, cudaStream_t 
 
 }  // namespace
 
-size_t norm_backward_bytes(int64_t rows, int64_t d) {
+size_t norm_backward_bytes(int64_t rows, int64_t d, int dtype) {
+    if (one_block(rows, d * row_type_bytes(dtype) / 16)) return 0;
     return align256((size_t)rows * 16) + (size_t)max_parts(rows, d) * (size_t)d * 8;
 }
 

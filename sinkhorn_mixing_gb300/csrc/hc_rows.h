@@ -33,7 +33,7 @@ struct RowNormBackward {
     float *dweight, *dbias;  // each may be null
     uint8_t *ws;
 };
-size_t norm_backward_bytes(int64_t rows, int64_t d);
+size_t norm_backward_bytes(int64_t rows, int64_t d, int dtype);
 cudaError_t launch_norm_backward(const RowNormBackward &p, const DeviceInfo &di, cudaStream_t s);
 
 // rows of a table into the copies of a stream (hc_embed.cu)

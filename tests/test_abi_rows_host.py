@@ -46,9 +46,9 @@ def norm(L, rows=4, d=64, dtype=BF16, center=0, eps=1e-6, **change):
     return L.hc_norm(rows, d, dtype, center, eps, *pointers(("x", "w", "b", "y"), change), None)
 
 
-def norm_bwd(L, rows=4, d=64, dtype=BF16, center=0, eps=1e-6, wsb=None, **change):
+def norm_bwd(L, rows=4096, d=64, dtype=BF16, center=0, eps=1e-6, wsb=None, **change):
     p = pointers(("dy", "x", "w", "dx", "dw", "db", "ws"), change)
-    wsb = L.hc_norm_backward_bytes(4, 64) if wsb is None else wsb
+    wsb = L.hc_norm_backward_bytes(4096, 64, BF16) if wsb is None else wsb
     return L.hc_norm_backward(rows, d, dtype, center, eps, *p, wsb, None)
 
 
@@ -96,10 +96,18 @@ def test_norm(L):
 
 
 def test_norm_backward(L):
-    need = L.hc_norm_backward_bytes(4, 64)
-    assert need > 0 and L.hc_norm_backward_bytes(0, 64) == 0 == L.hc_norm_backward_bytes(4, 12)
-    # wide rows and few rows need no more than their share
-    assert L.hc_norm_backward_bytes(1 << 20, 1 << 24) < 1 << 36
+    need = L.hc_norm_backward_bytes(4096, 64, BF16)
+    assert need > 0 and L.hc_norm_backward_bytes(0, 64, BF16) == 0
+    assert L.hc_norm_backward_bytes(4096, 12, BF16) == 0 == L.hc_norm_backward_bytes(4096, 64, 3)
+    # wide rows need no more than their share, few rows none
+    assert L.hc_norm_backward_bytes(1 << 20, 1 << 24, F32) < 1 << 36
+    for dtype in (BF16, F16, F32):
+        assert L.hc_norm_backward_bytes(2, 5120, dtype) == 0
+        assert L.hc_norm_backward_bytes(20, 5120, dtype) > 0
+        assert L.hc_norm_backward_bytes(1, 65536, dtype) > 0
+    if no_gpu():
+        assert norm_bwd(L, rows=2, ws=NULL, wsb=0) == CUDA
+        assert norm_bwd(L, rows=2, ws=fake(0, 8)) == CUDA
     for k in ("dy", "x", "dx", "ws"):
         assert norm_bwd(L, **{k: NULL}) == INVALID
     for k in ("dy", "x", "w", "dx", "dw", "db"):

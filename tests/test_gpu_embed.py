@@ -104,7 +104,7 @@ SIZES = [(1, 8, 1), (2, 8, 2), (31, 64, 7), (33, 5120, 40), (64, 1032, 511), (65
 
 
 # either side of where the tokens are put in order another way
-SIZES += [(4095, 16, 4095), (4096, 16, 70000), (4097, 8, 3), (8191, 24, 300), (16400, 16, 1 << 19),
+SIZES += [(7, 24, 3), (8, 24, 3), (9, 24, 3), (4095, 16, 4095), (4096, 16, 70000), (4097, 8, 3), (8191, 24, 300), (16400, 16, 1 << 19),
           (65535, 8, 131072), (65536, 16, 97), (65537, 8, 1000)]
 
 

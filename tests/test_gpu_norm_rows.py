@@ -248,6 +248,25 @@ def test_empty_and_shapes(hc):
     assert dx.shape == (2, 12, 64)
 
 
+@pytest.mark.parametrize("d", [8, 64, 128, 520, 1000, 1272, 1288, 5120, 16384])
+def test_few_rows(hc, d):
+    """The most rows that one block has alone (their sums need no workspace), and one more."""
+    rows = 1
+    while hc.hc_norm_backward_bytes(rows + 1, d) == 0:
+        rows += 1
+    for center in (False, True):
+        for n in (rows, rows + 1):
+            x, dy, w, b = case(n, d, BF16, 13)
+            got = check_backward(hc, dy, x, w, center, 1e-5)
+            xd, dyd, wd = dev(x, dy, w)
+            for k in ((True, False), (False, True), (False, False)):
+                out = hc.hc_norm_backward(dyd, xd, wd, eps=1e-5, center=center, want_dweight=k[0],
+                                          want_dbias=k[1])
+                assert torch.equal(out[0], got[0])
+                for a, c, want in zip(out[1:], got[1:], k):
+                    assert (a is not None) == want and (a is None or torch.equal(a, c))
+
+
 @pytest.mark.parametrize("d", [64, 20480])
 def test_long_tensors(hc, d):
     """More than 2^31 channels: the last rows are where 32-bit offsets would fail."""
@@ -328,8 +347,9 @@ def test_refusals(hc):
         hc.hc_norm_backward(x.float(), x)
     with pytest.raises(ValueError):
         hc.hc_norm_backward(x[:4], x)
+    many = torch.zeros(800, 1000, dtype=BF16, device="cuda")
     with pytest.raises(hc.HcError, match="INVALID"):
-        hc.hc_norm_backward(x, x, workspace=torch.empty(0, dtype=torch.uint8, device="cuda"))
+        hc.hc_norm_backward(many, many, workspace=torch.empty(0, dtype=torch.uint8, device="cuda"))
 
 
 @pytest.mark.parametrize("dtype", TYPES)
