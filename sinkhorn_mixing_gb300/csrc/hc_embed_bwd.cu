@@ -1,5 +1,5 @@
 // hc_embed_bwd.cu -- the gradient of an embedding table:
-//   dtable[v, :] (+)= scale * sum over the tokens t with id_t = v, over the copies j, of dx[t, j, :].
+//   dtable[v, :] (+)= scale * (sum over tokens t with id_t = v, over copies j, of dx[t, j, :]).
 //
 // Tokens are put in order of their ids, those of one id by position, so that a sum's
 // order depends on nothing but the ids.  The ordered tokens are cut into windows of
@@ -8,6 +8,9 @@
 // one piece, and its sum is written to the table at once.  Longer ones leave a row of
 // partial sums per piece, which k_embed_join adds up in order.  So every gradient
 // is read once and a frequent id's sum is spread over the GPU.
+//
+// An HBM stream: 65,536 tokens of 4 x 5120 into 131,072 fp32 rows (5.37 GB) 826 us, 6.5 TB/s,
+// 96% of a copy's rate; 16,384 497 us (6.8 TB/s); added to those rows 570 us (6.1 TB/s).
 #include <algorithm>
 
 #include "hc_embed_order.h"
@@ -63,7 +66,7 @@ Workspace layout(uint8_t *base, int64_t n, int64_t d, int64_t vocab) {
     return w;
 }
 
-// Eight channels of a row of the table's gradient lie in ROW16 vectors.
+// Eight channels of a row of the table's gradient lie in so many 16-byte vectors.
 template <int DT>
 constexpr int kRow16 = 8 / RowVec<DT>::E;
 
@@ -299,11 +302,10 @@ cudaError_t launch(const EmbedBackward &p, const DeviceInfo &di, cudaStream_t s)
     // 5120 into 131,072 fp32 rows: 498 us, with 16 blocks 502, with 4 about 520)
     const int64_t warps = slices * (threads / 32),
                   units = (p.vocab + 31) / 32 * clear_parts(p.d * row_type_bytes(p.dtype) / 16);
-    const int64_t clear =
-        ADD ? 0 : std::min((units + warps - 1) / warps, (int64_t)di.sms * 64);
-    e = launch_overlapped(kernel, dim3((unsigned)(windows + clear), (unsigned)slices), dim3(threads),
-                          (size_t)per_thread * threads, s, p.n, nv, windows, c, p.vocab, p.scale,
-                          sorted, o.count, w.longs, (const uint32_t *)o.present,
+    const int64_t clear = ADD ? 0 : std::min((units + warps - 1) / warps, (int64_t)di.sms * 64);
+    e = launch_overlapped(kernel, dim3((unsigned)(windows + clear), (unsigned)slices),
+                          dim3(threads), (size_t)per_thread * threads, s, p.n, nv, windows, c,
+                          p.vocab, p.scale, sorted, o.count, w.longs, (const uint32_t *)o.present,
                           (const uint32_t *)o.start, (const uint32_t *)o.end,
                           reinterpret_cast<const uint4 *>(p.dx), table,
                           reinterpret_cast<float4 *>(w.part));
@@ -311,8 +313,8 @@ cudaError_t launch(const EmbedBackward &p, const DeviceInfo &di, cudaStream_t s)
     // ids with more than c tokens: no more than windows, and few of them as a rule
     const int64_t parts = std::min<int64_t>((nv + 31) / 32, 1024);
     const int64_t joins = std::min(windows, std::max<int64_t>(2432 / parts, 16));
-    return launch_overlapped(&k_embed_join<DT, ADD>, dim3((unsigned)joins, (unsigned)parts), dim3(256), 0,
-                             s, nv, p.scale, (const uint32_t *)o.count,
+    return launch_overlapped(&k_embed_join<DT, ADD>, dim3((unsigned)joins, (unsigned)parts),
+                             dim3(256), 0, s, nv, p.scale, (const uint32_t *)o.count,
                              (const uint4 *)w.longs, (const float4 *)w.part, table);
 }
 

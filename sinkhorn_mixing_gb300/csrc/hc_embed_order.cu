@@ -283,7 +283,8 @@ cudaError_t order(int64_t n, int64_t vocab, const ID *ids, const TokenOrder &o, 
         e = sort_pass(n, FromPairs{o.sorted[to]}, i * digit, bins, o, o.sorted[to ^ 1], 0, s);
     if (e != cudaSuccess) return e;
     return launch_overlapped(&k_embed_places, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, n,
-                             (uint32_t)vocab, (const uint2 *)o.sorted[0], o.present, o.start, o.end);
+                             (uint32_t)vocab, (const uint2 *)o.sorted[0], o.present, o.start,
+                             o.end);
 }
 
 }  // namespace

@@ -1,5 +1,5 @@
-"""Refusals of hc_norm, hc_embed and their gradients on the host: bad arguments return the documented
-status before any CUDA call (the device pointers are fake addresses that nothing dereferences)."""
+"""Refusals of hc_norm, hc_embed and their gradients on the host: bad arguments return the
+documented status before any CUDA call (the device pointers are fake addresses that nothing dereferences)."""
 import ctypes
 import math
 import os
