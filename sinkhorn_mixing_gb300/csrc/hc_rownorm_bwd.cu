@@ -60,10 +60,13 @@ __device__ __forceinline__ void put_sums(float *row, int64_t v, const float a[E]
 // the sums over the block's rows stay in its registers.  DB: dbias as well.
 //
 // A row takes one round of sums: x^2 and g x or, for layer norm, x - p, (x - p)^2, g
-// and g (x - p) (see row_guess).  x and dy are held packed from the sums to the outputs.
+// and g (x - p) (see row_guess).  Behind the sums x and dy are read from shared memory
+// again, or held packed where registers are left: RMS 292 us held, 296 read again; 16,384
+// x 16384, four vectors a thread, x held 233, both 263, none 272; layer norm's sums leave
+// none (302 us there, 435 held).  Warps with rows of their own hold both.
 //
-// 65,536 x 5120 in bf16 (2.01 GB) 293 us, 6.9 TB/s: a copy's rate.  Layer norm with a bias 378 to
-// 388 us: 14 warps an SM (128 registers) issue in 60% of the slots.  131,072 x 128 20 us (5.0
+// 65,536 x 5120 in bf16 (2.01 GB) 292 us, 6.9 TB/s: a copy's rate.  Layer norm with a bias 377 us:
+// 14 warps an SM (128 registers) issue in 60% of the slots.  131,072 x 128 20 us (5.0
 // TB/s), 50,000 x 2048 in fp32 187 us (6.6 TB/s), the launch of k_norm_sum within.
 template <int DT, bool CENTER, bool DB, int V, bool BLOCK>
 __global__ void __launch_bounds__(BLOCK ? kRingThreads : 256,
@@ -72,6 +75,7 @@ __global__ void __launch_bounds__(BLOCK ? kRingThreads : 256,
                     const uint4 *__restrict__ x0, const float *__restrict__ w, uint4 *dx0,
                     float *__restrict__ part_w, float *__restrict__ part_b) {
     constexpr int E = RowVec<DT>::E, NS = CENTER ? 4 : 2, SLOTS = 2 * V + (CENTER ? 1 : 0);
+    constexpr bool HOLD_X = !BLOCK || !CENTER, HOLD_DY = !BLOCK || (!CENTER && V < 4);
     extern __shared__ uint4 ring[];
     __shared__ __align__(16) float red[2][NS][32];
     if (BLOCK) clear_red(&red[0][0][0], 2 * NS * 32);
@@ -120,18 +124,24 @@ __global__ void __launch_bounds__(BLOCK ? kRingThreads : 256,
         float s[NS], mu = 0.0f, delta = 0.0f, var;
         uint64_t f[E / 2], g[E / 2];
         if (CENTER && in) mu = row_guess<DT>(*slot(at, 2, 0));
-        uint4 xr[V], gr[V];
+        uint4 xr[HOLD_X ? V : 1], gr[HOLD_DY ? V : 1];
 #pragma unroll
         for (int i = 0; i < V; ++i)
-            if (in && l + i * lanes < nv) xr[i] = *slot(at, 0, i), gr[i] = *slot(at, 1, i);
+            if (in && l + i * lanes < nv) {
+                if (HOLD_X) xr[HOLD_X ? i : 0] = *slot(at, 0, i);
+                if (HOLD_DY) gr[HOLD_DY ? i : 0] = *slot(at, 1, i);
+            }
+        auto read = [&](int i) {
+            row_pairs<DT>(HOLD_X ? xr[HOLD_X ? i : 0] : *slot(at, 0, i), f);
+            row_pairs<DT>(HOLD_DY ? gr[HOLD_DY ? i : 0] : *slot(at, 1, i), g);
+        };
         auto sums = [&]() {
             uint64_t sq = 0, sgc = 0, sg = 0, sc = 0;
             const uint64_t minus_p = pack2(-mu, -mu);
 #pragma unroll
             for (int i = 0; i < V; ++i)
                 if (in && l + i * lanes < nv) {
-                    row_pairs<DT>(xr[i], f);
-                    row_pairs<DT>(gr[i], g);
+                    read(i);
 #pragma unroll
                     for (int e = 0; e < E / 2; ++e) {
                         const uint64_t c = CENTER ? fadd2(f[e], minus_p) : f[e];
@@ -171,8 +181,7 @@ __global__ void __launch_bounds__(BLOCK ? kRingThreads : 256,
 #pragma unroll
         for (int i = 0; i < V; ++i)
             if (in && l + i * lanes < nv) {
-                row_pairs<DT>(xr[i], f);
-                row_pairs<DT>(gr[i], g);
+                read(i);
 #pragma unroll
                 for (int e = 0; e < E / 2; ++e) {
                     const uint64_t h = fmul2(CENTER ? fadd2(f[e], minus_mu) : f[e], rr);
