@@ -49,8 +49,9 @@
  *     launch, so they may start while the kernel enqueued just before them in
  *     the stream is still running.  They read every activation only after that
  *     kernel has completed, but the decode kernel starts copying its slice of
- *     w_mix at once: w_mix must not be written by the kernel enqueued immediately before the call (weights written by an
- *     earlier kernel, a copy or a memset in between are fine).
+ *     w_mix at once: w_mix must not be written by the kernel enqueued
+ *     immediately before the call (weights written by an earlier kernel, a copy
+ *     or a memset in between are fine).
  */
 #ifndef HCMIX_H
 #define HCMIX_H
