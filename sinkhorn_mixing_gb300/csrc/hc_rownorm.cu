@@ -121,18 +121,26 @@ __global__ void __launch_bounds__(BLOCK ? kRingThreads : 256, BLOCK ? 1 : V < 3 
 // output (from L1 or L2 after the first time).  8,192 x 20480 in bf16 114 us (5.9
 // TB/s), layer norm with a bias 143 us; in one block's shared memory such a row left
 // room for no other block, 117 and 183 us.
+//
+// A sum of numbers around a far mean is rounded to K u |mean|, which may be worth more
+// than the row's deviation, and so is the mean that comes of it: with the squares about it
+// goes a second sum, of what its numbers differ from it by (exact differences, as both are
+// of one size), and takes the rest off (fp32, mean 1000, deviation 0.05: y is off by 1e-6 in
+// place of 2e-3).  With that sum five blocks fit an SM, 157 us, six as it is bounded.  One
+// round of sums about a guess, as k_norm has them, lost in spite of one reading less (160
+// us): no row is copied ahead here, and all of its loads wait for the guess.
 template <int DT, bool CENTER, int THREADS>
-__global__ void __launch_bounds__(THREADS)
+__global__ void __launch_bounds__(THREADS, CENTER && THREADS == 256 ? 6 : 0)
     k_norm_wide(int64_t rows, int64_t nv, float eps, const uint4 *x0, const float *__restrict__ w,
                 const float *__restrict__ b, uint4 *y0) {
-    constexpr int E = RowVec<DT>::E;
-    __shared__ __align__(16) float red[2][1][32];
-    clear_red(&red[0][0][0], 64);
+    constexpr int E = RowVec<DT>::E, NS = CENTER ? 2 : 1;
+    __shared__ __align__(16) float red[3][32];
+    clear_red(&red[0][0], 96);
     griddep_wait_then_release();
     const float inv_d = 1.0f / (float)(nv * E);
     for (int64_t t = blockIdx.x; t < rows; t += gridDim.x) {
         const uint4 *x = x0 + t * nv;
-        float mu = 0.0f, f[E];
+        float mu = 0.0f, delta = 0.0f, var, f[E];
         if (CENTER) {
             float s[1] = {0.0f};
             for (int64_t v = threadIdx.x; v < nv; v += blockDim.x) {
@@ -140,24 +148,35 @@ __global__ void __launch_bounds__(THREADS)
 #pragma unroll
                 for (int e = 0; e < E; ++e) s[0] += f[e];
             }
-            block_sum<1>(s, red[0]);
+            block_sum<1>(s, red);
             mu = s[0] * inv_d;
         }
-        float q[1] = {0.0f};
+        float q[NS];  // squares about mu and, in layer norm, what the mean differs from mu by
+        q[0] = q[NS - 1] = 0.0f;
         for (int64_t v = threadIdx.x; v < nv; v += blockDim.x) {
             RowVec<DT>::get(x[v], f);
 #pragma unroll
-            for (int e = 0; e < E; ++e) q[0] = fmaf(f[e] - mu, f[e] - mu, q[0]);
+            for (int e = 0; e < E; ++e) {
+                const float c = f[e] - mu;
+                q[0] = fmaf(c, c, q[0]);
+                if (CENTER) q[NS - 1] += c;
+            }
         }
-        block_sum<1>(q, red[1]);
-        const float r = rsqrtf(fmaf(q[0], inv_d, eps));
+        block_sum<NS>(q, red + 1);
+        var = q[0] * inv_d;
+        if (CENTER) {
+            delta = q[NS - 1] * inv_d;
+            var = row_variance(var, delta);
+        }
+        const float r = rsqrtf(var + eps), minus_dr = r == 0.0f ? 0.0f : -delta * r;
         for (int64_t v = threadIdx.x; v < nv; v += blockDim.x) {
             float wv[E], bv[E];
             RowVec<DT>::get(x[v], f);
             row_params<E>(w, v, 1.0f, wv);
             row_params<E>(b, v, 0.0f, bv);
 #pragma unroll
-            for (int e = 0; e < E; ++e) f[e] = fmaf((f[e] - mu) * r, wv[e], bv[e]);
+            for (int e = 0; e < E; ++e)
+                f[e] = fmaf(CENTER ? fmaf(f[e] - mu, r, minus_dr) : f[e] * r, wv[e], bv[e]);
             y0[t * nv + v] = RowVec<DT>::set(f);
         }
         __syncthreads();  // red is used again by the next row
