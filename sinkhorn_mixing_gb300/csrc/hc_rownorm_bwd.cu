@@ -44,7 +44,8 @@ bool one_block(int64_t rows, int64_t nv) {
            rows <= (int64_t)kAloneSteps * row_plan(nv, ring_vecs(nv), 1, 1).groups;
 }
 
-size_t align256(size_t b) { return (b + 255) & ~(size_t)255; }
+// What k_norm_stats leaves of a row, a float4 and a float.
+size_t stats_bytes(int64_t rows) { return ((size_t)rows * 20 + 255) & ~(size_t)255; }
 
 template <int E>
 __device__ __forceinline__ void put_sums(float *row, int64_t v, const float a[E]) {
@@ -65,7 +66,11 @@ __device__ __forceinline__ void put_sums(float *row, int64_t v, const float a[E]
 // x 16384, four vectors a thread, x held 233, both 263, none 272; layer norm's sums leave
 // none (302 us there, 435 held).  Warps with rows of their own hold both.
 //
-// 65,536 x 5120 in bf16 (2.01 GB) 292 us, 6.9 TB/s: a copy's rate.  Layer norm with a bias 377 us:
+// The mean is p + delta and is not rounded to one number: h = (x - p) r - delta r, whose x - p
+// is exact where p is near x (fp32, mean 1000, deviation 0.05: dw off by 3e-8 of 0.2, with one
+// number 5e-5).
+//
+// 65,536 x 5120 in bf16 (2.01 GB) 292 us, 6.9 TB/s: a copy's rate.  Layer norm with a bias 379 us:
 // 14 warps an SM (128 registers) issue in 60% of the slots.  131,072 x 128 20 us (5.0
 // TB/s), 50,000 x 2048 in fp32 187 us (6.6 TB/s), the launch of k_norm_sum within.
 template <int DT, bool CENTER, bool DB, int V, bool BLOCK>
@@ -175,8 +180,8 @@ __global__ void __launch_bounds__(BLOCK ? kRingThreads : 256,
         const float c1 = CENTER ? s[NS - 1] * inv_d : 0.0f;
         const float gc = CENTER ? fmaf(-delta, c1, s[1] * inv_d) : s[1] * inv_d;
         const float c2 = r == 0.0f ? 0.0f : gc * r;
-        const float minus_mean = -(mu + delta), rc1 = -c1 * r, rc2 = -c2 * r;
-        const uint64_t rr = pack2(r, r), minus_mu = pack2(minus_mean, minus_mean),
+        const float rc1 = -c1 * r, rc2 = -c2 * r, dr = r == 0.0f ? 0.0f : -delta * r;
+        const uint64_t rr = pack2(r, r), minus_mu = pack2(-mu, -mu), minus_dr = pack2(dr, dr),
                        minus_rc1 = pack2(rc1, rc1), minus_rc2 = pack2(rc2, rc2);
 #pragma unroll
         for (int i = 0; i < V; ++i)
@@ -184,7 +189,8 @@ __global__ void __launch_bounds__(BLOCK ? kRingThreads : 256,
                 read(i);
 #pragma unroll
                 for (int e = 0; e < E / 2; ++e) {
-                    const uint64_t h = fmul2(CENTER ? fadd2(f[e], minus_mu) : f[e], rr);
+                    const uint64_t h = CENTER ? ffma2_of(fadd2(f[e], minus_mu), rr, minus_dr)
+                                              : fmul2(f[e], rr);
                     ffma2(aw[i][e], g[e], h);
                     if (DB) ab[DB ? i : 0][e] = fadd2(ab[DB ? i : 0][e], g[e]);
                     const uint64_t gw = fmul2(g[e], wk[i][e]);
@@ -337,8 +343,8 @@ __global__ void __launch_bounds__(kRingThreads)
         const float c1 = CENTER ? s[NS - 1] * inv_d : 0.0f;
         const float gc = CENTER ? fmaf(-delta, c1, s[1] * inv_d) : s[1] * inv_d;
         const float c2 = r == 0.0f ? 0.0f : gc * r;
-        const float minus_mean = -(mu + delta), rc1 = -c1 * r, rc2 = -c2 * r;
-        const uint64_t rr = pack2(r, r), minus_mu = pack2(minus_mean, minus_mean),
+        const float rc1 = -c1 * r, rc2 = -c2 * r, dr = r == 0.0f ? 0.0f : -delta * r;
+        const uint64_t rr = pack2(r, r), minus_mu = pack2(-mu, -mu), minus_dr = pack2(dr, dr),
                        minus_rc1 = pack2(rc1, rc1), minus_rc2 = pack2(rc2, rc2);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
@@ -348,7 +354,8 @@ __global__ void __launch_bounds__(kRingThreads)
             if (v < nv) {
 #pragma unroll
                 for (int e = 0; e < E / 2; ++e) {
-                    const uint64_t h = fmul2(CENTER ? fadd2(f[e], minus_mu) : f[e], rr);
+                    const uint64_t h = CENTER ? ffma2_of(fadd2(f[e], minus_mu), rr, minus_dr)
+                                              : fmul2(f[e], rr);
                     ffma2(aw[i][e], g[e], h);
                     if (DB) ab[DB ? i : 0][e] = fadd2(ab[DB ? i : 0][e], g[e]);
                     const uint64_t gw = fmul2(g[e], wk[e]);
@@ -376,20 +383,22 @@ __global__ void __launch_bounds__(kRingThreads)
     }
 }
 
-// Any width, first part: a row's mean, r, mean(g) and mean(g h).
+// Any width, first part: a row's mean as its sum gives it, r, mean(g) and mean(g h), and, of layer
+// norm, the number that makes (x - mean) r h (see k_norm_wide).  Six blocks an SM: layer norm's
+// sums in 16 bits took 44 registers, 4,096 x 20488 in bf16 175 us in place of 170.
 template <int DT, bool CENTER>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, CENTER && DT != HC_F32 ? 6 : 0)
     k_norm_stats(int64_t rows, int64_t nv, float eps, const uint4 *__restrict__ dy0,
                  const uint4 *__restrict__ x0, const float *__restrict__ w,
-                 float4 *__restrict__ stats) {
-    constexpr int E = RowVec<DT>::E;
+                 float4 *__restrict__ stats, float *__restrict__ rest) {
+    constexpr int E = RowVec<DT>::E, NS = CENTER ? 2 : 1;
     __shared__ __align__(16) float red[3][2][32];
     clear_red(&red[0][0][0], 192);
     griddep_wait_then_release();
     const float inv_d = 1.0f / (float)(nv * E);
     for (int64_t t = blockIdx.x; t < rows; t += gridDim.x) {
         const uint4 *x = x0 + t * nv, *dy = dy0 + t * nv;
-        float mu = 0.0f, f[E], g[E], wv[E];
+        float mu = 0.0f, delta = 0.0f, var, f[E], g[E], wv[E];
         if (CENTER) {
             float s[1] = {0.0f};
             for (int64_t v = threadIdx.x; v < nv; v += blockDim.x) {
@@ -400,14 +409,24 @@ __global__ void __launch_bounds__(256)
             block_sum<1>(s, red[0]);
             mu = s[0] * inv_d;
         }
-        float q[1] = {0.0f};
+        float q[NS];
+        q[0] = q[NS - 1] = 0.0f;
         for (int64_t v = threadIdx.x; v < nv; v += blockDim.x) {
             RowVec<DT>::get(x[v], f);
 #pragma unroll
-            for (int e = 0; e < E; ++e) q[0] = fmaf(f[e] - mu, f[e] - mu, q[0]);
+            for (int e = 0; e < E; ++e) {
+                const float a = f[e] - mu;
+                q[0] = fmaf(a, a, q[0]);
+                if (CENTER) q[NS - 1] += a;
+            }
         }
-        block_sum<1>(q, red[1]);
-        const float r = rsqrtf(fmaf(q[0], inv_d, eps));
+        block_sum<NS>(q, red[1]);
+        var = q[0] * inv_d;
+        if (CENTER) {
+            delta = q[NS - 1] * inv_d;
+            var = row_variance(var, delta);
+        }
+        const float r = rsqrtf(var + eps), minus_dr = r == 0.0f ? 0.0f : -delta * r;
         float c[2] = {0.0f, 0.0f};
         for (int64_t v = threadIdx.x; v < nv; v += blockDim.x) {
             RowVec<DT>::get(x[v], f);
@@ -417,23 +436,25 @@ __global__ void __launch_bounds__(256)
             for (int e = 0; e < E; ++e) {
                 const float ge = g[e] * wv[e];
                 c[0] += ge;
-                c[1] = fmaf(ge, (f[e] - mu) * r, c[1]);
+                c[1] = fmaf(ge, CENTER ? fmaf(f[e] - mu, r, minus_dr) : f[e] * r, c[1]);
             }
         }
         block_sum<2>(c, red[2]);
-        if (threadIdx.x == 0)
+        if (threadIdx.x == 0) {
             stats[t] = make_float4(mu, r, CENTER ? c[0] * inv_d : 0.0f, c[1] * inv_d);
+            if (CENTER) rest[t] = minus_dr;
+        }
         __syncthreads();  // red is used again by the next row
     }
 }
 
 // Second part: a block has 128 vectors of a run of rows.
-template <int DT>
+template <int DT, bool CENTER>
 __global__ void __launch_bounds__(128)
     k_norm_grad(int64_t rows, int64_t nv, int64_t run, const uint4 *dy,
                 const uint4 *__restrict__ x, const float *__restrict__ w,
-                const float4 *__restrict__ stats, uint4 *dx, float *__restrict__ dw,
-                float *__restrict__ db) {
+                const float4 *__restrict__ stats, const float *__restrict__ rest, uint4 *dx,
+                float *__restrict__ dw, float *__restrict__ db) {
     constexpr int E = RowVec<DT>::E;
     griddep_wait_then_release();
     const int64_t v = (int64_t)blockIdx.x * 128 + threadIdx.x;
@@ -445,12 +466,13 @@ __global__ void __launch_bounds__(128)
     for (int e = 0; e < E; ++e) aw[e] = ab[e] = 0.0f;
     for (int64_t t = t0; t < t1; ++t) {
         const float4 st = __ldg(stats + t);
+        const float minus_dr = CENTER ? __ldg(rest + t) : 0.0f;
         float f[E], g[E];
         RowVec<DT>::get(x[t * nv + v], f);
         RowVec<DT>::get(dy[t * nv + v], g);
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-            const float h = (f[e] - st.x) * st.y;
+            const float h = CENTER ? fmaf(f[e] - st.x, st.y, minus_dr) : f[e] * st.y;
             aw[e] = fmaf(g[e], h, aw[e]);
             ab[e] += g[e];
             f[e] = (fmaf(g[e], wv[e], -st.z) - h * st.w) * st.y;
@@ -589,15 +611,17 @@ cudaError_t launch(const RowNormBackward &p, const DeviceInfo &di, cudaStream_t 
     float4 *stats = reinterpret_cast<float4 *>(p.ws);
     const int64_t most = max_parts(p.rows, p.d), run = (p.rows + most - 1) / most;
     const int parts = (int)((p.rows + run - 1) / run);
-    float *part_w = reinterpret_cast<float *>(p.ws + align256((size_t)p.rows * 16));
+    float *rest = reinterpret_cast<float *>(stats + p.rows);
+    float *part_w = reinterpret_cast<float *>(p.ws + stats_bytes(p.rows));
     float *part_b = part_w + (size_t)parts * p.d;
     cudaError_t e = launch_overlapped(&k_norm_stats<DT, CENTER>,
                                       dim3((unsigned)(p.rows < cap ? p.rows : cap)), dim3(256), 0,
-                                      s, p.rows, nv, p.eps, dy, x, p.weight, stats);
+                                      s, p.rows, nv, p.eps, dy, x, p.weight, stats, rest);
     if (e != cudaSuccess) return e;
-    e = launch_overlapped(&k_norm_grad<DT>, dim3((unsigned)((nv + 127) / 128), (unsigned)parts),
-                          dim3(128), 0, s, p.rows, nv, run, dy, x, p.weight,
-                          (const float4 *)stats, static_cast<uint4 *>(p.dx),
+    e = launch_overlapped(&k_norm_grad<DT, CENTER>,
+                          dim3((unsigned)((nv + 127) / 128), (unsigned)parts), dim3(128), 0, s,
+                          p.rows, nv, run, dy, x, p.weight, (const float4 *)stats,
+                          (const float *)rest, static_cast<uint4 *>(p.dx),
                           p.dweight ? part_w : nullptr, p.dbias ? part_b : nullptr);
     if (e != cudaSuccess) return e;
     return launch_sums(p, parts, part_w, part_b, s);
@@ -612,7 +636,7 @@ cudaError_t launch(const RowNormBackward &p, const DeviceInfo &di, cudaStream_t 
 
 size_t norm_backward_bytes(int64_t rows, int64_t d, int dtype) {
     if (one_block(rows, d * row_type_bytes(dtype) / 16)) return 0;
-    return align256((size_t)rows * 16) + (size_t)max_parts(rows, d) * (size_t)d * 8;
+    return stats_bytes(rows) + (size_t)max_parts(rows, d) * (size_t)d * 8;
 }
 
 cudaError_t launch_norm_backward(const RowNormBackward &p, const DeviceInfo &di, cudaStream_t s) {
