@@ -96,3 +96,42 @@ def embed_chain(n):
     """Additions a gradient passes through: 8 copies of 32 tokens, then an eighth of the pieces of
     its id (n / 32 at most, or n where pieces are single tokens), 8 partial sums, the scale."""
     return 8 * 32 + n / 8 + 16
+
+
+def embed_backward_bound(n, want, mag, dtype, added=False):
+    """How far a table's gradient, `want` in 64 bits, may be off where n tokens' gradients, of
+    magnitudes that sum to `mag`, are added up: 8 copies of the 32 tokens of a piece, then of the
+    n / 4 pieces that an id has at most (a piece has four tokens or more) an eighth, then 8 partial
+    sums and the scale; added to what was there in one more step; rounded to the type once."""
+    off = (8 * 32 + n / 32 + 16) * U32 * mag + (U32 * want.abs() if added else 0)
+    return off * 1.01 + (1 + 1e-3) * HALF[dtype] * want.abs() + TINY[dtype]
+
+
+def check_embed_backward(got, base, ids, dx, vocab, scale, dtype, seed=0):
+    """A table's gradient `got` (with `base`, added to that) against the 64-bit sums, element by
+    element, and against differences of the 64-bit lookup along directions in which the gradient's
+    terms do not cancel: all of it, and one row.  What a difference may be off by follows from the
+    bound of the elements alone, and not from `got`."""
+    got, dx = got.detach().cpu().double(), dx.detach().cpu().double()
+    ids = ids.cpu().long()
+    want, mag = embed_backward(ids, dx, vocab, scale)
+    total = want if base is None else want + base.cpu().double()
+    bound = embed_backward_bound(ids.numel(), total, mag, dtype, base is not None)
+    assert torch.all((got - total).abs() <= bound), float(((got - total).abs() - bound).max())
+    if base is not None:
+        got = got - base.cpu().double()
+    ok = (ids >= 0) & (ids < vocab)
+    g = torch.Generator().manual_seed(seed)
+    table = torch.randn(want.shape, generator=g, dtype=torch.float64)
+
+    def loss(t):
+        return (scale * t[ids[ok]] * dx[ok].sum(1)).sum()
+
+    along = want.sign() * (0.5 + torch.rand(want.shape, generator=g, dtype=torch.float64))
+    one = torch.zeros_like(along)
+    row = int(mag.sum(1).argmax())
+    one[row] = along[row]
+    for u in (along, one):
+        diff = (loss(table + u) - loss(table - u)) / 2      # linear: any step will do
+        slack = 1e-12 * ((table.abs() + u.abs()) * mag).sum()
+        assert abs(float((got * u).sum() - diff)) <= float((bound * u.abs()).sum() + slack)
