@@ -442,8 +442,8 @@ hc_status hc_mixes_pre_backward(int64_t n, int hc, int64_t d, int iters, float e
  *   weight, bias [d] float (in, each may be NULL: ones, zeros)
  * A sublayer that is recomputed from a kept stream runs hc_pre_restore, then this.
  * A row whose sum of squares is above binary32's range has r = 0 (in layer norm NaN
- * where the sum of its numbers is, too); eps = 0 and a row whose squares are all 0
- * gives NaN, as the formula does.
+ * where a sum of some of its numbers, or of their distances from one another, is,
+ * too); eps = 0 and a row whose squares are all 0 gives NaN, as the formula does.
  */
 hc_status hc_norm(int64_t rows, int64_t d, int dtype, int center, float eps, const void *x,
                   const float *weight, const float *bias, void *y, hc_stream_t stream);

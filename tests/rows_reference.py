@@ -77,7 +77,7 @@ def norm_backward_bound(dy, x, w, center, eps, dtype):
     off = r * (off1 + h.abs() * off2 + c2.abs() * off_h +
                4 * U32 * (g.abs() + c1.abs() + (h * c2).abs())) + dx.abs() * rel_r
     off = off * 1.01 + (1 + 1e-3) * HALF[dtype] * dx.abs() + TINY[dtype]
-    # a block adds up its rows one by one, 304 blocks' sums are added up in turn
+    # a block adds up its rows one by one, and up to 608 blocks' sums are added up by 32 threads
     kw = min(n, n / 64 + 400) + 16
     off_w = kw * U32 * (dy * h).abs().sum(0) + (dy.abs() * off_h).sum(0)
     return off, off_w * 1.01 + 1e-44, kw * U32 * dy.abs().sum(0) + 1e-44
@@ -94,7 +94,8 @@ def embed_backward(ids, dx, vocab, scale):
 
 def embed_chain(n):
     """Additions a gradient passes through: 8 copies of 32 tokens, then an eighth of the pieces of
-    its id (n / 32 at most, or n where pieces are single tokens), 8 partial sums, the scale."""
+    its id, 8 partial sums, the scale.  n / 8 allows for pieces of single tokens; the library's have
+    four or more (embed_backward_bound)."""
     return 8 * 32 + n / 8 + 16
 
 

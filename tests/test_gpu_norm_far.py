@@ -1,8 +1,8 @@
 """Layer norm and its gradients of rows whose mean is thousands of deviations away, in fp32 (GPU).
 
 The bounds hold no term of half a step of the mean times 1 / sqrt(variance): they follow the row's
-numbers about a number p that is subtracted from them exactly (both lie within a factor of two of one
-another), and what the mean differs from p by is taken off as a number of its own."""
+numbers about a number p that is subtracted from them exactly (both lie within a factor of two of
+one another), and what the mean differs from p by is taken off as a number of its own."""
 import pytest
 import torch
 
@@ -30,9 +30,9 @@ def case(d, rows=7):
 
 
 def errors(x):
-    """h, r, and how far binary32's h and (relatively) r may be off.  p is off the mean by a deviation
-    at most, or by what a sum of the row is rounded by; a sum's terms pass through ref.chain(d)
-    additions at most."""
+    """h, r, and how far binary32's h and (relatively) r may be off.  p is off the mean by a
+    deviation at most, or by what a sum of the row is rounded by; a sum's terms pass through
+    ref.chain(d) additions at most."""
     k, u = ref.chain(x.shape[1]), ref.U32
     c = x - x.mean(1, keepdim=True)
     v = c.square().mean(1, keepdim=True)
