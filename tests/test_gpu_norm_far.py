@@ -22,10 +22,15 @@ def hc():
     assert lib.hc_device_error(clear=True) == 0
 
 
-def case(d, rows=7):
+# few rows and more than there are SMs: wide rows go to blocks of another size
+ROWS = [7, 160]
+
+
+def case(rows, d):
     g = torch.Generator().manual_seed(d)
     r = lambda *s: torch.randn(s, generator=g)  # noqa: E731
-    mean = torch.tensor([1000.0, -1000.0, 3.0, 777.7, -0.01, 65.3, 1001.0])[:rows, None]
+    mean = torch.tensor([1000.0, -1000.0, 3.0, 777.7, -0.01, 65.3, 1001.0])
+    mean = mean.repeat(rows // 7 + 1)[:rows, None]
     return mean + 0.05 * r(rows, d), r(rows, d) * 2.0 ** -6, 1 + 0.5 * r(d), r(d)
 
 
@@ -51,9 +56,10 @@ def within(got, want, bound):
     assert worst <= 1.0, worst
 
 
+@pytest.mark.parametrize("rows", ROWS)
 @pytest.mark.parametrize("d", WIDTHS)
-def test_norm(hc, d):
-    x, _, w, b = case(d)
+def test_norm(hc, d, rows):
+    x, _, w, b = case(rows, d)
     y = hc.hc_norm(x.cuda(), w.cuda(), b.cuda(), eps=EPS, center=True)
     x, w, b = x.double(), w.double(), b.double()
     h, _, off_h, _ = errors(x)
@@ -61,9 +67,10 @@ def test_norm(hc, d):
     within(y, want, 1.01 * (off_h * w.abs() + 3 * ref.U32 * ((h * w).abs() + want.abs())))
 
 
+@pytest.mark.parametrize("rows", ROWS)
 @pytest.mark.parametrize("d", WIDTHS)
-def test_norm_backward(hc, d):
-    x, dy, w, _ = case(d)
+def test_norm_backward(hc, d, rows):
+    x, dy, w, _ = case(rows, d)
     got = hc.hc_norm_backward(dy.cuda(), x.cuda(), w.cuda(), eps=EPS, center=True, want_dbias=True)
     x, dy, w = x.double(), dy.double(), w.double()
     h, r, off_h, rel_r = errors(x)
@@ -78,6 +85,6 @@ def test_norm_backward(hc, d):
     off = r * (off1 + h.abs() * off2 + c2.abs() * off_h +
                5 * u * (g.abs() + c1.abs() + (h * c2).abs())) + dx.abs() * rel_r
     within(got[0], dx, 1.01 * off + 2 * u * dx.abs())
-    rows = x.shape[0] + 16
-    within(got[1], dw, 1.01 * (rows * u * (dy * h).abs().sum(0) + (dy.abs() * off_h).sum(0)))
-    within(got[2], db, rows * u * dy.abs().sum(0))
+    adds = rows + 16
+    within(got[1], dw, 1.01 * (adds * u * (dy * h).abs().sum(0) + (dy.abs() * off_h).sum(0)))
+    within(got[2], db, adds * u * dy.abs().sum(0))
