@@ -125,8 +125,8 @@ __global__ void __launch_bounds__(BLOCK ? kRingThreads : 256, BLOCK ? 1 : V < 3 
 // A sum of numbers around a far mean is rounded to K u |mean|, which may be worth more
 // than the row's deviation, and so is the mean that comes of it: with the squares about it
 // goes a second sum, of what its numbers differ from it by (exact differences, as both are
-// of one size), and takes the rest off (fp32, mean 1000, deviation 0.05: y is off by 1e-6 in
-// place of 2e-3).  With that sum five blocks fit an SM, 157 us, six as it is bounded.  One
+// of one size), and takes the rest off (fp32, mean 1000, deviation 0.05: y is off by 2e-6 at
+// most in place of 2e-3).  With that sum five blocks fit an SM, 157 us, six as it is bounded.  One
 // round of sums about a guess, as k_norm has them, lost in spite of one reading less (160
 // us): no row is copied ahead here, and all of its loads wait for the guess.
 template <int DT, bool CENTER, int THREADS>
@@ -228,10 +228,11 @@ cudaError_t launch(const RowNorm &p, const DeviceInfo &di, cudaStream_t s) {
             default: return launch_ring<DT, CENTER, 5>(p, nv, di, s);
         }
     }
-    // few rows: many threads for each (100 x 20480: 5.8 us in place of 7.1, layer norm 7.5 and
-    // 8.5; of more rows than this 256 are as fast, 305 x 20480 layer norm 12.4)
-    return p.rows <= 2 * di.sms ? launch_wide<DT, CENTER, 1024>(p, nv, di, s)
-                                : launch_wide<DT, CENTER, 256>(p, nv, di, s);
+    // No more rows than SMs: many threads for each.  100 x 20480 5.8 us in place of 7.1, layer norm
+    // 7.5 and 8.5, 152 6.1 and 7.4; 153 rows, of which an SM has two in turn, 9.8 and 7.5, layer
+    // norm 13.0 and 9.5, 304 11.2 and 8.6
+    return p.rows <= di.sms ? launch_wide<DT, CENTER, 1024>(p, nv, di, s)
+                            : launch_wide<DT, CENTER, 256>(p, nv, di, s);
 }
 
 template <int DT>
